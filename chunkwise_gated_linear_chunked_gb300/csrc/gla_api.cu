@@ -4,33 +4,12 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
+#include "api_common.h"
 #include "gla_internal.h"
 
 namespace gla {
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-int sm_count()
-{
-    static std::mutex mu;
-    static int cache[128] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128)
-        return 148;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!cache[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
 
 bool supported_k(int K) { return K == 64 || K == 128; }
 // Accepted chunk lengths.  The kernels always tile at kChunk rows: the result of the method does not depend
@@ -172,53 +151,6 @@ void make_plan(Plan &pl, int B, int T, int H, int K, int V, int N, int chunk, in
         off += align_up(sizeof(int) * (size_t)pl.J * H * pl.NV);
     pl.total = off;
 }
-
-// Per-thread measurement hook state (gla_profile_events).
-struct Profile {
-    cudaEvent_t *events = nullptr;
-    int n_events = 0;
-    int *ids = nullptr;
-    int launches = 0;
-};
-thread_local Profile g_prof;
-
-enum KernelId {
-    K_PLAN = 1, K_STATE_FFMA = 2, K_SCAN = 3, K_OUT_FFMA = 4, K_FUSED_TC = 7,
-    K_BWD_SUMS = 8, K_BWD_SCAN = 9, K_BWD_GRADS = 10, K_BWD_DG = 11, K_TTT = 12, K_WY = 13,
-    K_WY_TC = 14, K_BWD_SUMS_TC = 15, K_BWD_GRADS_TC = 16, K_TTT_TC = 17
-};
-
-// Launch one kernel through `fn`, bracketed by the profiling events when they are armed.
-template <typename Fn>
-cudaError_t profiled(int id, cudaStream_t s, Fn fn)
-{
-    Profile &p = g_prof;
-    const int i = p.launches++;
-    const bool rec = p.events && 2 * i + 1 < p.n_events;
-    if (rec && cudaEventRecord(p.events[2 * i], s) != cudaSuccess)
-        return cudaErrorUnknown;
-    cudaError_t e = fn();
-    if (e != cudaSuccess)
-        return e;
-    if (rec) {
-        if (p.ids)
-            p.ids[i] = id;
-        return cudaEventRecord(p.events[2 * i + 1], s);
-    }
-    return cudaSuccess;
-}
-
-bool misaligned(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-Range range_of(const void *p, size_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
 
 }  // namespace
 }  // namespace gla
@@ -438,6 +370,14 @@ extern "C" const char *gla_kernel_name(int kernel_id)
     case K_BWD_SUMS_TC: return "bwd_chunk_sums_tc";
     case K_BWD_GRADS_TC: return "bwd_grads_tc";
     case K_TTT_TC: return "ttt_linear_tc";
+    case K_SCAN_FWD: return "scan_fwd";
+    case K_SCAN_BWD: return "scan_bwd";
+    case K_SCAN_STEP: return "scan_step";
+    case K_GLA_STEP: return "gla_step";
+    case K_NORM_FWD: return "norm_fwd";
+    case K_NORM_QUANT: return "norm_quant_fwd";
+    case K_NORM_BWD: return "norm_bwd";
+    case K_NORM_DW: return "norm_dw";
     default: return "unknown";
     }
 }
