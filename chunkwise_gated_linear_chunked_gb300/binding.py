@@ -7,6 +7,8 @@ no CPU fallback: if ``_build/libgla.so`` is missing the import fails loudly (run
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 import threading
 
@@ -16,13 +18,16 @@ from .build import LIB
 
 GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_ALIGNMENT, GLA_ERR_WORKSPACE, GLA_ERR_CUDA, \
     GLA_ERR_TIMEOUT, GLA_ERR_RANGE = range(8)
-GLA_F32, GLA_BF16, GLA_BF16_OBF16, GLA_F16, GLA_BF16_GF32, GLA_F16_GF32 = 0, 1, 2, 3, 4, 5
+GLA_F32, GLA_BF16, GLA_BF16_OBF16, GLA_F16, GLA_BF16_GF32, GLA_F16_GF32, GLA_F16_OF16 = 0, 1, 2, 3, 4, 5, 6
 GLA_HEAD_FIRST = 0x100   # OR-ed into the dtype code: [B, H, T, *] tensors
+GLA_RES_F32 = 0x200      # OR-ed into the dtype code of the norms: fp32 residual stream
 
 EXPORTS = ("gla_fwd", "gla_fwd_workspace_size", "gla_get_status", "gla_strerror", "gla_chunk_local_cumsum",
            "gla_profile_events", "gla_profile_launches", "gla_kernel_name", "gla_fwd_noalloc", "gla_bwd",
            "gla_bwd_workspace_size", "gla_ttt_linear_fwd", "gla_ttt_workspace_size", "gla_wy_fwd",
-           "gla_wy_workspace_size", "gla_fwd_host", "gla_fwd_host_workspace_size")
+           "gla_wy_workspace_size", "gla_fwd_host", "gla_fwd_host_workspace_size", "gla_scan_fwd", "gla_scan_bwd",
+           "gla_scan_step", "gla_scan_workspace_size", "gla_step", "gla_norm_fwd", "gla_norm_quant_fwd",
+           "gla_norm_bwd", "gla_norm_bwd_workspace_size")
 
 if not os.path.exists(LIB):
     raise ImportError(f"libgla.so not built ({LIB}); call chunkwise_gated_linear_chunked_gb300.build.build()")
@@ -63,6 +68,25 @@ _lib.gla_wy_workspace_size.argtypes = [_i, _i, _i, _i]
 _lib.gla_wy_workspace_size.restype = _sz
 _lib.gla_ttt_workspace_size.argtypes = []
 _lib.gla_ttt_workspace_size.restype = _sz
+_i64 = ctypes.c_int64
+_lib.gla_scan_fwd.argtypes = [_p] * 6 + [_i] * 4 + [_i64] * 2 + [_i, _p, _sz, _p]
+_lib.gla_scan_fwd.restype = _i
+_lib.gla_scan_bwd.argtypes = [_p] * 9 + [_i] * 4 + [_i64] * 3 + [_i, _p, _sz, _p]
+_lib.gla_scan_bwd.restype = _i
+_lib.gla_scan_step.argtypes = [_p] * 6 + [_i] * 3 + [_i64] * 2 + [_i, _p, _sz, _p]
+_lib.gla_scan_step.restype = _i
+_lib.gla_scan_workspace_size.argtypes = []
+_lib.gla_scan_workspace_size.restype = _sz
+_lib.gla_step.argtypes = [_p] * 5 + [_f] + [_p] * 3 + [_i] * 6 + [_p, _sz, _p]
+_lib.gla_step.restype = _i
+_lib.gla_norm_fwd.argtypes = [_p] * 6 + [_i64, _i, _f, _i, _p]
+_lib.gla_norm_fwd.restype = _i
+_lib.gla_norm_quant_fwd.argtypes = [_p] * 7 + [_i64, _i, _f, _i, _i, _p]
+_lib.gla_norm_quant_fwd.restype = _i
+_lib.gla_norm_bwd.argtypes = [_p] * 8 + [_i64, _i, _i, _p, _sz, _p]
+_lib.gla_norm_bwd.restype = _i
+_lib.gla_norm_bwd_workspace_size.argtypes = [_i64, _i]
+_lib.gla_norm_bwd_workspace_size.restype = _sz
 
 
 class GlaError(RuntimeError):
@@ -326,6 +350,338 @@ def wy_fwd(k, v, beta, A, g=None, cu_seqlens=None, out_dtype=None, stream=None, 
     if rc != GLA_OK:
         raise GlaError(rc, "gla_wy_fwd")
     return w, u
+
+
+# ---------------------------------------------------------------------------------------------------------
+# Operators beside the chunkwise kernels: vector-state recurrence, one-token updates, residual norm
+# ---------------------------------------------------------------------------------------------------------
+
+# (x, gate, output) types of the recurrence -> dtype code
+SCAN_CODE = {(torch.float32, torch.float32, torch.float32): GLA_F32,
+             (torch.bfloat16, torch.bfloat16, torch.float32): GLA_BF16,
+             (torch.bfloat16, torch.bfloat16, torch.bfloat16): GLA_BF16_OBF16,
+             (torch.float16, torch.float16, torch.float32): GLA_F16,
+             (torch.float16, torch.float16, torch.float16): GLA_F16_OF16,
+             (torch.bfloat16, torch.float32, torch.float32): GLA_BF16_GF32,
+             (torch.float16, torch.float32, torch.float32): GLA_F16_GF32}
+_NORM_CODE = {torch.float32: GLA_F32, torch.bfloat16: GLA_BF16, torch.float16: GLA_F16}
+_STATUS_BYTES = int(_lib.gla_scan_workspace_size())
+_stream_ws: dict = {}
+
+
+def stream_workspace(nbytes: int, device) -> torch.Tensor:
+    """A zeroed device workspace of at least ``nbytes``, cached per device and current stream, so that calls on
+    different streams never share one.  During a CUDA graph capture it is a fresh tensor instead: the graph zeroes
+    it on every replay and owns its memory."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+    key = (device.index, stream)
+    ws = _stream_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _stream_ws[key] = ws
+    return ws
+
+
+def _on_stream(fn):
+    """Runs a call on its ``stream`` argument (or the current stream) of its first tensor's device: the outputs and
+    the workspace are then allocated on the stream that the kernels run on.  The inputs are the caller's to order."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise GlaError(GLA_ERR_INVALID_ARG, f"{fn.__name__}: the first argument must be a cuda tensor")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _check(what, name, t, dtype, shape, device):
+    """``t`` is a contiguous tensor of this dtype, shape and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must be a contiguous {dtype} tensor of shape "
+                                            f"{tuple(shape)} on {device}")
+
+
+def _row_stride(what, name, t, shape, device):
+    """Elements between consecutive rows of a [..., D] tensor: the channels adjacent, the rows evenly spaced (a
+    contiguous tensor, or a column range of one)."""
+    if t.shape != shape or t.device != device:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must have shape {tuple(shape)} on {device}")
+    if t.is_contiguous():
+        return shape[-1]
+    D, ld = shape[-1], t.stride(-2)
+    even = all(t.stride(i) == ld * math.prod(shape[i + 1:-1]) or shape[i] == 1 for i in range(len(shape) - 2))
+    if shape[-2] == 1:   # a single row per sequence: the spacing is the outer dimension's
+        ld = next((t.stride(i) for i in range(len(shape) - 3, -1, -1) if shape[i] > 1), D)
+        even = all(t.stride(i) == ld * math.prod(shape[i + 1:-1]) or shape[i] == 1 for i in range(len(shape) - 2))
+    if (D > 1 and t.stride(-1) != 1) or ld < D or not even:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must have adjacent channels and evenly spaced rows "
+                                            f"(a contiguous tensor or a column range of one)")
+    return ld
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pack(what, shape, cu_seqlens, device):
+    """(N, B, T, D) of a [B, T, D] recurrence, dense or packed."""
+    if len(shape) != 3:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: expected [B, T, D] tensors, got shape {tuple(shape)}")
+    B, T, D = shape
+    if cu_seqlens is None:
+        return B, B, T, D
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
+            cu_seqlens.device != device or not cu_seqlens.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: cu_seqlens must be a contiguous int32 vector on {device}")
+    return cu_seqlens.numel() - 1, B, T, D
+
+
+@_on_stream
+def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None, out_dtype=None, out=None,
+             workspace=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t on the GPU.
+
+    x, g: [B, T, D], cuda, channels adjacent and rows evenly spaced (contiguous, or column ranges of one projection's
+    output); both fp32, bf16 or fp16, or a 16-bit x with an fp32 g.  initial_state: fp32 [N, D] or None.
+    cu_seqlens: int32 [N+1] cuda offsets (B == 1).  out_dtype: x's type (default; fp32 beside an fp32 g) or fp32.
+    out: optional [B, T, D] tensor for h.  stream=: the stream to run on.  Returns (h, ht fp32 [N, D] or None).
+    """
+    shape, device = x.shape, x.device
+    N, B, T, D = _pack("gla_scan_fwd", shape, cu_seqlens, device)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else g.dtype
+    code = SCAN_CODE.get((x.dtype, g.dtype, out_dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"gla_scan_fwd dtypes x {x.dtype}, g {g.dtype} -> {out_dtype}")
+    ldx = _row_stride("gla_scan_fwd", "x", x, shape, device)
+    ldg = _row_stride("gla_scan_fwd", "g", g, shape, device)
+    if initial_state is not None:
+        _check("gla_scan_fwd", "initial_state", initial_state, torch.float32, (N, D), device)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        _check("gla_scan_fwd", "out", out, out_dtype, shape, device)
+    ht = torch.empty(N, D, dtype=torch.float32, device=device) if output_final_state else None
+    if workspace is None:
+        workspace = stream_workspace(_STATUS_BYTES, device)
+    rc = _lib.gla_scan_fwd(x.data_ptr(), g.data_ptr(), out.data_ptr(), _at(initial_state), _at(ht), _at(cu_seqlens),
+                           N, B, T, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
+                           torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_scan_fwd")
+    return out, ht
+
+
+@_on_stream
+def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=None, want_dh0=True, dx=None, dg=None,
+             workspace=None):
+    """Gradients of ``scan_fwd`` for L = sum(h * dh) + sum(ht * dht), from its gate g and its output h.
+
+    g as for scan_fwd; h, dh: [B, T, D] contiguous, of the forward's out_dtype; initial_state, dht: fp32 [N, D] or
+    None.  dx_dtype: x's type (default: g's).  dx, dg: optional tensors to write, which may be column ranges of one
+    gradient.  Returns (dx, dg in g's type, dh0 fp32 [N, D] or None).
+    """
+    shape, device = g.shape, g.device
+    N, B, T, D = _pack("gla_scan_bwd", shape, cu_seqlens, device)
+    if dx_dtype is None:
+        dx_dtype = g.dtype if dx is None else dx.dtype
+    code = SCAN_CODE.get((dx_dtype, g.dtype, h.dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"gla_scan_bwd dtypes dx {dx_dtype}, g {g.dtype}, h {h.dtype}")
+    ldg = _row_stride("gla_scan_bwd", "g", g, shape, device)
+    _check("gla_scan_bwd", "h", h, h.dtype, shape, device)
+    _check("gla_scan_bwd", "dh", dh, h.dtype, shape, device)
+    for name, t in (("initial_state", initial_state), ("dht", dht)):
+        if t is not None:
+            _check("gla_scan_bwd", name, t, torch.float32, (N, D), device)
+    lddx = lddg = D
+    if dx is None:
+        dx = torch.empty(shape, dtype=dx_dtype, device=device)
+    elif dx.dtype != dx_dtype:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"gla_scan_bwd: dx must be a {dx_dtype} tensor")
+    else:
+        lddx = _row_stride("gla_scan_bwd", "dx", dx, shape, device)
+    if dg is None:
+        dg = torch.empty(shape, dtype=g.dtype, device=device)
+    elif dg.dtype != g.dtype:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"gla_scan_bwd: dg must be a {g.dtype} tensor")
+    else:
+        lddg = _row_stride("gla_scan_bwd", "dg", dg, shape, device)
+    dh0 = torch.empty(N, D, dtype=torch.float32, device=device) if want_dh0 else None
+    if workspace is None:
+        workspace = stream_workspace(_STATUS_BYTES, device)
+    rc = _lib.gla_scan_bwd(g.data_ptr(), h.data_ptr(), dh.data_ptr(), _at(initial_state), _at(dht), dx.data_ptr(),
+                           dg.data_ptr(), _at(dh0), _at(cu_seqlens), N, B, T, D, ldg, lddx, lddg, code,
+                           workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_scan_bwd")
+    return dx, dg, dh0
+
+
+def _pool(what, state, state_out, slots, B, tail, device):
+    """(pool rows, the pool to write) of a one-token update."""
+    if state.dim() != 1 + len(tail) or (slots is None and state.shape[0] != B):
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: state must be [{'S' if slots is not None else B}, "
+                                            f"{', '.join(map(str, tail))}]")
+    S = state.shape[0]
+    _check(what, "state", state, torch.float32, (S, *tail), device)
+    if state_out is None:
+        state_out = state
+    else:
+        _check(what, "state_out", state_out, torch.float32, (S, *tail), device)
+    if slots is not None:
+        _check(what, "slots", slots, torch.int32, (B,), device)
+    return S, state_out
+
+
+@_on_stream
+def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace=None):
+    """One token of ``scan_fwd``'s recurrence for each of B sequences.
+
+    x, g: [B, D] (types and strides as for scan_fwd); state: fp32 [S, D] pool, updated in place (or written to
+    state_out, of which only the addressed rows are written); slots: int32 [B] cuda, the pool row of each sequence
+    (-1: idle, its h is zeros), or None when S == B.  Returns h [B, D].
+    """
+    if x.dim() != 2:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"gla_scan_step: x must be [B, D], got shape {tuple(x.shape)}")
+    shape, device = x.shape, x.device
+    B, D = shape
+    if out_dtype is None:
+        out_dtype = g.dtype
+    code = SCAN_CODE.get((x.dtype, g.dtype, out_dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"gla_scan_step dtypes x {x.dtype}, g {g.dtype} -> {out_dtype}")
+    ldx = _row_stride("gla_scan_step", "x", x, shape, device)
+    ldg = _row_stride("gla_scan_step", "g", g, shape, device)
+    S, state_out = _pool("gla_scan_step", state, state_out, slots, B, (D,), device)
+    h = torch.empty(shape, dtype=out_dtype, device=device)
+    if workspace is None:
+        workspace = stream_workspace(_STATUS_BYTES, device)
+    rc = _lib.gla_scan_step(x.data_ptr(), g.data_ptr(), h.data_ptr(), state.data_ptr(), state_out.data_ptr(),
+                            _at(slots), B, S, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
+                            torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_scan_step")
+    return h
+
+
+@_on_stream
+def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtype=None, workspace=None):
+    """One token of ``gla_fwd``'s recurrence for each of B sequences: S = diag(exp g) S + k^T v, o = scale q S.
+
+    q, k, g: [B, H, K]; v: [B, H, V] (contiguous; types as for gla_fwd); state: fp32 [S, H, K, V] pool, updated in
+    place (or written to state_out); slots as for scan_step.  out_dtype: fp32 (default) or q's type.
+    Returns o [B, H, V].
+    """
+    if q.dim() != 3 or v.dim() != 3:
+        raise GlaError(GLA_ERR_INVALID_ARG, "gla_step: q, k, g must be [B, H, K] and v [B, H, V]")
+    device = q.device
+    B, H, K = q.shape
+    V = v.shape[-1]
+    out_dtype = out_dtype or torch.float32
+    code = SCAN_CODE.get((q.dtype, g.dtype, out_dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"gla_step dtypes q {q.dtype}, g {g.dtype} -> {out_dtype}")
+    _check("gla_step", "q", q, q.dtype, (B, H, K), device)
+    _check("gla_step", "k", k, q.dtype, (B, H, K), device)
+    _check("gla_step", "v", v, q.dtype, (B, H, V), device)
+    _check("gla_step", "g", g, g.dtype, (B, H, K), device)
+    S, state_out = _pool("gla_step", state, state_out, slots, B, (H, K, V), device)
+    o = torch.empty(B, H, V, dtype=out_dtype, device=device)
+    if workspace is None:
+        workspace = stream_workspace(_STATUS_BYTES, device)
+    rc = _lib.gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), o.data_ptr(),
+                       K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B, S,
+                       H, K, V, code, workspace.data_ptr(), workspace.numel(),
+                       torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_step")
+    return o
+
+
+def _norm_args(what, x, residual, weight, stream_dtype):
+    """(rows, D, dtype code) of a norm of x whose residual stream has this type."""
+    code = _NORM_CODE.get(x.dtype)
+    if code is None or stream_dtype not in (x.dtype, torch.float32):
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what} dtypes x {x.dtype}, residual {stream_dtype}")
+    if x.dim() < 1 or not x.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: x must be a contiguous [..., D] tensor")
+    D = x.shape[-1]
+    if D == 0:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: no columns")
+    if residual is not None:
+        _check(what, "residual", residual, stream_dtype, x.shape, x.device)
+    if weight is not None:
+        _check(what, "weight", weight, torch.float32, (D,), x.device)
+    return x.numel() // D, D, code if stream_dtype == x.dtype else code | GLA_RES_F32
+
+
+@_on_stream
+def norm_fwd(x, residual=None, weight=None, eps=1e-6):
+    """Residual addition and root-mean-square norm over the last dimension: s = x + residual, y = s rstd weight.
+
+    x: contiguous [..., D] fp32 / bf16 / fp16; residual: like x, or fp32; weight: fp32 [D] or None.
+    Returns (y in x's type, s in the residual's type (x itself without a residual), rstd fp32 [...]).
+    """
+    stream_dtype = x.dtype if residual is None else residual.dtype
+    rows, D, code = _norm_args("gla_norm_fwd", x, residual, weight, stream_dtype)
+    y = torch.empty_like(x)
+    s = None if residual is None else torch.empty_like(residual)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rc = _lib.gla_norm_fwd(x.data_ptr(), _at(residual), _at(weight), y.data_ptr(), _at(s), rstd.data_ptr(), rows, D,
+                           eps, code, torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_norm_fwd")
+    return y, x if s is None else s, rstd
+
+
+@_on_stream
+def norm_quant_fwd(x, residual=None, weight=None, eps=1e-6, group=0):
+    """``norm_fwd`` with its output in 8 bits: y is q times its scale.  group: columns of one scale, 128, or 0 for
+    one scale per row.  Returns (q float8_e4m3fn [..., D], scales fp32 [..., ceil(D / group)], s, rstd)."""
+    stream_dtype = x.dtype if residual is None else residual.dtype
+    rows, D, code = _norm_args("gla_norm_quant_fwd", x, residual, weight, stream_dtype)
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    groups = -(-D // group) if group > 0 else 1
+    scales = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=x.device)
+    s = None if residual is None else torch.empty_like(residual)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rc = _lib.gla_norm_quant_fwd(x.data_ptr(), _at(residual), _at(weight), q.data_ptr(), scales.data_ptr(), _at(s),
+                                 rstd.data_ptr(), rows, D, eps, group, code, torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_norm_quant_fwd")
+    return q, scales, x if s is None else s, rstd
+
+
+@_on_stream
+def norm_bwd(s, rstd, dy, weight=None, ds=None, want_dw=True, workspace=None):
+    """Gradients of ``norm_fwd`` from its s and rstd, for the gradients dy of y and ds of s (or None).
+
+    Returns (the gradient of x in dy's type, the gradient of the residual in s's type, dw fp32 [D] or None).  The
+    first two are one tensor when the types are the same.  ``want_dw=False`` skips dw (also None without a weight).
+    """
+    rows, D, code = _norm_args("gla_norm_bwd", dy, s, weight, s.dtype)
+    if ds is not None:
+        _check("gla_norm_bwd", "ds", ds, s.dtype, s.shape, s.device)
+    _check("gla_norm_bwd", "rstd", rstd, torch.float32, s.shape[:-1], s.device)
+    dx = torch.empty_like(dy)
+    dres = dx if s.dtype == dy.dtype else torch.empty_like(s)
+    dw = torch.empty(D, dtype=torch.float32, device=s.device) if want_dw and weight is not None else None
+    if workspace is None:
+        workspace = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(rows, D)), s.device)
+    rc = _lib.gla_norm_bwd(s.data_ptr(), rstd.data_ptr(), _at(weight), dy.data_ptr(), _at(ds), dx.data_ptr(),
+                           None if dres is dx else dres.data_ptr(), _at(dw), rows, D, code, workspace.data_ptr(),
+                           workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    if rc != GLA_OK:
+        raise GlaError(rc, "gla_norm_bwd")
+    return dx, dres, dw
 
 
 def get_status(workspace, stream=None) -> int:

@@ -1,0 +1,93 @@
+// Internal declarations of the operators beside the chunkwise kernels: the vector-state gated linear recurrence
+// (scan.cu), the one-token state updates (step.cu) and the residual norm (norm.cu); entry points in layer_api.cu.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "gla.h"
+
+namespace gla {
+
+// Recurrence forward and backward (passed by value).  Row r of a strided tensor starts at r * ld elements.
+struct ScanArgs {
+    const void *x, *g, *h_in, *dh;     // forward: x, g; backward: g, h_in (the forward's output), dh
+    const float *h0, *dht;
+    void *h, *dx, *dg;
+    float *ht, *dh0;
+    const int32_t *cu;                 // device offsets or nullptr
+    int N, T, D;                       // sequences, rows of one sequence (dense) or of the pack, channels
+    int64_t ldx, ldg, lddx, lddg;
+    int *status;
+};
+
+// One-token updates (passed by value).
+struct StepArgs {
+    const void *x, *g;                 // scan: x, g;  GLA: q in x
+    const void *k, *v;
+    void *h;
+    const float *h0;
+    float *ht;
+    const int32_t *slots;              // or nullptr: sequence b uses state b
+    float scale;
+    int B, S, D, H, K, V;
+    int64_t ldx, ldg;
+    int *status;
+};
+
+// Norm forward and backward (passed by value).
+struct NormArgs {
+    const void *x, *res, *s_in, *dy, *ds;
+    const float *w, *rstd_in;
+    void *y, *s, *dx, *dres;           // y: x's type, or e4m3 with scales
+    float *rstd, *scales, *dw, *part;  // part: partial sums of dw, one row per CTA
+    int64_t rows;
+    int D, group, ctas;
+    float eps;
+};
+
+cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_step(const StepArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_gla_step(const StepArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s);
+cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s);
+int norm_bwd_ctas(int64_t rows, int D);   // CTAs (and partial sums of dw) of the norm's backward
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+
+// Calls f with null pointers of the (x, gate, output) types of a recurrence dtype code.
+template <typename F>
+cudaError_t by_types(int dtype, F f)
+{
+    typedef __nv_bfloat16 bf;
+    switch (dtype) {
+    case GLA_F32: return f((float *)0, (float *)0, (float *)0);
+    case GLA_BF16: return f((bf *)0, (bf *)0, (float *)0);
+    case GLA_BF16_OBF16: return f((bf *)0, (bf *)0, (bf *)0);
+    case GLA_F16: return f((__half *)0, (__half *)0, (float *)0);
+    case GLA_F16_OF16: return f((__half *)0, (__half *)0, (__half *)0);
+    case GLA_BF16_GF32: return f((bf *)0, (float *)0, (float *)0);
+    case GLA_F16_GF32: return f((__half *)0, (float *)0, (float *)0);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace gla

@@ -60,7 +60,8 @@ typedef enum gla_dtype {
     GLA_BF16_OBF16 = 2, /* q, k, v, g bf16; o bf16 (the pages' o.to(v) convention)                  */
     GLA_F16 = 3,        /* q, k, v, g fp16; o fp32 (same paths and bounds as GLA_BF16)                */
     GLA_BF16_GF32 = 4,  /* q, k, v bf16, g fp32; o fp32 (forward: the tensor-core path for K == 128)  */
-    GLA_F16_GF32 = 5    /* q, k, v fp16, g fp32; o fp32 (as GLA_BF16_GF32)                             */
+    GLA_F16_GF32 = 5,   /* q, k, v fp16, g fp32; o fp32 (as GLA_BF16_GF32)                             */
+    GLA_F16_OF16 = 6    /* q, k, v, g fp16; o fp16 (gla_step and the gla_scan_* functions only)        */
 } gla_dtype;
 
 /* OR-ed into the dtype argument of gla_fwd / gla_bwd (and their workspace queries): q, k, v, g, o (and the
@@ -290,6 +291,141 @@ int gla_wy_fwd(const void *k, const void *v, const void *beta, const void *A, co
 
 /* Bytes of device workspace gla_wy_fwd needs (dense batches: N is ignored). */
 size_t gla_wy_workspace_size(int T, int N, int chunk, int varlen);
+
+/* ---------------------------------------------------------------------------------------------------------
+ * Operators beside the chunkwise kernels in a model: a gated linear recurrence with a vector state (forward,
+ * backward, one token), the GLA state update for one token, and the root-mean-square norm with the residual's
+ * addition.  They have no counterpart on the pages.  The conventions at the top of this file hold (16-byte
+ * aligned device pointers, caller-owned memory, stream order, synchronous argument checks), except that row
+ * counts and sizes may exceed 2^31 elements.  Sums, states and norms are held in fp32 whatever the input types.
+ * ------------------------------------------------------------------------------------------------------ */
+
+/*
+ * gla_scan_fwd — gated linear recurrence with a vector state.  Per sequence n and channel d,
+ *
+ *     h_t = exp(g_t) h_{t-1} + x_t,   h_0 = h0[n] (or 0),   ht[n] = h_last
+ *
+ *   x, g        [rows, D] device; rows = B * T (dense) or the packed length T (cu_seqlens, B == 1).  Row r starts
+ *               at r * ldx (ldg) elements, so x and g may be column ranges of one projection's output
+ *   h           [rows, D] device, contiguous, written
+ *   h0, ht      [N, D] fp32 device or NULL; ht may equal h0.  A sequence of length zero has ht = h0 (or 0)
+ *   D >= 1, ldx >= D, ldg >= D (odd sizes and strides are fine; rows of 16-byte multiples are fastest)
+ *   dtype       types of (x, g, h): GLA_F32 (f32, f32, f32), GLA_BF16 (bf16, bf16, f32), GLA_BF16_OBF16 (bf16, bf16,
+ *               bf16), GLA_F16 (f16, f16, f32), GLA_F16_OF16 (f16, f16, f16), GLA_BF16_GF32 (bf16, f32, f32),
+ *               GLA_F16_GF32 (f16, f32, f32)
+ *   workspace   gla_scan_workspace_size() bytes, 256-byte aligned, zeroed before first use: the status word.  A
+ *               sequence with bad offsets (cu_seqlens must run from 0 to T without decreasing) is reported there
+ *               (gla_get_status) and skipped
+ *
+ * g is usually <= 0 but may be any value: the recurrence is evaluated as written, and infinities and NaN spread as
+ * they would step by step, except that a segment's total decay multiplies the state that enters it (a state of
+ * infinity that meets a total decay of 0 becomes NaN).  Results do not depend on timing (no atomics).
+ */
+int gla_scan_fwd(const void *x, const void *g, void *h, const float *h0, float *ht, const int32_t *cu_seqlens, int N,
+                 int B, int T, int D, int64_t ldx, int64_t ldg, int dtype, void *workspace, size_t workspace_bytes,
+                 void *stream);
+
+/*
+ * gla_scan_bwd — gradients of gla_scan_fwd for L = sum(h * dh) + sum(ht * dht), from the forward's gate and output:
+ *
+ *     lam_t = dh_t + mu_{t+1},   mu_t = exp(g_t) lam_t,   mu_{last+1} = dht (or 0)
+ *     dx_t = lam_t,   dg_t = mu_t h_{t-1},   dh0 = mu_1
+ *
+ *   g, h        as the forward read and wrote them (dg carries h's rounding);  dh [rows, D] contiguous, h's type
+ *   h0, dht     [N, D] fp32 or NULL (zeros);  dh0 [N, D] fp32 or NULL to skip it
+ *   dx, dg      written, the types of x and g; row r at r * lddx (lddg) elements, so both may be column ranges of
+ *               one gradient
+ * The rest as for gla_scan_fwd.  Outputs must not overlap any input or one another.
+ */
+int gla_scan_bwd(const void *g, const void *h, const void *dh, const float *h0, const float *dht, void *dx, void *dg,
+                 float *dh0, const int32_t *cu_seqlens, int N, int B, int T, int D, int64_t ldg, int64_t lddx,
+                 int64_t lddg, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gla_scan_fwd, gla_scan_bwd, gla_scan_step and gla_step need (the status word). */
+size_t gla_scan_workspace_size(void);
+
+/*
+ * gla_scan_step — one token of the recurrence above for each of B sequences, with the states in a pool:
+ *
+ *     s = slots ? slots[b] : b,   ht[s] = exp(g_b) h0[s] + x_b,   h_b = ht[s] rounded to h's type
+ *
+ *   x, g        [B, D], row strides ldx, ldg;   h [B, D] contiguous, written
+ *   h0, ht      [S, D] fp32 state pools; ht may equal h0 (update in place).  Only the addressed rows are written
+ *   slots       int32 [B] device or NULL (then S == B).  A slot of -1 marks an idle sequence: its h is zeros and no
+ *               state is read or written.  Any other slot outside [0, S) is treated the same and reported in the
+ *               status word as GLA_ERR_INVALID_ARG.  Two sequences must not share a slot
+ *   dtype, workspace as for gla_scan_fwd
+ */
+int gla_scan_step(const void *x, const void *g, void *h, const float *h0, float *ht, const int32_t *slots, int B,
+                  int S, int D, int64_t ldx, int64_t ldg, int dtype, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/*
+ * gla_step — one token of the GLA recurrence (gla_fwd) for each of B sequences, with the states in a pool:
+ *
+ *     s = slots ? slots[b] : b,   ht[s] = diag(exp g_b) h0[s] + k_b^T v_b,   o_b = scale * q_b ht[s]
+ *
+ *   q, k, g     [B, H, K],  v [B, H, V] device, contiguous;  o [B, H, V] device, written
+ *   h0, ht      [S, H, K, V] fp32 state pools; ht may equal h0 (update in place)
+ *   slots       as for gla_scan_step (an idle sequence's o is zeros)
+ *   K in {64, 128}, V in {64, 128, 256};  scale finite and > 0
+ *   dtype       types of (q, k, v; g; o), as the types of (x, g, h) of gla_scan_fwd
+ *   workspace   as for gla_scan_fwd
+ */
+int gla_step(const void *q, const void *k, const void *v, const void *g, void *o, float scale, const float *h0,
+             float *ht, const int32_t *slots, int B, int S, int H, int K, int V, int dtype, void *workspace,
+             size_t workspace_bytes, void *stream);
+
+/* OR-ed into the dtype argument of the gla_norm_* functions: the residual stream (res, s and its gradients) is fp32
+ * whatever the type of x and y. */
+#define GLA_RES_F32 0x200
+
+/*
+ * gla_norm_fwd — residual addition and root-mean-square norm of each row:
+ *
+ *     s = x + res,   rstd = 1 / sqrt(mean(s^2) + eps),   y = s * rstd * w
+ *
+ *   x, y        [rows, D] device, fp32 / bf16 / fp16 by dtype (GLA_F32, GLA_BF16, GLA_F16)
+ *   res, s      [rows, D] device, x's type (fp32 with GLA_RES_F32).  res may be NULL (s = x); s may be NULL to skip
+ *               it, and may equal res (update in place).  The norm takes s before its rounding to the stored type
+ *   w           [D] fp32 or NULL (ones);   rstd [rows] fp32 or NULL to skip it (the backward needs it)
+ *   1 <= D <= 16384,  eps finite and >= 0.  A row with a NaN has NaN everywhere; rows are independent
+ */
+int gla_norm_fwd(const void *x, const void *res, const float *w, void *y, void *s, float *rstd, int64_t rows, int D,
+                 float eps, int dtype, void *stream);
+
+/*
+ * gla_norm_quant_fwd — gla_norm_fwd with y in 8 bits (e4m3) and fp32 scales, for a product with 8-bit operands:
+ *
+ *     scale = max(max |y| / 448, 1e-30) over each group of columns,   q = e4m3(y / scale)  (to nearest, ties to even)
+ *
+ *   q           [rows, D] device, written.  y is not rounded in between; the quotient is formed as y times the fp32
+ *               reciprocal of the scale
+ *   scales      [rows, ceil(D / group)] fp32 device, written (the last group may be partial)
+ *   group       0 (one scale per row) or 128
+ * The rest as for gla_norm_fwd.  A NaN makes its row's values and scales NaN.
+ */
+int gla_norm_quant_fwd(const void *x, const void *res, const float *w, void *q, float *scales, void *s, float *rstd,
+                       int64_t rows, int D, float eps, int group, int dtype, void *stream);
+
+/*
+ * gla_norm_bwd — gradients of gla_norm_fwd for upstream gradients dy of y and ds of the written s:
+ *
+ *     n = s * rstd,   grad = rstd * (w dy - n mean(w dy n)) + ds,   dw = sum over rows of dy n
+ *
+ *   s, rstd     as the forward wrote them (s = x where res was NULL);  dy [rows, D], x's type
+ *   ds          [rows, D], s's type, or NULL (zeros)
+ *   dx          [rows, D] grad in x's type, dres [rows, D] grad in s's type; either may be NULL, not both.  Without
+ *               GLA_RES_F32 the two types are the same: pass one of them.  dres may equal ds, dx may equal dy
+ *   dw          [D] fp32 or NULL to skip it
+ *   workspace   gla_norm_bwd_workspace_size() bytes, 256-byte aligned (no zeroing): partial sums of dw, added in a
+ *               fixed order, so that results do not depend on timing
+ */
+int gla_norm_bwd(const void *s, const float *rstd, const float *w, const void *dy, const void *ds, void *dx, void *dres,
+                 float *dw, int64_t rows, int D, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gla_norm_bwd needs on the CURRENT device (0 for a D it would reject). */
+size_t gla_norm_bwd_workspace_size(int64_t rows, int D);
 
 #ifdef __cplusplus
 }
