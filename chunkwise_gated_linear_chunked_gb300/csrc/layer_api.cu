@@ -95,7 +95,7 @@ int check_scan_shape(int N, int B, int T, int D, bool varlen, std::initializer_l
     for (int64_t ld : lds)
         if (ld < D || ld > kMaxStride)
             return GLA_ERR_INVALID_ARG;
-    if ((long long)B * T > INT_MAX || !tiles_ok(N, D))   // row and CTA numbers are 32-bit
+    if ((long long)B * T > INT_MAX - (1 << 16) || !tiles_ok(N, D))   // row and CTA numbers are 32-bit, slices included
         return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }

@@ -73,6 +73,16 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
 
+// exp(g) as 2^(g log2 e): two instructions for the eight of expf.  Measured against fp64 on 2^20 gates a range: off by
+// at most 2.6 u (mean -0.4 u, u = 2^-24) for -1 < g < 0, where expf is off by 2.3 u (mean 0.2 u).  Further out the
+// rounding of g log2 e adds about |g| u relative, of a decay that is small by then: |g| exp(g) <= 0.37 for g <= 0.
+__device__ __forceinline__ float decay(float g)
+{
+    float a;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g * 1.4426950408889634f));
+    return a;
+}
+
 // Calls f with null pointers of the (x, gate, output) types of a recurrence dtype code.
 template <typename F>
 cudaError_t by_types(int dtype, F f)

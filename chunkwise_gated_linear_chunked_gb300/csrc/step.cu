@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(StepArgs a, int tiles)
     float h = 0.f;
     if (s >= 0) {
         const size_t at = (size_t)s * a.D + d;
-        h = fmaf(expf(widen(static_cast<const Tg *>(a.g)[b * a.ldg + d])), a.h0[at],
+        h = fmaf(decay(widen(static_cast<const Tg *>(a.g)[b * a.ldg + d])), a.h0[at],
                  widen(static_cast<const Tx *>(a.x)[b * a.ldx + d]));
         a.ht[at] = h;
     }
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(256) gla_step_kernel(StepArgs a)
         const float v = widen(static_cast<const Tx *>(a.v)[bh * a.V + j]);
         for (int i = 0; i < a.K; ++i) {
             const size_t e = bh * a.K + i;
-            const float s = fmaf(expf(widen(static_cast<const Tg *>(a.g)[e])), a.h0[at + (size_t)i * a.V],
+            const float s = fmaf(decay(widen(static_cast<const Tg *>(a.g)[e])), a.h0[at + (size_t)i * a.V],
                                  widen(static_cast<const Tx *>(a.k)[e]) * v);
             a.ht[at + (size_t)i * a.V] = s;
             o = fmaf(widen(static_cast<const Tx *>(a.x)[e]), s, o);

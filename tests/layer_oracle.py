@@ -1,9 +1,9 @@
 """Plain numpy fp64 forms of the operators beside the chunkwise kernels, each with an a-priori bound on what an
 fp32 evaluation in any order may be off by (before the output's own rounding, see ``rounding``).
 
-With u = 2^-24 (fp32): exp is within 2u of the true value, every product and sum within u.  In a recurrence
-h_t = a_t h_{t-1} + x_t, the share of h_t that comes from row s has passed t - s decays, each at most 4u (exp,
-product, sum), and at most 100 more roundings where segments are joined; W_t = sum over s of (t - s) |share| obeys
+With u = 2^-24 (fp32): exp of a gate in [-1, 0] is within 3u of the true value, every product and sum within u.  In a
+recurrence h_t = a_t h_{t-1} + x_t, the share of h_t that comes from row s has passed t - s decays, each at most 5u
+(exp, product, sum), and at most 100 more roundings where segments are joined; W_t = sum over s of (t - s) |share| obeys
 W_t = a_t (W_{t-1} + H_{t-1}) with H_t the sum of the shares' magnitudes.  The bound is u (5 W + 100 H).
 """
 import numpy as np
