@@ -10,6 +10,7 @@
 //
 // Every input is read once and every output written once.  The order of all sums is fixed by the shape.
 #include <algorithm>
+#include <type_traits>
 
 #include "api_common.h"
 #include "gla_internal.h"
@@ -22,6 +23,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kCols = 64;       // channels of a CTA: two per lane
 constexpr int kMaxCluster = 8;
+constexpr int kSlots = 2;       // tiles whose maps are in shared memory at a time
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -29,16 +31,15 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// The same variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(const float4 *p, uint32_t rank, float4 v)
+__device__ __forceinline__ void cluster_sync()
 {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank)   // the same variable of another CTA
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+    return r;
 }
 
 // 16 bytes of global memory to shared memory, the first `bytes` of them read and the rest zeros.
@@ -46,6 +47,10 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -117,6 +122,12 @@ struct Tile {
             const bool in = 16 * u < width;
             const T *p = src + (int64_t)(r0 + DIR * j0) * ld + 16 / (int)sizeof(T) * u;
             char *q = dst + j0 * kPitch + 16 * u;
+            if (width == kPitch && (unsigned)r0 < (unsigned)len && (unsigned)(r0 + DIR * (R - 1)) < (unsigned)len) {
+#pragma unroll
+                for (int j = 0; j < R; j += kStep)
+                    copy16(q + j * kPitch, p + DIR * (int64_t)j * ld);
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < R; j += kStep) {
                 const int r = r0 + DIR * (j0 + j);
@@ -170,20 +181,20 @@ struct Pair {
         on[0] = d[0] < D;
         on[1] = d[1] < D;
     }
-    template <typename T>
+    template <bool WHOLE, typename T>   // WHOLE: both channels exist
     __device__ __forceinline__ void store(T *row, float2 v) const
     {
         if constexpr (ALIGNED) {
-            if (!on[0])
+            if (!WHOLE && !on[0])
                 return;
             if constexpr (sizeof(T) == 4)
                 *reinterpret_cast<float2 *>(row + d[0]) = v;
             else
                 *reinterpret_cast<uint32_t *>(row + d[0]) = narrow2<T>(v);
         } else {
-            if (on[0])
+            if (WHOLE || on[0])
                 row[d[0]] = narrow<T>(v.x);
-            if (on[1])
+            if (WHOLE || on[1])
                 row[d[1]] = narrow<T>(v.y);
         }
     }
@@ -239,45 +250,106 @@ struct Map {
     __device__ __forceinline__ float2 operator()(float2 h) const { return fma2(A, h, H); }
 };
 
-// The state that enters this warp's rows, from the maps of all warps of all CTAs of the cluster in order.  Advances
-// `carry` past all of them.  `warps` has a row per warp, `exch` a row per CTA.
-__device__ __forceinline__ float2 enter(const Map &own, float2 &carry, float4 (*warps)[32], float4 (*exch)[32], int S,
-                                        uint32_t rank, bool first)
+struct Shared {
+    float4 warps[kSlots][kWarps][32];       // the maps of a tile's warps
+    float4 ctas[kSlots][kMaxCluster][32];   // the maps of the cluster's CTAs, pushed by each of them
+    uint64_t full[kSlots];                  // all CTAs' maps of the slot's tile are here
+    int abort;
+};
+
+__device__ __forceinline__ void open_cluster(Shared &sh)
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    warps[w][lane] = own.packed();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i)
+            tc::bar_init(&sh.full[i], 1);
+        sh.abort = 0;
+        tc::bar_fence_init();
+    }
     __syncthreads();
+    cluster_sync();   // every CTA's barriers are set up
+}
+__device__ __forceinline__ void close_cluster(Shared &sh, int *status)
+{
+    cluster_sync();   // nobody leaves while another may push into it
+    if (threadIdx.x == 0 && sh.abort)
+        report(status, GLA_ERR_TIMEOUT);
+}
+
+// This warp's map of tile t.  The last warp composes the CTA's and pushes it to every CTA of the cluster: 512 bytes a
+// CTA, counted by the receiver's barrier.  The slot's last readers are past it: a CTA pushes tile t after it has
+// received tile t - 1, hence after every CTA has pushed t - 1, which each does after reading tile t - 2.
+__device__ __forceinline__ void publish(Shared &sh, const Map &own, int t, int S, uint32_t rank)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slot = t % kSlots;
+    if (w < kWarps - 1 || S == 1) {
+        sh.warps[slot][w][lane] = own.packed();
+        if (S > 1)   // two barriers in turn: a warp arrives for tile t + 1 once it has received tile t
+            asm volatile("barrier.cta.arrive %0, %1;" ::"r"(1 + (t & 1)), "n"(kThreads) : "memory");
+        return;
+    }
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + (t & 1)), "n"(kThreads) : "memory");
+    if (lane == 0)
+        tc::bar_expect_tx(&sh.full[slot], S * 512);
+    Map all;
+#pragma unroll
+    for (int i = 0; i < kWarps - 1; ++i)
+        all.then(sh.warps[slot][i][lane]);
+    all.then(own);
+    for (int i = 0; i < S; ++i)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                         remote(&sh.ctas[slot][rank][lane], i)),
+                     "f"(all.A.x), "f"(all.A.y), "f"(all.H.x), "f"(all.H.y), "r"(remote(&sh.full[slot], i))
+                     : "memory");
+}
+
+// Waits for phase `parity` of a barrier that other CTAs' pushes complete.  Bounded: after about a second the CTA's
+// abort word is set and later waits return at once; the results are then void.
+__device__ __forceinline__ void wait_pushes(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    auto done = [&] {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}\n"
+                     : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(100000u) : "memory");
+        return ok != 0;
+    };
+    if (done())
+        return;
+    const unsigned long long t0 = tc::global_ns();
+    while (!done()) {
+        if (*abort)
+            return;
+        if (tc::global_ns() - t0 > tc::kWaitNs) {
+            *abort = 1;
+            return;
+        }
+    }
+}
+
+// The state that enters this warp's rows of tile t; advances `carry` past the cluster's tiles.
+__device__ __forceinline__ float2 receive(Shared &sh, float2 &carry, int t, int S, uint32_t rank)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slot = t % kSlots;
+    float2 in = carry;
     if (S == 1) {
-        float2 in = carry;
+        __syncthreads();   // every warp has published tile t
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             if (i == w)
                 in = carry;
-            carry = Map(warps[i][lane])(carry);
+            carry = Map(sh.warps[slot][i][lane])(carry);
         }
         return in;
     }
-    Map before;
-    for (int i = 0; i < w; ++i)
-        before.then(warps[i][lane]);
-    if (first)
-        cluster_wait();   // every CTA of the cluster has started
-    if (w == kWarps - 1) {
-        Map all = before;
-        all.then(own);
-        const float4 v = all.packed();
-        for (int i = 0; i < S; ++i)
-            store_remote(&exch[rank][lane], i, v);
-    }
-    cluster_arrive();
-    cluster_wait();
-    float2 in = carry;
+    wait_pushes(&sh.full[slot], t / kSlots & 1, &sh.abort);
     for (int i = 0; i < S; ++i) {
         if (i == (int)rank)
             in = carry;
-        carry = Map(exch[i][lane])(carry);
+        carry = Map(sh.ctas[slot][i][lane])(carry);
     }
-    return before(in);
+    for (int i = 0; i < w; ++i)
+        in = Map(sh.warps[slot][i][lane])(in);
+    return in;
 }
 
 template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT, int STAGES>
@@ -288,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(ScanArgs a, int t
     typedef Tile<Tg, R, ALIGNED> TG;
     constexpr int kStage = TX::kBytes + TG::kBytes;
     extern __shared__ __align__(128) char smem[];
-    __shared__ float4 warps[kWarps][32], exch[2][kMaxCluster][32];
+    __shared__ Shared sh;
 
     const int unit = blockIdx.x / S, n = unit / tiles, d0 = (unit - n * tiles) * kCols;
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
@@ -297,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(ScanArgs a, int t
     if (!sequence_rows(a, n, begin, len))
         return;                                       // the whole cluster leaves here
     const Pair<ALIGNED> pair(d0, a.D);
+    const bool full = d0 + kCols <= a.D;
     const int w = threadIdx.x >> 5;
     const int64_t state = (int64_t)n * a.D;
     const Tx *x = static_cast<const Tx *>(a.x) + begin * a.ldx + d0;
@@ -316,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(ScanArgs a, int t
     for (int i = 0; i < STAGES - 1; ++i)
         load(i);
     if (S > 1)
-        cluster_arrive();
+        open_cluster(sh);
     for (int it = 0; it < iters; ++it) {
         copy_wait<STAGES - 2>();
         __syncthreads();                              // tile `it` is here, and nobody reads tile it - 1 any more
@@ -330,21 +403,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(ScanArgs a, int t
             row[i].H = TX::read(st, w * RPT + i, x, a.ldx, r0 + i);
             own.then(row[i]);
         }
-        float2 s = enter(own, carry, warps, exch[it & 1], S, rank, it == 0);
+        publish(sh, own, it, S, rank);
+        float2 s = receive(sh, carry, it, S, rank);
         To *h = static_cast<To *>(a.h) + (begin + r0) * a.D;
         const int left = len - r0;
+        auto emit = [&](auto tag) {
+            constexpr bool whole = decltype(tag)::value;
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            s = row[i](s);
-            if (i < left)
-                pair.store(h, s);
-            h += a.D;
-        }
+            for (int i = 0; i < RPT; ++i) {
+                s = row[i](s);
+                if (whole || i < left)
+                    pair.template store<whole>(h + (int64_t)i * a.D, s);
+            }
+        };
+        if (left >= RPT && full)
+            emit(std::true_type());
+        else
+            emit(std::false_type());
     }
-    if (S > 1 && iters == 0)
-        cluster_wait();
     if (a.ht && rank == 0 && w == 0)
         pair.put_state(a.ht, state, carry);
+    if (S > 1)
+        close_cluster(sh, a.status);
 }
 
 template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT, int STAGES>
@@ -355,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int t
     typedef Tile<To, R, ALIGNED> TO;
     constexpr int kStage = TG::kBytes + 2 * TO::kBytes;
     extern __shared__ __align__(128) char smem[];
-    __shared__ float4 warps[kWarps][32], exch[2][kMaxCluster][32];
+    __shared__ Shared sh;
 
     const int unit = blockIdx.x / S, n = unit / tiles, d0 = (unit - n * tiles) * kCols;
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
@@ -364,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int t
     if (!sequence_rows(a, n, begin, len))
         return;
     const Pair<ALIGNED> pair(d0, a.D);
+    const bool full = d0 + kCols <= a.D;
     const int w = threadIdx.x >> 5;
     const int64_t state = (int64_t)n * a.D;
     const Tg *g = static_cast<const Tg *>(a.g) + begin * a.ldg + d0;
@@ -387,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int t
     for (int i = 0; i < STAGES - 1; ++i)
         load(i);
     if (S > 1)
-        cluster_arrive();
+        open_cluster(sh);
     for (int it = 0; it < iters; ++it) {
         copy_wait<STAGES - 2>();
         __syncthreads();
@@ -403,28 +484,34 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int t
             own.A = mul2(own.A, dec[i]);
             own.H = mul2(dec[i], add2(own.H, up[i]));
         }
-        float2 mu = enter(own, carry, warps, exch[it & 1], S, rank, it == 0);
+        publish(sh, own, it, S, rank);
+        float2 mu = receive(sh, carry, it, S, rank);
         Tx *dx = static_cast<Tx *>(a.dx) + (begin + last) * a.lddx;
         Tg *dg = static_cast<Tg *>(a.dg) + (begin + last) * a.lddg;
+        auto emit = [&](auto tag) {
+            constexpr bool whole = decltype(tag)::value;
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            float2 prev = TO::read(st + TG::kBytes + TO::kBytes, w * RPT + i, h, a.D, last - i - 1);
-            if (i == last)
-                prev = h0;
-            const float2 lam = add2(up[i], mu);
-            mu = mul2(dec[i], lam);
-            if (i <= last) {
-                pair.store(dx, lam);
-                pair.store(dg, mul2(mu, prev));
+            for (int i = 0; i < RPT; ++i) {
+                float2 prev = TO::read(st + TG::kBytes + TO::kBytes, w * RPT + i, h, a.D, last - i - 1);
+                if (!whole && i == last)
+                    prev = h0;
+                const float2 lam = add2(up[i], mu);
+                mu = mul2(dec[i], lam);
+                if (whole || i <= last) {
+                    pair.template store<whole>(dx - (int64_t)i * a.lddx, lam);
+                    pair.template store<whole>(dg - (int64_t)i * a.lddg, mul2(mu, prev));
+                }
             }
-            dx -= a.lddx;
-            dg -= a.lddg;
-        }
+        };
+        if (last >= RPT && full)
+            emit(std::true_type());
+        else
+            emit(std::false_type());
     }
-    if (S > 1 && iters == 0)
-        cluster_wait();
     if (a.dh0 && rank == 0 && w == 0)
         pair.put_state(a.dh0, state, carry);
+    if (S > 1)
+        close_cluster(sh, a.status);
 }
 
 // CTAs of a cluster: as many as run at once (two CTAs an SM), up to one time slice of R rows each.  More would wait
