@@ -23,6 +23,7 @@ struct ScanArgs {
     const int32_t *cu;                 // device offsets or nullptr
     int N, T, D;                       // sequences, rows of one sequence (dense) or of the pack, channels
     int64_t ldx, ldg, lddx, lddg;
+    int alone;                         // sequences of at most so many rows go to threads that walk alone (-1: none)
     int *status;
 };
 
@@ -51,8 +52,8 @@ struct NormArgs {
     float eps;
 };
 
-cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, cudaStream_t s);
-cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_step(const StepArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_gla_step(const StepArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s);

@@ -9,7 +9,7 @@
 // The backward is the same chain from the last row to the first: mu_t = a_t (dh_t + mu_{t+1}).
 //
 // Every input is read once and every output written once.  The order of all sums is fixed by the shape.
-#include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "api_common.h"
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kCols = 64;       // channels of a CTA: two per lane
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kSlots = 2;       // tiles whose maps are in shared memory at a time
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -111,7 +111,8 @@ struct Tile {
     static constexpr int kBytes = R * kPitch;
 
     // Row j of the tile is row r0 + DIR j of the sequence (src: its first row at the tile's first channel); rows
-    // outside [0, len) and channels from `cols` on are zeros.  A thread copies one 16-byte column of the tile.
+    // outside [0, len) and channels from `cols` on are zeros.  A thread copies
+    // from one 16-byte column of the tile.
     template <int DIR>
     static __device__ __forceinline__ void load(char *dst, const T *src, int64_t ld, int r0, int len, int cols)
     {
@@ -137,14 +138,18 @@ struct Tile {
                 q += kStep * kPitch;
             }
         } else {
-            for (int i = threadIdx.x; i < R * kUnits; i += kThreads) {
-                const int j = i / kUnits, u = i - j * kUnits, r = r0 + DIR * j;
+            constexpr int kStep = kThreads / kUnits;
+            const int u = threadIdx.x % kUnits, j0 = threadIdx.x / kUnits;
+            if (j0 >= kStep)
+                return;
+#pragma unroll
+            for (int j = j0; j < R; j += kStep) {
+                const int r = r0 + DIR * j;
                 const bool ok = (unsigned)r < (unsigned)len;
-                const T *p = src + (ok ? r * ld : 0);
+                const char *p = reinterpret_cast<const char *>(src + (ok ? r * ld : 0));
                 const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);
                 const int bytes = ok ? max(0, min(16, shift + width - 16 * u)) : 0;
-                const char *from = reinterpret_cast<const char *>(p) - shift;
-                copy16(dst + j * kPitch + 16 * u, from + (bytes ? 16 * u : 0), bytes);
+                copy16(dst + j * kPitch + 16 * u, p - shift + (bytes ? 16 * u : 0), bytes);
             }
         }
     }
@@ -252,7 +257,6 @@ struct Map {
 
 struct Shared {
     float4 warps[kSlots][kWarps][32];       // the maps of a tile's warps
-    float4 ctas[kSlots][kMaxCluster][32];   // the maps of the cluster's CTAs, pushed by each of them
     uint64_t full[kSlots];                  // all CTAs' maps of the slot's tile are here
     int abort;
 };
@@ -275,19 +279,26 @@ __device__ __forceinline__ void close_cluster(Shared &sh, int *status)
         report(status, GLA_ERR_TIMEOUT);
 }
 
-// This warp's map of tile t.  The last warp composes the CTA's and pushes it to every CTA of the cluster: 512 bytes a
-// CTA, counted by the receiver's barrier.  The slot's last readers are past it: a CTA pushes tile t after it has
+// This warp's map of tile t.  The last warp composes the CTA's and pushes it to every CTA of the cluster (`ctas`, S
+// rows a slot): 512 bytes a CTA, counted by the receiver's barrier.  The slot's last readers are past it: a CTA pushes tile t after it has
 // received tile t - 1, hence after every CTA has pushed t - 1, which each does after reading tile t - 2.
-__device__ __forceinline__ void publish(Shared &sh, const Map &own, int t, int S, uint32_t rank)
+__device__ __forceinline__ void publish(Shared &sh, float4 *ctas, const Map &own, int t, int S, uint32_t rank)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slot = t % kSlots;
     if (w < kWarps - 1 || S == 1) {
         sh.warps[slot][w][lane] = own.packed();
-        if (S > 1)   // two barriers in turn: a warp arrives for tile t + 1 once it has received tile t
-            asm volatile("barrier.cta.arrive %0, %1;" ::"r"(1 + (t & 1)), "n"(kThreads) : "memory");
+        if (S > 1) {   // two barriers in turn: a warp arrives for tile t + 1 once it has received tile t
+            if (t & 1)
+                asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory");
+            else
+                asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kThreads) : "memory");
+        }
         return;
     }
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + (t & 1)), "n"(kThreads) : "memory");
+    if (t & 1)
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
+    else
+        asm volatile("barrier.cta.sync 2, %0;" ::"n"(kThreads) : "memory");
     if (lane == 0)
         tc::bar_expect_tx(&sh.full[slot], S * 512);
     Map all;
@@ -297,7 +308,7 @@ __device__ __forceinline__ void publish(Shared &sh, const Map &own, int t, int S
     all.then(own);
     for (int i = 0; i < S; ++i)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                         remote(&sh.ctas[slot][rank][lane], i)),
+                         remote(ctas + (slot * S + rank) * 32 + lane, i)),
                      "f"(all.A.x), "f"(all.A.y), "f"(all.H.x), "f"(all.H.y), "r"(remote(&sh.full[slot], i))
                      : "memory");
 }
@@ -327,7 +338,7 @@ __device__ __forceinline__ void wait_pushes(uint64_t *bar, uint32_t parity, vola
 }
 
 // The state that enters this warp's rows of tile t; advances `carry` past the cluster's tiles.
-__device__ __forceinline__ float2 receive(Shared &sh, float2 &carry, int t, int S, uint32_t rank)
+__device__ __forceinline__ float2 receive(Shared &sh, const float4 *ctas, float2 &carry, int t, int S, uint32_t rank)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slot = t % kSlots;
     float2 in = carry;
@@ -345,247 +356,454 @@ __device__ __forceinline__ float2 receive(Shared &sh, float2 &carry, int t, int 
     for (int i = 0; i < S; ++i) {
         if (i == (int)rank)
             in = carry;
-        carry = Map(sh.ctas[slot][i][lane])(carry);
+        carry = Map(ctas[(slot * S + i) * 32 + lane])(carry);
     }
     for (int i = 0; i < w; ++i)
         in = Map(sh.warps[slot][i][lane])(in);
     return in;
 }
 
-template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT, int STAGES>
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(ScanArgs a, int tiles, int S)
-{
-    constexpr int R = kWarps * RPT;
+// What a CTA does with its tiles.  Position p of the forward's walk is row p of the sequence.
+template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT_>
+struct Forward {
+    static constexpr int RPT = RPT_, R = kWarps * RPT;
     typedef Tile<Tx, R, ALIGNED> TX;
     typedef Tile<Tg, R, ALIGNED> TG;
-    constexpr int kStage = TX::kBytes + TG::kBytes;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ Shared sh;
-
-    const int unit = blockIdx.x / S, n = unit / tiles, d0 = (unit - n * tiles) * kCols;
-    const uint32_t rank = S > 1 ? cluster_rank() : 0;
-    int64_t begin;
+    static constexpr int kStage = TX::kBytes + TG::kBytes;
+    typedef Pair<ALIGNED> Lane;
+    Map row[RPT];
+    const Tx *x;
+    const Tg *g;
+    To *h;
     int len;
-    if (!sequence_rows(a, n, begin, len))
-        return;                                       // the whole cluster leaves here
-    const Pair<ALIGNED> pair(d0, a.D);
-    const bool full = d0 + kCols <= a.D;
-    const int w = threadIdx.x >> 5;
-    const int64_t state = (int64_t)n * a.D;
-    const Tx *x = static_cast<const Tx *>(a.x) + begin * a.ldx + d0;
-    const Tg *g = static_cast<const Tg *>(a.g) + begin * a.ldg + d0;
-    float2 carry = pair.state(a.h0, state);
-    const int step = S * R, iters = (len + step - 1) / step;
-    auto load = [&](int it) {
-        if (it < iters) {
-            char *st = smem + it % STAGES * kStage;
-            const int r0 = it * step + rank * R;
-            TX::template load<1>(st, x, a.ldx, r0, len, a.D - d0);
-            TG::template load<1>(st + TX::kBytes, g, a.ldg, r0, len, a.D - d0);
-        }
-        copy_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        load(i);
-    if (S > 1)
-        open_cluster(sh);
-    for (int it = 0; it < iters; ++it) {
-        copy_wait<STAGES - 2>();
-        __syncthreads();                              // tile `it` is here, and nobody reads tile it - 1 any more
-        load(it + STAGES - 1);
-        const char *st = smem + it % STAGES * kStage;
-        const int r0 = it * step + rank * R + w * RPT;
-        Map row[RPT], own;
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            row[i].A = decay2(TG::read(st + TX::kBytes, w * RPT + i, g, a.ldg, r0 + i));
-            row[i].H = TX::read(st, w * RPT + i, x, a.ldx, r0 + i);
-            own.then(row[i]);
-        }
-        publish(sh, own, it, S, rank);
-        float2 s = receive(sh, carry, it, S, rank);
-        To *h = static_cast<To *>(a.h) + (begin + r0) * a.D;
-        const int left = len - r0;
-        auto emit = [&](auto tag) {
-            constexpr bool whole = decltype(tag)::value;
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                s = row[i](s);
-                if (whole || i < left)
-                    pair.template store<whole>(h + (int64_t)i * a.D, s);
-            }
-        };
-        if (left >= RPT && full)
-            emit(std::true_type());
-        else
-            emit(std::false_type());
+    bool full;   // the tile's channels all exist
+
+    __device__ __forceinline__ Forward(const ScanArgs &a, int64_t begin, int len, int d0, const Lane &, int64_t)
+        : x(static_cast<const Tx *>(a.x) + begin * a.ldx + d0), g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0),
+          h(static_cast<To *>(a.h) + begin * a.D), len(len), full(d0 + kCols <= a.D) {}
+    static __device__ __forceinline__ const float *start(const ScanArgs &a) { return a.h0; }
+    static __device__ __forceinline__ float *end(const ScanArgs &a) { return a.ht; }
+    __device__ __forceinline__ void load(const ScanArgs &a, char *st, int p, int d0) const
+    {
+        TX::template load<1>(st, x, a.ldx, p, len, a.D - d0);
+        TG::template load<1>(st + TX::kBytes, g, a.ldg, p, len, a.D - d0);
     }
-    if (a.ht && rank == 0 && w == 0)
-        pair.put_state(a.ht, state, carry);
-    if (S > 1)
-        close_cluster(sh, a.status);
-}
-
-template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT, int STAGES>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int tiles, int S)
-{
-    constexpr int R = kWarps * RPT;
-    typedef Tile<Tg, R, ALIGNED> TG;
-    typedef Tile<To, R, ALIGNED> TO;
-    constexpr int kStage = TG::kBytes + 2 * TO::kBytes;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ Shared sh;
-
-    const int unit = blockIdx.x / S, n = unit / tiles, d0 = (unit - n * tiles) * kCols;
-    const uint32_t rank = S > 1 ? cluster_rank() : 0;
-    int64_t begin;
-    int len;
-    if (!sequence_rows(a, n, begin, len))
-        return;
-    const Pair<ALIGNED> pair(d0, a.D);
-    const bool full = d0 + kCols <= a.D;
-    const int w = threadIdx.x >> 5;
-    const int64_t state = (int64_t)n * a.D;
-    const Tg *g = static_cast<const Tg *>(a.g) + begin * a.ldg + d0;
-    const To *h = static_cast<const To *>(a.h_in) + begin * a.D + d0;
-    const To *dh = static_cast<const To *>(a.dh) + begin * a.D + d0;
-    float2 carry = pair.state(a.dht, state);
-    const float2 h0 = pair.state(a.h0, state);
-    const int step = S * R, iters = (len + step - 1) / step;
-    // position p of the walk is row len - 1 - p
-    auto load = [&](int it) {
-        if (it < iters) {
-            char *st = smem + it % STAGES * kStage;
-            const int last = len - 1 - (it * step + (int)rank * R);
-            TG::template load<-1>(st, g, a.ldg, last, len, a.D - d0);
-            TO::template load<-1>(st + TG::kBytes, dh, a.D, last, len, a.D - d0);
-            TO::template load<-1>(st + TG::kBytes + TO::kBytes, h, a.D, last - 1, len, a.D - d0);
-        }
-        copy_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        load(i);
-    if (S > 1)
-        open_cluster(sh);
-    for (int it = 0; it < iters; ++it) {
-        copy_wait<STAGES - 2>();
-        __syncthreads();
-        load(it + STAGES - 1);
-        const char *st = smem + it % STAGES * kStage;
-        const int last = len - 1 - (it * step + (int)rank * R + w * RPT);
-        float2 dec[RPT], up[RPT];
+    // Positions p.. of the walk, rows j.. of the tile.
+    __device__ __forceinline__ Map fold(const ScanArgs &a, const char *st, int p, int j)
+    {
         Map own;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            dec[i] = decay2(TG::read(st, w * RPT + i, g, a.ldg, last - i));
-            up[i] = TO::read(st + TG::kBytes, w * RPT + i, dh, a.D, last - i);
+            row[i].A = decay2(TG::read(st + TX::kBytes, j + i, g, a.ldg, p + i));
+            row[i].H = TX::read(st, j + i, x, a.ldx, p + i);
+            own.then(row[i]);
+        }
+        return own;
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void put(const ScanArgs &a, float2 s, int p, const Lane &lane) const
+    {
+        To *at = h + (int64_t)p * a.D;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            s = row[i](s);
+            if (WHOLE || p + i < len)
+                lane.template store<WHOLE>(at + (int64_t)i * a.D, s);
+        }
+    }
+    __device__ __forceinline__ void emit(const ScanArgs &a, const char *, float2 s, int p, int, const Lane &lane) const
+    {
+        if (full && p + RPT <= len)
+            put<true>(a, s, p, lane);
+        else
+            put<false>(a, s, p, lane);
+    }
+};
+
+// Position p of the backward's walk is row len - 1 - p; its state is mu.
+template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT_>
+struct Backward {
+    static constexpr int RPT = RPT_, R = kWarps * RPT;
+    typedef Tile<Tg, R, ALIGNED> TG;
+    typedef Tile<To, R, ALIGNED> TO;
+    static constexpr int kStage = TG::kBytes + 2 * TO::kBytes;
+    typedef Pair<ALIGNED> Lane;
+    float2 dec[RPT], up[RPT];
+    const Tg *g;
+    const To *h, *dh;
+    Tx *dx;
+    Tg *dg;
+    int len;
+    bool full;
+    const float2 h0;
+
+    __device__ __forceinline__ Backward(const ScanArgs &a, int64_t begin, int len, int d0, const Lane &lane, int64_t state)
+        : g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0), h(static_cast<const To *>(a.h_in) + begin * a.D + d0),
+          dh(static_cast<const To *>(a.dh) + begin * a.D + d0), dx(static_cast<Tx *>(a.dx) + begin * a.lddx),
+          dg(static_cast<Tg *>(a.dg) + begin * a.lddg), len(len), full(d0 + kCols <= a.D), h0(lane.state(a.h0, state)) {}
+    static __device__ __forceinline__ const float *start(const ScanArgs &a) { return a.dht; }
+    static __device__ __forceinline__ float *end(const ScanArgs &a) { return a.dh0; }
+    __device__ __forceinline__ void load(const ScanArgs &a, char *st, int p, int d0) const
+    {
+        const int r = len - 1 - p;
+        TG::template load<-1>(st, g, a.ldg, r, len, a.D - d0);
+        TO::template load<-1>(st + TG::kBytes, dh, a.D, r, len, a.D - d0);
+        TO::template load<-1>(st + TG::kBytes + TO::kBytes, h, a.D, r - 1, len, a.D - d0);
+    }
+    __device__ __forceinline__ Map fold(const ScanArgs &a, const char *st, int p, int j)
+    {
+        const int r = len - 1 - p;
+        Map own;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            dec[i] = decay2(TG::read(st, j + i, g, a.ldg, r - i));
+            up[i] = TO::read(st + TG::kBytes, j + i, dh, a.D, r - i);
             own.A = mul2(own.A, dec[i]);
             own.H = mul2(dec[i], add2(own.H, up[i]));
         }
-        publish(sh, own, it, S, rank);
-        float2 mu = receive(sh, carry, it, S, rank);
-        Tx *dx = static_cast<Tx *>(a.dx) + (begin + last) * a.lddx;
-        Tg *dg = static_cast<Tg *>(a.dg) + (begin + last) * a.lddg;
-        auto emit = [&](auto tag) {
-            constexpr bool whole = decltype(tag)::value;
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                float2 prev = TO::read(st + TG::kBytes + TO::kBytes, w * RPT + i, h, a.D, last - i - 1);
-                if (!whole && i == last)
-                    prev = h0;
-                const float2 lam = add2(up[i], mu);
-                mu = mul2(dec[i], lam);
-                if (whole || i <= last) {
-                    pair.template store<whole>(dx - (int64_t)i * a.lddx, lam);
-                    pair.template store<whole>(dg - (int64_t)i * a.lddg, mul2(mu, prev));
-                }
-            }
-        };
-        if (last >= RPT && full)
-            emit(std::true_type());
-        else
-            emit(std::false_type());
+        return own;
     }
-    if (a.dh0 && rank == 0 && w == 0)
-        pair.put_state(a.dh0, state, carry);
+    template <bool WHOLE>
+    __device__ __forceinline__ void put(const ScanArgs &a, const char *st, float2 mu, int r, int j, const Lane &lane) const
+    {
+        Tx *to_x = dx + (int64_t)r * a.lddx;
+        Tg *to_g = dg + (int64_t)r * a.lddg;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            float2 prev = TO::read(st + TG::kBytes + TO::kBytes, j + i, h, a.D, r - i - 1);
+            if (!WHOLE && i == r)
+                prev = h0;
+            const float2 lam = add2(up[i], mu);
+            mu = mul2(dec[i], lam);
+            if (WHOLE || i <= r) {
+                lane.template store<WHOLE>(to_x - (int64_t)i * a.lddx, lam);
+                lane.template store<WHOLE>(to_g - (int64_t)i * a.lddg, mul2(mu, prev));
+            }
+        }
+    }
+    __device__ __forceinline__ void emit(const ScanArgs &a, const char *st, float2 mu, int p, int j, const Lane &lane) const
+    {
+        const int r = len - 1 - p;
+        if (full && r >= RPT)
+            put<true>(a, st, mu, r, j, lane);
+        else
+            put<false>(a, st, mu, r, j, lane);
+    }
+};
+
+// Tiles in shared memory at a time: three where two CTAs of an SM have room for them (16-bit forward), else two.
+template <typename Role>
+constexpr int kStages = Role::kStage <= 32768 ? 3 : 2;
+
+template <typename Role>
+__global__ void __launch_bounds__(kThreads, 2) scan_tiles(ScanArgs a, int tiles, int S)
+{
+    constexpr int RPT = Role::RPT, R = Role::R, STAGES = kStages<Role>;
+    extern __shared__ __align__(128) char smem[];     // STAGES tiles, then the cluster's maps
+    __shared__ Shared sh;
+    float4 *ctas = reinterpret_cast<float4 *>(smem + STAGES * Role::kStage);
+
+    const int unit = blockIdx.x / S, n = unit / tiles, d0 = (unit - n * tiles) * kCols;
+    const uint32_t rank = S > 1 ? cluster_rank() : 0;
+    int64_t begin;
+    int len;
+    if (!sequence_rows(a, n, begin, len) || len <= a.alone)
+        return;                                       // the whole cluster leaves here
+    const typename Role::Lane lane(d0, a.D);
+    const int w = threadIdx.x >> 5;
+    const int64_t state = (int64_t)n * a.D;
+    Role role(a, begin, len, d0, lane, state);
+    float2 carry = lane.state(Role::start(a), state);
+    const int step = S * R, iters = (len + step - 1) / step;
+    auto load = [&](int t) {
+        if (t < iters)
+            role.load(a, smem + t % STAGES * Role::kStage, t * step + rank * R, d0);
+        copy_commit();
+    };
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t)
+        load(t);
+    if (S > 1)
+        open_cluster(sh);
+    for (int t = 0; t < iters; ++t) {
+        copy_wait<STAGES - 2>();
+        __syncthreads();                              // tile t is here, and nobody reads tile t - 1 any more
+        load(t + STAGES - 1);
+        const char *st = smem + t % STAGES * Role::kStage;
+        const int p = t * step + rank * R + w * RPT;
+        publish(sh, ctas, role.fold(a, st, p, w * RPT), t, S, rank);
+        role.emit(a, st, receive(sh, ctas, carry, t, S, rank), p, w * RPT, lane);
+    }
+    if (Role::end(a) && rank == 0 && w == 0)
+        lane.put_state(Role::end(a), state, carry);
     if (S > 1)
         close_cluster(sh, a.status);
 }
 
-// CTAs of a cluster: as many as run at once (two CTAs an SM), up to one time slice of R rows each.  More would wait
-// for a second wave, whose clusters start when the first have ended: 8 x 4096 rows of 2048 channels, backward, run in
-// 115 us with 256 CTAs and in 152 us with 512.
-int cluster_size(int64_t units, int64_t rows, int R)
+// The lane's two channels of a row as they lie in memory: 2 l and 2 l + 1 in one load where rows start and step in
+// whole pairs (PAIRED), else l and l + 32 one by one.
+template <typename T, bool PAIRED>
+struct Two {
+    typedef std::conditional_t<PAIRED, std::conditional_t<sizeof(T) == 4, float2, uint32_t>, T> Raw;
+    Raw v[PAIRED ? 1 : 2];
+
+    __device__ __forceinline__ void load(const T *p, bool on0, bool on1)   // p: the lane's first channel
+    {
+        if constexpr (PAIRED) {
+            v[0] = on0 ? *reinterpret_cast<const Raw *>(p) : Raw{};
+        } else {
+            v[0] = on0 ? p[0] : T(0.f);
+            v[1] = on1 ? p[32] : T(0.f);
+        }
+    }
+    __device__ __forceinline__ float2 get() const
+    {
+        if constexpr (!PAIRED)
+            return make_float2(widen(v[0]), widen(v[1]));
+        else if constexpr (sizeof(T) == 4)
+            return v[0];
+        else
+            return widen2<T>(v[0]);
+    }
+    static __device__ __forceinline__ void store(T *p, float2 f, bool on0, bool on1)
+    {
+        if constexpr (PAIRED) {
+            if (on0) {
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<float2 *>(p) = f;
+                else
+                    *reinterpret_cast<uint32_t *>(p) = narrow2<T>(f);
+            }
+        } else {
+            if (on0)
+                p[0] = narrow<T>(f.x);
+            if (on1)
+                p[32] = narrow<T>(f.y);
+        }
+    }
+};
+
+
+// Few rows, or so many channels that they alone fill the GPU: a thread walks two channels of a sequence, kAhead rows
+// at a time.
+constexpr int kAhead = 8;
+
+template <typename Tx, typename Tg, typename To, bool PAIRED>
+__global__ void __launch_bounds__(128) scan_fwd_rows(ScanArgs a, int tiles)
 {
-    const int64_t fit = 2 * sm_count() / std::max<int64_t>(units, 1), slices = (rows + R - 1) / R;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({fit, slices, kMaxCluster}));
+    const int n = blockIdx.x / tiles, c = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5), d0 = c * kCols;
+    int64_t begin;
+    int len;
+    if (!sequence_rows(a, n, begin, len) || len > a.alone || d0 >= a.D)
+        return;
+    const Pair<PAIRED> lane(d0, a.D);
+    const int64_t state = (int64_t)n * a.D;
+    const Tx *x = static_cast<const Tx *>(a.x) + begin * a.ldx + lane.d[0];
+    const Tg *g = static_cast<const Tg *>(a.g) + begin * a.ldg + lane.d[0];
+    To *h = static_cast<To *>(a.h) + begin * a.D + lane.d[0];
+    float2 s = lane.state(a.h0, state);
+    for (int r = 0; r < len; r += kAhead) {
+        Two<Tx, PAIRED> xs[kAhead];
+        Two<Tg, PAIRED> gs[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const bool ok = r + i < len;
+            xs[i].load(x + (int64_t)i * a.ldx, ok && lane.on[0], ok && lane.on[1]);
+            gs[i].load(g + (int64_t)i * a.ldg, ok && lane.on[0], ok && lane.on[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (r + i < len) {
+                s = fma2(decay2(gs[i].get()), s, xs[i].get());
+                Two<To, PAIRED>::store(h + (int64_t)i * a.D, s, lane.on[0], lane.on[1]);
+            }
+        x += kAhead * a.ldx;
+        g += kAhead * a.ldg;
+        h += kAhead * (int64_t)a.D;
+    }
+    if (a.ht)
+        lane.put_state(a.ht, state, s);
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ScanArgs &a, int R, int smem, cudaStream_t s)
+template <typename Tx, typename Tg, typename To, bool PAIRED>
+__global__ void __launch_bounds__(128) scan_bwd_rows(ScanArgs a, int tiles)
 {
-    const int tiles = (a.D + kCols - 1) / kCols;
-    const int S = cluster_size((int64_t)a.N * tiles, a.T, R);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.N * tiles * S);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
+    const int n = blockIdx.x / tiles, c = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5), d0 = c * kCols;
+    int64_t begin;
+    int len;
+    if (!sequence_rows(a, n, begin, len) || len > a.alone || d0 >= a.D)
+        return;
+    const Pair<PAIRED> lane(d0, a.D);
+    const int64_t state = (int64_t)n * a.D;
+    const float2 h0 = lane.state(a.h0, state);
+    float2 mu = lane.state(a.dht, state);
+    for (int r = len - 1; r >= 0; r -= kAhead) {
+        const int64_t at = begin + r;
+        const Tg *g = static_cast<const Tg *>(a.g) + at * a.ldg + lane.d[0];
+        const To *dh = static_cast<const To *>(a.dh) + at * a.D + lane.d[0];
+        const To *h = static_cast<const To *>(a.h_in) + (at - 1) * a.D + lane.d[0];
+        Two<Tg, PAIRED> gs[kAhead];
+        Two<To, PAIRED> ds[kAhead], hs[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            gs[i].load(g - (int64_t)i * a.ldg, i <= r && lane.on[0], i <= r && lane.on[1]);
+            ds[i].load(dh - (int64_t)i * a.D, i <= r && lane.on[0], i <= r && lane.on[1]);
+            hs[i].load(h - (int64_t)i * a.D, i < r && lane.on[0], i < r && lane.on[1]);
+        }
+        Tx *dx = static_cast<Tx *>(a.dx) + at * a.lddx + lane.d[0];
+        Tg *dg = static_cast<Tg *>(a.dg) + at * a.lddg + lane.d[0];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i <= r) {
+                const float2 lam = add2(ds[i].get(), mu);
+                mu = mul2(decay2(gs[i].get()), lam);
+                Two<Tx, PAIRED>::store(dx - (int64_t)i * a.lddx, lam, lane.on[0], lane.on[1]);
+                Two<Tg, PAIRED>::store(dg - (int64_t)i * a.lddg, mul2(mu, i == r ? h0 : hs[i].get()), lane.on[0], lane.on[1]);
+            }
+    }
+    if (a.dh0)
+        lane.put_state(a.dh0, state, mu);
+}
+
+// Clusters of S = 1..kMaxCluster CTAs of a kernel that the current device runs at once.
+struct Fit {
+    std::mutex mu;
+    bool known[128] = {};
+    int clusters[128][kMaxCluster + 1] = {};
+};
+
+template <typename Role>
+cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
+{
+    static Fit fit;
+    constexpr int STAGES = kStages<Role>;
+    auto kernel = scan_tiles<Role>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= 128)
+        return e != cudaSuccess ? e : cudaErrorInvalidDevice;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = S;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    auto shape = [&](int64_t units, int S) {
+        at[0].val.clusterDim.x = S;
+        cfg.gridDim = dim3((unsigned)(units * S));
+        cfg.dynamicSmemBytes = STAGES * Role::kStage + (S > 1 ? kSlots * S * 512 : 0);
+    };
+    std::lock_guard<std::mutex> lock(fit.mu);
+    if (!fit.known[dev]) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      STAGES * Role::kStage + kSlots * kMaxCluster * 512)) != cudaSuccess)
+            return e;
+        for (int S = 1; S <= kMaxCluster; ++S) {
+            shape(1, S);
+            if (cudaOccupancyMaxActiveClusters(&fit.clusters[dev][S], kernel, &cfg) != cudaSuccess)
+                fit.clusters[dev][S] = 0;   // a size this device does not have
+        }
+        cudaGetLastError();
+        fit.known[dev] = true;
+    }
+    // As many CTAs a sequence as run at once, up to one time slice each.  More would wait for a second wave, whose
+    // clusters start when the first have ended: 8 x 4096 rows of 2048 channels, backward, run in 115 us with 256 CTAs
+    // and in 152 us with 512.
+    const int tiles = (a.D + kCols - 1) / kCols;
+    const int64_t units = (int64_t)a.N * tiles;
+    int S = 1;
+    for (int c = 2; c <= kMaxCluster && (c - 1) * Role::R < a.T; ++c)
+        if (fit.clusters[dev][c] >= units)
+            S = c;
+    shape(units, S);
     return cudaLaunchKernelEx(&cfg, kernel, a, tiles, S);
 }
 
-// Whether rows of `elem`-byte elements start and step in 16-byte units.
+// Whether rows of `elem`-byte elements start and step in 16-byte units, or in whole pairs of channels.
 bool units16(int64_t ld, int D, int elem) { return ld * elem % 16 == 0 && (int64_t)D * elem % 16 == 0; }
+bool pairs(int64_t ld, int D) { return ld % 2 == 0 && D % 2 == 0; }
 
-template <typename Tx, typename Tg, typename To, bool ALIGNED>
-cudaError_t fwd(const ScanArgs &a, cudaStream_t s)
+// How a call's sequences are shared out: those of at most `rows` rows to threads that walk alone, the others to the
+// tiles.  Alone is better for 16 rows at most (512 x 16 rows of 2048 channels: 19 us against 130), and for up to 128
+// where there are enough channels to fill the GPU (256 x 128 rows of 2048 channels: 69 us against 83; 64 x 128 rows of
+// 1024: 20 against 15).  The lengths of a pack are not known here: one of many sequences takes both kernels, each
+// leaving the other's sequences alone; a pack of fewer takes the tiles, which split a long sequence too.
+struct Share {
+    int rows;
+    bool tiles;
+};
+Share share_out(const ScanArgs &a)
 {
-    constexpr int RPT = sizeof(Tx) + sizeof(Tg) > 4 ? 8 : 16, R = kWarps * RPT, STAGES = 3;
-    return launch(scan_fwd_kernel<Tx, Tg, To, ALIGNED, RPT, STAGES>, a, R,
-                  STAGES * (Tile<Tx, R, ALIGNED>::kBytes + Tile<Tg, R, ALIGNED>::kBytes), s);
+    const int64_t channels = (int64_t)a.N * a.D;
+    if (a.cu)
+        return channels >= 8 * kCols * (int64_t)sm_count() ? Share{64, true} : Share{-1, true};
+    const bool alone = a.T <= 16 || (a.T <= 128 && channels >= 2048 * (int64_t)a.T);
+    return alone ? Share{a.T, false} : Share{-1, true};
 }
 
 template <typename Tx, typename Tg, typename To, bool ALIGNED>
-cudaError_t bwd(const ScanArgs &a, cudaStream_t s)
+cudaError_t fwd_tiles(const ScanArgs &a, cudaStream_t s)
 {
-    constexpr int RPT = 8, R = kWarps * RPT, STAGES = 3;
-    return launch(scan_bwd_kernel<Tx, Tg, To, ALIGNED, RPT, STAGES>, a, R,
-                  STAGES * (Tile<Tg, R, ALIGNED>::kBytes + 2 * Tile<To, R, ALIGNED>::kBytes), s);
+    // rows of a thread: the more the fewer exchanges, as registers and shared memory allow for two CTAs an SM
+    return launch_tiles<Forward<Tx, Tg, To, ALIGNED, sizeof(Tx) + sizeof(Tg) == 4 ? 16 : 8>>(a, s);
+}
+
+template <typename Tx, typename Tg, typename To, bool ALIGNED>
+cudaError_t bwd_tiles(const ScanArgs &a, cudaStream_t s)
+{
+    constexpr int kBytes = sizeof(Tg) + 2 * sizeof(To);
+    return launch_tiles<Backward<Tx, Tg, To, ALIGNED, ALIGNED ? (kBytes == 6 ? 16 : 8) : (kBytes == 12 ? 4 : 8)>>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, cudaStream_t s)
+cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s)
 {
+    const Share share = share_out(a);
+    a.alone = share.rows;
     return by_types(dtype, [&](auto x, auto g, auto o) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
+        if (share.rows >= 0) {
+            const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
+            if (pairs(a.ldx, a.D) && pairs(a.ldg, a.D))
+                scan_fwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
+            else
+                scan_fwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess || !share.tiles)
+                return e;
+        }
         const bool ok = units16(a.ldx, a.D, sizeof(Tx)) && units16(a.ldg, a.D, sizeof(Tg));
-        return ok ? fwd<Tx, Tg, To, true>(a, s) : fwd<Tx, Tg, To, false>(a, s);
+        return ok ? fwd_tiles<Tx, Tg, To, true>(a, s) : fwd_tiles<Tx, Tg, To, false>(a, s);
     });
 }
 
-cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, cudaStream_t s)
+cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s)
 {
+    const Share share = share_out(a);
+    a.alone = share.rows;
     return by_types(dtype, [&](auto x, auto g, auto o) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
+        if (share.rows >= 0) {
+            const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
+            if (pairs(a.ldg, a.D) && pairs(a.lddx, a.D) && pairs(a.lddg, a.D))
+                scan_bwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
+            else
+                scan_bwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess || !share.tiles)
+                return e;
+        }
         const bool ok = units16(a.ldg, a.D, sizeof(Tg)) && units16(a.D, a.D, sizeof(To)) &&
                         units16(a.lddx, a.D, sizeof(Tx)) && units16(a.lddg, a.D, sizeof(Tg));
-        return ok ? bwd<Tx, Tg, To, true>(a, s) : bwd<Tx, Tg, To, false>(a, s);
+        return ok ? bwd_tiles<Tx, Tg, To, true>(a, s) : bwd_tiles<Tx, Tg, To, false>(a, s);
     });
 }
 

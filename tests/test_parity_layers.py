@@ -107,6 +107,23 @@ def test_scan_many_short_sequences(B):
     within(ht, ref_t, tol_t)
 
 
+@pytest.mark.parametrize("types,D", [((TB, TB, TB), 128), ((T32, T32, T32), 77)], ids=["bf16", "f32"])
+def test_scan_pack_of_many_lengths(B, types, D):
+    """Enough sequences that short ones and long ones are walked by different kernels."""
+    lengths = [3, 0, 64, 65, 1, 130, 700] * 160
+    x, g, h0, cu = scan_inputs(types, 1, 0, D, lengths, seed=30)
+    cu_d, h0_d, g_d = cu.cuda(), h0.cuda(), g.cuda()
+    h, ht = B.scan_fwd(x.cuda(), g_d, initial_state=h0_d, cu_seqlens=cu_d)
+    ref, ref_t, tol, tol_t = lo.scan_fwd(f64(x), f64(g), f64(h0), cu)
+    within(h, ref, tol, "h")
+    within(ht, ref_t, tol_t, "ht")
+    dh = torch.randn(h.shape, generator=torch.Generator().manual_seed(31)).to(types[2]).cuda()
+    grads = B.scan_bwd(g_d, h, dh, initial_state=h0_d, cu_seqlens=cu_d)
+    refs, tols = lo.scan_bwd(f64(g), f64(h), f64(dh), f64(h0), None, cu)
+    for name, y, r, t in zip(("dx", "dg", "dh0"), grads, refs, tols):
+        within(y, r, t, name)
+
+
 def test_scan_many_batches_of_few_rows(B):
     for T in (1, 2, 9, 17):
         x, g, h0, _ = scan_inputs((TH, TH), 301, T, 72, seed=T)
