@@ -1,5 +1,6 @@
 // C ABI of the operators beside the chunkwise kernels: argument checks and launches of the vector-state gated
 // linear recurrence, the one-token state updates and the residual norm.  Contracts: include/gla.h.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -327,7 +328,8 @@ extern "C" size_t gla_norm_bwd_workspace_size(int64_t rows, int D)
 {
     if (rows < 0 || D <= 0 || D > kMaxNormD)
         return 0;
-    return kAlign + align_up((size_t)norm_bwd_ctas(rows, D) * D * 4);
+    const int ctas = std::max(norm_bwd_ctas(rows, D, GLA_F32), norm_bwd_ctas(rows, D, GLA_BF16));
+    return kAlign + align_up((size_t)ctas * D * 4);
 }
 
 extern "C" int gla_norm_bwd(const void *s, const float *rstd, const float *w, const void *dy, const void *ds, void *dx,
@@ -367,7 +369,7 @@ extern "C" int gla_norm_bwd(const void *s, const float *rstd, const float *w, co
     a.s_in = s; a.rstd_in = rstd; a.w = w; a.dy = dy; a.ds = ds; a.dx = dx; a.dres = dres; a.dw = dw;
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAlign);
     a.rows = rows; a.D = D;
-    a.ctas = norm_bwd_ctas(rows, D);
+    a.ctas = norm_bwd_ctas(rows, D, dtype & ~GLA_RES_F32);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool res_f32 = (dtype & GLA_RES_F32) != 0;
     if (rows > 0 && profiled(K_NORM_BWD, st, [&] {

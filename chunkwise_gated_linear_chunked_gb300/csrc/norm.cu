@@ -1,10 +1,15 @@
 // Residual addition and root-mean-square norm: forward (fp32 / 16-bit or e4m3 output) and backward.
 //
-// Up to 8192 columns a row lives in registers, 16 values a thread: it is read once, reduced, and written.  A warp holds
-// 512 adjacent columns (so a group of 128 columns never leaves a warp), up to 16 warps a row; rows of at most 256
-// columns share a warp.  A CTA keeps its share of the weights in registers, walks rows a grid apart, and asks for its
-// next row before it reduces the present one.  Wider rows are read again from cache instead, by one CTA a row.
+// Up to 8176 columns a row lives in registers, 16 values a thread: it is read once, reduced, and written.  A warp holds
+// 512 adjacent columns, up to 16 warps a row; rows of at most 256 columns share a warp.  A CTA keeps its share of the
+// weights in registers, walks rows a grid apart, and asks for its next row before it reduces the present one.  Wider
+// rows are read again from cache instead, by one CTA a row.
+//
+// Memory is read and written in whole 16-byte units whatever D is.  A row starts k values into such a unit; a thread's
+// vectors lie on units, so vector v holds columns VEC v - k and up, and the two vectors that hang over the row's ends
+// go value by value.  Rows a multiple of VEC apart have the same k, so a thread keeps its columns (and its weights).
 #include <algorithm>
+#include <atomic>
 
 #include "api_common.h"
 #include "layer_internal.h"
@@ -14,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;        // threads of a CTA (more where a row needs them)
 constexpr int kHeld = 16;            // values of a row in a thread
-constexpr int kMaxHeld = 8192;       // columns of a row that 16 warps hold
+constexpr int kMaxHeld = 8192;       // columns of a row that 16 warps hold (fewer by kHeld where rows are shifted)
 constexpr float kE4m3Max = 448.f, kScaleMin = 1e-30f;
 
 // Maximum that keeps a NaN of either side.
@@ -29,366 +34,504 @@ __device__ __forceinline__ float max_nan(float a, float b)
 struct Split {
     int lanes, rows, threads;
 };
-inline Split split_of(int D)
+int held_columns(int D, int vec) { return D % vec ? D + vec - 1 : D; }   // with what hangs over
+Split split_of(int D, int vec)
 {
+    const int held = held_columns(D, vec);
     Split s;
-    if (D <= 256) {
+    if (held <= 256) {
         s.lanes = 1;
-        while (s.lanes * kHeld < D)
+        while (s.lanes * kHeld < held)
             s.lanes *= 2;
     } else {
-        s.lanes = (D + 32 * kHeld - 1) / (32 * kHeld) * 32;
+        s.lanes = (held + 32 * kHeld - 1) / (32 * kHeld) * 32;
     }
     s.rows = s.lanes < kThreads ? kThreads / s.lanes : 1;
     s.threads = s.rows * s.lanes;
     return s;
 }
 
-// VEC adjacent values of a row as they lie in memory.
-template <typename T, int VEC>
-struct Vec {
-    T v[VEC];
-    __device__ __forceinline__ void load(const T *p)
-    {
-        if constexpr (VEC * sizeof(T) == 32) {
-            reinterpret_cast<uint4 *>(v)[0] = reinterpret_cast<const uint4 *>(p)[0];
-            reinterpret_cast<uint4 *>(v)[1] = reinterpret_cast<const uint4 *>(p)[1];
-        } else if constexpr (VEC * sizeof(T) == 16) {
-            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
-        } else {
-            static_assert(VEC == 1, "whole 16-byte units or single values");
-            v[0] = *p;
-        }
-    }
-    __device__ __forceinline__ void store(T *p) const
-    {
-        if constexpr (VEC * sizeof(T) == 32) {
-            reinterpret_cast<uint4 *>(p)[0] = reinterpret_cast<const uint4 *>(v)[0];
-            reinterpret_cast<uint4 *>(p)[1] = reinterpret_cast<const uint4 *>(v)[1];
-        } else if constexpr (VEC * sizeof(T) == 16) {
-            *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
-        } else {
-            *p = v[0];
-        }
-    }
+// A row's place: its first value's number in the tensor, its columns, and the tensor's values.
+struct Place {
+    int64_t at;
+    int D;
+    int64_t end;
 };
 
-// A thread's part of a row: kHeld / VEC vectors.
-template <typename T, int VEC>
+template <int VEC, bool SHIFTED>
+__device__ __forceinline__ bool over(int c, int D) { return SHIFTED && (c < 0 || c + VEC > D); }   // the vector at c
+
+// A thread's part of a row as it lies in memory: N vectors of VEC values.  SHIFTED: some vectors hang over the row's
+// ends.  Of 32-bit values they are loaded one by one.  Of 16-bit values, two a register, that would make every load wait
+// to be put together; they are loaded like the others (their other values are the neighbouring rows') and mended when
+// they are used, and what would reach over the tensor's end is loaded only then.
+template <typename T, int VEC, bool SHIFTED>
 struct Part {
     static constexpr int N = kHeld / VEC;
-    alignas(16) Vec<T, VEC> vec[N];
-    __device__ __forceinline__ void load(const T *row, const int (&col)[N], int D)
+    static constexpr bool kOneByOne = SHIFTED && sizeof(T) == 4;
+    alignas(16) T v[kHeld];
+    __device__ __forceinline__ void load(const T *p, const Place &at, const int (&col)[N])
     {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (col[j] < D)
-                vec[j].load(row + col[j]);
-            else
+        for (int j = 0; j < N; ++j) {
+            if (kOneByOne && over<VEC, SHIFTED>(col[j], at.D)) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    vec[j].v[i] = T(0.f);
+                    v[j * VEC + i] = (unsigned)(col[j] + i) < (unsigned)at.D ? p[at.at + col[j] + i] : T(0.f);
+                continue;
+            }
+            const bool ok = col[j] < at.D && (!SHIFTED || kOneByOne || at.at + col[j] + VEC <= at.end);
+#pragma unroll
+            for (int i = 0; i < VEC * (int)sizeof(T) / 16; ++i)
+                reinterpret_cast<uint4 *>(v + j * VEC)[i] =
+                    ok ? reinterpret_cast<const uint4 *>(p + at.at + col[j])[i] : make_uint4(0, 0, 0, 0);
+        }
     }
-    __device__ __forceinline__ float at(int i) const { return widen(vec[i / VEC].v[i % VEC]); }
-    __device__ __forceinline__ void set(int i, float f) { vec[i / VEC].v[i % VEC] = narrow<T>(f); }
-    __device__ __forceinline__ void store(T *row, const int (&col)[N], int D) const
+    __device__ __forceinline__ void mend(const T *p, const Place &at, const int (&col)[N])
     {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (col[j] < D)
-                vec[j].store(row + col[j]);
+            if (!kOneByOne && over<VEC, SHIFTED>(col[j], at.D)) {
+                const bool late = at.at + col[j] + VEC > at.end;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if ((unsigned)(col[j] + i) >= (unsigned)at.D)
+                        v[j * VEC + i] = T(0.f);
+                    else if (late)
+                        v[j * VEC + i] = p[at.at + col[j] + i];
+            }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kHeld * (int)sizeof(T) / 16; ++i)
+            reinterpret_cast<uint4 *>(v)[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ float2 pair(int i) const   // values 2 i and 2 i + 1
+    {
+        if constexpr (sizeof(T) == 4)
+            return make_float2(v[2 * i], v[2 * i + 1]);
+        else
+            return widen2<T>(reinterpret_cast<const uint32_t *>(v)[i]);
+    }
+    __device__ __forceinline__ void set(int i, float2 f)
+    {
+        if constexpr (sizeof(T) == 4) {
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        } else {
+            reinterpret_cast<uint32_t *>(v)[i] = narrow2<T>(f);
+        }
+    }
+    __device__ __forceinline__ void store(T *p, const Place &at, const int (&col)[N]) const
+    {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (over<VEC, SHIFTED>(col[j], at.D)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if ((unsigned)(col[j] + i) < (unsigned)at.D)
+                        p[at.at + col[j] + i] = v[j * VEC + i];
+            } else if (col[j] < at.D) {
+#pragma unroll
+                for (int i = 0; i < VEC * (int)sizeof(T) / 16; ++i)
+                    reinterpret_cast<uint4 *>(p + at.at + col[j])[i] = reinterpret_cast<const uint4 *>(v + j * VEC)[i];
+            }
+        }
     }
 };
 
-// The first column of each of a thread's vectors: lane l of a row.
+// The first column of each vector of a row's lane l, for rows that start k values into a 16-byte unit.
 template <int VEC>
-__device__ __forceinline__ void columns(int (&col)[kHeld / VEC], int l, int lanes)
+__device__ __forceinline__ void columns(int (&col)[kHeld / VEC], int l, int lanes, int k)
 {
     constexpr int N = kHeld / VEC;
 #pragma unroll
     for (int j = 0; j < N; ++j)
-        col[j] = (lanes < 32 ? j * lanes + l : (l / 32 * N + j) * 32 + l % 32) * VEC;
+        col[j] = (lanes < 32 ? j * lanes + l : (l / 32 * N + j) * 32 + l % 32) * VEC - k;
 }
 
 template <int VEC>
-__device__ __forceinline__ void load_weights(float (&w)[kHeld], const float *p, const int (&col)[kHeld / VEC], int D)
+__device__ __forceinline__ void load_weights(float2 (&w)[kHeld / 2], const float *p, const int (&col)[kHeld / VEC], int D)
 {
+    auto one = [&](int i) {
+        const int c = col[i / VEC] + i % VEC;
+        return (unsigned)c >= (unsigned)D ? 0.f : p ? p[c] : 1.f;
+    };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int c = col[i / VEC];
-        w[i] = c >= D ? 0.f : p ? p[c + i % VEC] : 1.f;
-    }
+    for (int i = 0; i < kHeld / 2; ++i)
+        w[i] = make_float2(one(2 * i), one(2 * i + 1));
 }
 
-// Sum (and maximum) over the lanes of a row.  `part` has a slot per warp; a CTA's rows come here together, and two
-// calls in a row use different `part`s.
-template <bool MAX>
-__device__ __forceinline__ void reduce_row(float &sum, float &most, int lanes, float2 *part)
+__device__ __forceinline__ float max_lanes(float m, int lanes)   // over groups of so many adjacent lanes
 {
-    for (int m = min(lanes, 32) / 2; m; m >>= 1) {
-        sum += __shfl_xor_sync(~0u, sum, m);
-        if (MAX)
-            most = max_nan(most, __shfl_xor_sync(~0u, most, m));
-    }
+    for (int d = lanes / 2; d; d >>= 1)
+        m = max_nan(m, __shfl_xor_sync(~0u, m, d));
+    return m;
+}
+
+// What a warp tells the other warps of its row: its sum and maximum, and of the groups of 128 columns that it shares
+// with them the maxima of its first (`head`: the columns before its first whole group) and of its last.
+struct Told {
+    float sum, most, head, last;
+};
+
+// Sum (and maximum) over the lanes of a row.  `told` has a slot per warp; a CTA's rows come here together, and two
+// calls in a row use different slots.
+template <bool MAX>
+__device__ __forceinline__ void reduce_row(Told &t, int lanes, Told *told)
+{
+    for (int m = min(lanes, 32) / 2; m; m >>= 1)
+        t.sum += __shfl_xor_sync(~0u, t.sum, m);
+    if (MAX)
+        t.most = max_lanes(t.most, min(lanes, 32));
     if (lanes <= 32)
         return;
     const int warp = threadIdx.x / 32, count = lanes / 32, first = warp / count * count;
     if (threadIdx.x % 32 == 0)
-        part[warp] = make_float2(sum, most);
+        told[warp] = t;
     __syncthreads();
-    float2 t = part[first];
-    sum = t.x;
-    most = t.y;
+    t.sum = told[first].sum;
+    t.most = told[first].most;
     for (int i = 1; i < count; ++i) {
-        t = part[first + i];
-        sum += t.x;
+        t.sum += told[first + i].sum;
         if (MAX)
-            most = max_nan(most, t.y);
+            t.most = max_nan(t.most, told[first + i].most);
     }
 }
 
-// Groups of 128 columns.  Where a row has whole warps, kGroupLanes lanes' kGroupVecs vectors make one up, and a thread's
-// vectors lie in kHeld / VEC / kGroupVecs of them; where rows share a warp, a row has at most two.
+// Maxima of |v| over groups of 128 columns.  Where rows share a warp a row has at most two groups, and a value counts by
+// its column.  Where a row has whole warps, group g is vectors G g .. G g + G - 1 (G = 128 / VEC lanes) but
+// for the k values that the first of them has before the group's first column, plus the k such values of vector
+// G (g + 1): those of a neighbouring vector, or of the next warp's first, which reduce_row carries.
 template <int VEC>
-constexpr int kGroupLanes = VEC >= 4 ? 128 / VEC : 32;
-template <int VEC>
-constexpr int kGroupVecs = VEC >= 4 ? 1 : 4 / VEC;
-constexpr int kGroups = 4;   // most of a thread
+struct Groups {
+    static constexpr int N = kHeld / VEC, G = 128 / VEC;
+    static constexpr int kFew = 2;     // most groups of a row that shares a warp
+    float m[N];                        // by group, or by vector: of the group that holds vector j's own columns
+    float before[N];                   // of the k values of vector j that belong to the group before
 
-template <int VEC>
-__device__ __forceinline__ void group_maxima(float (&m)[kGroups], const float (&v)[kHeld], const int (&col)[kHeld / VEC],
-                                             int lanes)
-{
+    __device__ __forceinline__ void find(const float2 (&v)[kHeld / 2], const int (&col)[N], int lanes, int k, Told &t)
+    {
+        auto size = [&](int i) { return fabsf(i % 2 ? v[i / 2].y : v[i / 2].x); };
+        const int lane = threadIdx.x % 32;
+        if (lanes < 32) {
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k)
-        m[k] = 0.f;
-    if (lanes < 32) {
+            for (int g = 0; g < kFew; ++g) {
+                m[g] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            if (col[i / VEC] < 128)
-                m[0] = max_nan(m[0], fabsf(v[i]));
-            else
-                m[1] = max_nan(m[1], fabsf(v[i]));
+                for (int i = 0; i < kHeld; ++i)
+                    m[g] = (col[i / VEC] + i % VEC) >> 7 == g ? max_nan(m[g], size(i)) : m[g];
+                m[g] = max_lanes(m[g], lanes);
+            }
+            return;
         }
-        for (int d = lanes / 2; d; d >>= 1) {
-            m[0] = max_nan(m[0], __shfl_xor_sync(~0u, m[0], d));
-            m[1] = max_nan(m[1], __shfl_xor_sync(~0u, m[1], d));
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            m[j] = before[j] = 0.f;
+            const bool first = lane % G == 0;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if (first && i < k)
+                    before[j] = max_nan(before[j], size(j * VEC + i));
+                else
+                    m[j] = max_nan(m[j], size(j * VEC + i));
+            }
+            m[j] = max_lanes(m[j], G);
         }
-        return;
+        t.head = before[0];                                   // lane 0's is what counts
+        t.last = __shfl_sync(~0u, m[N - 1], 31);
+        if (k) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float up = __shfl_sync(~0u, before[j], G % 32);            // of this block's second group
+                const float next = j + 1 < N ? __shfl_sync(~0u, before[j + 1 < N ? j + 1 : j], 0) : 0.f;
+                m[j] = max_nan(m[j], G < 32 && lane < G ? up : next);
+            }
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        m[i / VEC / kGroupVecs<VEC>] = max_nan(m[i / VEC / kGroupVecs<VEC>], fabsf(v[i]));
-#pragma unroll
-    for (int k = 0; k < kHeld / VEC / kGroupVecs<VEC>; ++k)
-#pragma unroll
-        for (int d = kGroupLanes<VEC> / 2; d; d >>= 1)
-            m[k] = max_nan(m[k], __shfl_xor_sync(~0u, m[k], d));
-}
 
-// The row's group that a thread's k-th maximum belongs to (past the last for those it does not have).
-template <int VEC>
-__device__ __forceinline__ int group_of(int k, int l, int lanes)
-{
-    constexpr int kOwn = kHeld / VEC / kGroupVecs<VEC>;   // of a thread
-    if (lanes < 32)
-        return k < 2 ? k : 1 << 30;
-    // a warp's 512 columns are four groups: k-th of a thread is a block of 32 / kGroupLanes adjacent ones
-    return k < kOwn ? l / 32 * 4 + k * (32 / kGroupLanes<VEC>) + l % 32 / kGroupLanes<VEC> : 1 << 30;
-}
-
-// VEC adjacent values v * rstd * inv in e4m3.
-template <int VEC>
-__device__ __forceinline__ void put_e4m3(uint8_t *q, const float *v, float rstd, float inv)
-{
-    if constexpr (VEC == 1) {
-        *q = __nv_cvt_float_to_fp8(v[0] * rstd * inv, __NV_SATFINITE, __NV_E4M3);
-    } else {
-        alignas(8) __nv_fp8x2_storage_t b[VEC / 2];
+    // After the reduction: scales from the maxima, written by one lane a group; `m` and `before` become the scales'
+    // reciprocals, of the vectors' own columns and of the k before.
+    __device__ __forceinline__ void scale(float *out, int groups, float rstd, int l, int lanes, int k, const Told *told)
+    {
+        auto of = [&](float most) { return max_nan(most * rstd / kE4m3Max, kScaleMin); };
+        if (lanes < 32) {
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i)
-            b[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * rstd * inv, v[2 * i + 1] * rstd * inv),
-                                            __NV_SATFINITE, __NV_E4M3);
+            for (int g = 0; g < kFew; ++g) {
+                m[g] = of(m[g]);
+                if (l == 0 && g < groups)
+                    out[g] = m[g];
+                m[g] = 1.f / m[g];
+            }
+            return;
+        }
+        const int lane = l % 32, warp = threadIdx.x / 32, in_row = l / 32;
+        float prior = 0.f;   // the group that the warp's first k columns belong to
+        if (k && lanes > 32) {
+            if (in_row + 1 < lanes / 32 && lane >= 32 - G)   // the last group goes on in the next warp
+                m[N - 1] = max_nan(m[N - 1], told[warp + 1].head);
+            if (in_row > 0)
+                prior = max_nan(told[warp - 1].last, told[warp].head);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            m[j] = of(m[j]);
+            const int g = (in_row * N + j) * (32 / G) + lane / G;
+            if (lane % G == 0 && g < groups)
+                out[g] = m[j];
+            m[j] = 1.f / m[j];
+        }
+        if (k) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float down = __shfl_sync(~0u, m[j], 0);   // first group of this block
+                const float back = j ? __shfl_sync(~0u, m[j ? j - 1 : 0], 31) : 1.f / of(prior);   // last before it
+                before[j] = lane >= G ? down : back;
+            }
+        }
+    }
+    __device__ __forceinline__ float inverse(int i, const int (&col)[N], int lanes, int k) const   // for value i
+    {
+        if (lanes < 32)
+            return col[i / VEC] + i % VEC < 128 ? m[0] : m[1];
+        return i % VEC < k && threadIdx.x % G == 0 ? before[i / VEC] : m[i / VEC];
+    }
+};
+
+// A vector of e4m3 values.
+template <int VEC, bool SHIFTED>
+__device__ __forceinline__ void put_e4m3(uint8_t *p, const Place &at, int c, const float2 *v)
+{
+    alignas(8) __nv_fp8x2_storage_t b[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i)
+        b[i] = __nv_cvt_float2_to_fp8x2(v[i], __NV_SATFINITE, __NV_E4M3);
+    if (over<VEC, SHIFTED>(c, at.D)) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if ((unsigned)(c + i) < (unsigned)at.D)
+                p[at.at + c + i] = reinterpret_cast<const uint8_t *>(b)[i];
+    } else if (c < at.D) {
         if constexpr (VEC == 8)
-            *reinterpret_cast<uint2 *>(q) = *reinterpret_cast<const uint2 *>(b);
+            *reinterpret_cast<uint2 *>(p + at.at + c) = *reinterpret_cast<const uint2 *>(b);
         else
-            *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(b);
+            *reinterpret_cast<uint32_t *>(p + at.at + c) = *reinterpret_cast<const uint32_t *>(b);
     }
 }
 
-template <typename Tx, typename Tr, int VEC, bool QUANT>
-__global__ void __launch_bounds__(512) norm_fwd_rows(NormArgs a, Split sp)
+enum Quant { kPlain, kByRow, kByGroup };
+
+template <typename Tx, typename Tr, Quant Q, bool SHIFTED>
+__global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) norm_fwd_rows(NormArgs a, Split sp)
 {
-    constexpr int N = kHeld / VEC;
-    __shared__ float2 part[2][16];
-    const int l = threadIdx.x % sp.lanes, D = a.D;
-    int col[N];
-    columns<VEC>(col, l, sp.lanes);
+    constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
+    __shared__ Told told[2][16];
+    const int l = threadIdx.x % sp.lanes;
+    const Tx *x_in = static_cast<const Tx *>(a.x);
+    const Tr *res_in = static_cast<const Tr *>(a.res);
     const int64_t stride = (int64_t)gridDim.x * sp.rows;
     int64_t row = (int64_t)blockIdx.x * sp.rows + threadIdx.x / sp.lanes;
-    Part<Tx, VEC> x;
-    Part<Tr, VEC> res;
+    const int k = SHIFTED ? (int)(row * a.D % VEC) : 0;
+    Place at = {row * a.D, a.D, a.rows * a.D};
+    int col[N];
+    columns<VEC>(col, l, sp.lanes, k);
+    Part<Tx, VEC, SHIFTED> x;
+    Part<Tr, VEC, SHIFTED> res;
+    res.zero();
     auto fetch = [&](int64_t r) {
         if (r < a.rows) {
-            x.load(static_cast<const Tx *>(a.x) + r * D, col, D);
-            if (a.res)
-                res.load(static_cast<const Tr *>(a.res) + r * D, col, D);
+            const Place to = {r * a.D, a.D, at.end};
+            x.load(x_in, to, col);
+            if (res_in)
+                res.load(res_in, to, col);
+        } else {
+            x.zero();
         }
     };
     fetch(row);
-    float w[kHeld];
-    load_weights<VEC>(w, a.w, col, D);
+    float2 w[kHeld / 2];
+    load_weights<VEC>(w, a.w, col, a.D);
+    const float part = 1.f / a.D;
     // every thread of the CTA takes the same number of turns (they meet in the reduction)
-    for (int64_t first = (int64_t)blockIdx.x * sp.rows, turn = 0; first < a.rows; first += stride, row += stride, ++turn) {
+    for (int64_t first = (int64_t)blockIdx.x * sp.rows, turn = 0; first < a.rows; first += stride, ++turn) {
         const bool on = row < a.rows;
-        float v[kHeld], sum = 0.f, most = 0.f, most_of[kGroups];
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            v[i] = x.at(i);
-            if (a.res)
-                v[i] += res.at(i);
-            sum = fmaf(v[i], v[i], sum);
+        at.at = row * a.D;
+        if (SHIFTED && on) {
+            x.mend(x_in, at, col);
+            if (res_in)
+                res.mend(res_in, at, col);
         }
+        float2 v[kHeld / 2], sq = make_float2(0.f, 0.f);
+        Told t = {};
+#pragma unroll
+        for (int i = 0; i < kHeld / 2; ++i) {
+            v[i] = add2(x.pair(i), res.pair(i));
+            sq = fma2(v[i], v[i], sq);
+        }
+        t.sum = sq.x + sq.y;
         if (on && a.s) {
-            Part<Tr, VEC> s;
+            Part<Tr, VEC, SHIFTED> s;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
+            for (int i = 0; i < kHeld / 2; ++i)
                 s.set(i, v[i]);
-            s.store(static_cast<Tr *>(a.s) + row * D, col, D);
+            s.store(static_cast<Tr *>(a.s), at, col);
         }
-        fetch(row + stride);
+        row += stride;
+        fetch(row);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            v[i] *= w[i];
-            if (QUANT)
-                most = max_nan(most, fabsf(v[i]));
+        for (int i = 0; i < kHeld / 2; ++i) {
+            v[i] = mul2(v[i], w[i]);
+            if (Q == kByRow)
+                t.most = max_nan(t.most, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
         }
-        if (QUANT && a.group)
-            group_maxima<VEC>(most_of, v, col, sp.lanes);
-        reduce_row<QUANT>(sum, most, sp.lanes, part[turn & 1]);
-        const float rstd = rsqrtf(sum / D + a.eps);
-        if (!on)
-            continue;
-        if (a.rstd && l == 0)
-            a.rstd[row] = rstd;
-        if constexpr (!QUANT) {
-            Part<Tx, VEC> y;
+        Groups<VEC> groups;
+        if (Q == kByGroup)
+            groups.find(v, col, sp.lanes, k, t);
+        reduce_row<Q == kByRow>(t, sp.lanes, told[turn & 1]);
+        const float rstd = rsqrtf(t.sum * part + a.eps);
+        if (on && a.rstd && l == 0)
+            a.rstd[row - stride] = rstd;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                y.set(i, v[i] * rstd);
-            y.store(static_cast<Tx *>(a.y) + row * D, col, D);
+        for (int i = 0; i < kHeld / 2; ++i)
+            v[i] = mul2(v[i], make_float2(rstd, rstd));
+        if constexpr (Q == kPlain) {
+            Part<Tx, VEC, SHIFTED> y;
+#pragma unroll
+            for (int i = 0; i < kHeld / 2; ++i)
+                y.set(i, v[i]);
+            if (on)
+                y.store(static_cast<Tx *>(a.y), at, col);
         } else {
-            const int groups = a.group ? (D + 127) / 128 : 1;
+            if constexpr (Q == kByRow) {
+                const float scale = max_nan(t.most * rstd / kE4m3Max, kScaleMin), inv = 1.f / scale;
+                if (on && l == 0)
+                    a.scales[row - stride] = scale;
 #pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
-                most_of[k] = max_nan((a.group ? most_of[k] : most) * rstd / kE4m3Max, kScaleMin);
-                const int g = a.group ? group_of<VEC>(k, l, sp.lanes) : 0;
-                const bool lead = a.group ? (sp.lanes < 32 ? l == 0 : l % kGroupLanes<VEC> == 0) : l == 0 && k == 0;
-                if (lead && g < groups)
-                    a.scales[row * groups + g] = most_of[k];
-            }
+                for (int i = 0; i < kHeld / 2; ++i)
+                    v[i] = mul2(v[i], make_float2(inv, inv));
+            } else {
+                const int count = (a.D + 127) / 128;
+                groups.scale(a.scales + (on ? (row - stride) * count : 0), on ? count : 0, rstd, l, sp.lanes, k, told[turn & 1]);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                // a vector lies in one group: by its columns where a row shares a warp, else by its number
-                const float scale = !a.group ? most_of[0]
-                                    : sp.lanes < 32 ? (col[j] < 128 ? most_of[0] : most_of[1])
-                                                    : most_of[j / kGroupVecs<VEC>];
-                if (col[j] < D)
-                    put_e4m3<VEC>(static_cast<uint8_t *>(a.y) + row * D + col[j], v + j * VEC, rstd, 1.f / scale);
+                for (int i = 0; i < kHeld / 2; ++i)
+                    v[i] = mul2(v[i], make_float2(groups.inverse(2 * i, col, sp.lanes, k),
+                                                  groups.inverse(2 * i + 1, col, sp.lanes, k)));
             }
+            if (on)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    put_e4m3<VEC, SHIFTED>(static_cast<uint8_t *>(a.y), at, col[j], v + j * VEC / 2);
         }
     }
 }
 
-template <typename Tx, typename Tr, int VEC>
+template <typename Tx, typename Tr, bool SHIFTED>
 __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
 {
-    constexpr int N = kHeld / VEC;
-    constexpr bool kEarly = VEC == 8 && sizeof(Tr) == 2;   // registers for the next row beside the present one
-    __shared__ float2 part[2][16];
+    constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
+    constexpr bool kEarly = sizeof(Tr) == 2;   // registers for the next row beside the present one
+    __shared__ Told told[2][16];
     __shared__ float acc[2048];   // a CTA of several rows has at most so many columns
     const int l = threadIdx.x % sp.lanes, D = a.D;
-    int col[N];
-    columns<VEC>(col, l, sp.lanes);
+    const Tr *s_in = static_cast<const Tr *>(a.s_in), *ds_in = static_cast<const Tr *>(a.ds);
+    const Tx *dy_in = static_cast<const Tx *>(a.dy);
     const int64_t stride = (int64_t)gridDim.x * sp.rows;
     int64_t row = (int64_t)blockIdx.x * sp.rows + threadIdx.x / sp.lanes;
-    Part<Tr, VEC> s, ds;
-    Part<Tx, VEC> dy;
+    Place at = {row * D, D, a.rows * D};
+    int col[N];
+    columns<VEC>(col, l, sp.lanes, SHIFTED ? (int)(row * D % VEC) : 0);
+    Part<Tr, VEC, SHIFTED> s, ds;
+    Part<Tx, VEC, SHIFTED> dy;
     float rstd = 0.f;
+    ds.zero();
     auto fetch = [&](int64_t r) {
         if (r < a.rows) {
-            s.load(static_cast<const Tr *>(a.s_in) + r * D, col, D);
-            dy.load(static_cast<const Tx *>(a.dy) + r * D, col, D);
-            if (a.ds)
-                ds.load(static_cast<const Tr *>(a.ds) + r * D, col, D);
+            const Place to = {r * D, D, at.end};
+            s.load(s_in, to, col);
+            dy.load(dy_in, to, col);
+            if (ds_in)
+                ds.load(ds_in, to, col);
             rstd = a.rstd_in[r];
+        } else {
+            s.zero();
+            dy.zero();
         }
     };
     if (kEarly)
         fetch(row);
-    float w[kHeld], dw[kHeld];
+    float2 w[kHeld / 2], dw[kHeld / 2];
     load_weights<VEC>(w, a.w, col, D);
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        dw[i] = 0.f;
+    for (int i = 0; i < kHeld / 2; ++i)
+        dw[i] = make_float2(0.f, 0.f);
+    const float part = 1.f / D;
     for (int64_t first = (int64_t)blockIdx.x * sp.rows, turn = 0; first < a.rows; first += stride, row += stride, ++turn) {
-        const bool on = row < a.rows;
         if (!kEarly)
             fetch(row);
+        const bool on = row < a.rows;
+        at.at = row * D;
+        if (SHIFTED && on) {
+            s.mend(s_in, at, col);
+            dy.mend(dy_in, at, col);
+            if (ds_in)
+                ds.mend(ds_in, at, col);
+        }
         const float r = rstd;
-        float n[kHeld], g[kHeld], up[kHeld], c = 0.f, none = 0.f;
+        float2 n[kHeld / 2], g[kHeld / 2], up[kHeld / 2], c = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            n[i] = s.at(i) * r;
-            g[i] = dy.at(i);
-            up[i] = a.ds ? ds.at(i) : 0.f;
-            if (on)
-                dw[i] = fmaf(g[i], n[i], dw[i]);
-            g[i] *= w[i];
-            c = fmaf(g[i], n[i], c);
+        for (int i = 0; i < kHeld / 2; ++i) {
+            n[i] = mul2(s.pair(i), make_float2(r, r));
+            g[i] = dy.pair(i);
+            up[i] = ds.pair(i);
+            dw[i] = fma2(g[i], n[i], dw[i]);
+            g[i] = mul2(g[i], w[i]);
+            c = fma2(g[i], n[i], c);
         }
         if (kEarly)
             fetch(row + stride);
-        reduce_row<false>(c, none, sp.lanes, part[turn & 1]);
-        if (!on)
-            continue;
-        c /= D;
+        Told t = {};
+        t.sum = c.x + c.y;
+        reduce_row<false>(t, sp.lanes, told[turn & 1]);
+        const float mean = -t.sum * part;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            up[i] = fmaf(r, g[i] - n[i] * c, up[i]);
-        if (a.dx) {
-            Part<Tx, VEC> out;
+        for (int i = 0; i < kHeld / 2; ++i)
+            up[i] = fma2(make_float2(r, r), fma2(n[i], make_float2(mean, mean), g[i]), up[i]);
+        if (on && a.dx) {
+            Part<Tx, VEC, SHIFTED> out;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
+            for (int i = 0; i < kHeld / 2; ++i)
                 out.set(i, up[i]);
-            out.store(static_cast<Tx *>(a.dx) + row * D, col, D);
+            out.store(static_cast<Tx *>(a.dx), at, col);
         }
-        if (a.dres) {
-            Part<Tr, VEC> out;
+        if (on && a.dres) {
+            Part<Tr, VEC, SHIFTED> out;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
+            for (int i = 0; i < kHeld / 2; ++i)
                 out.set(i, up[i]);
-            out.store(static_cast<Tr *>(a.dres) + row * D, col, D);
+            out.store(static_cast<Tr *>(a.dres), at, col);
         }
     }
     if (!a.dw)
         return;
-    // the CTA's sum of dw: over the rows of a warp, then over the warps in order
-    for (int m = sp.lanes; m < 32; m *= 2)
+    // the CTA's sum of dw: over the rows of a warp at once where they hold the same columns, then one by one
+    const bool same = !SHIFTED && sp.lanes < 32;
+    if (same)
+        for (int m = sp.lanes; m < 32; m *= 2)
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            dw[i] += __shfl_xor_sync(~0u, dw[i], m);
+            for (int i = 0; i < kHeld / 2; ++i)
+                dw[i] = add2(dw[i], make_float2(__shfl_xor_sync(~0u, dw[i].x, m), __shfl_xor_sync(~0u, dw[i].y, m)));
     float *out = a.part + (size_t)blockIdx.x * D;
-    const int wide = max(sp.lanes, 32), turns = sp.threads / wide, mine = threadIdx.x / wide;
-    const bool lead = threadIdx.x % wide < sp.lanes;
+    const int width = same ? 32 : sp.lanes, turns = sp.threads / width, mine = threadIdx.x / width;
+    const bool lead = threadIdx.x % width < sp.lanes;
     for (int t = 0; t < turns; ++t) {
         if (t == mine && lead)
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int d = col[i / VEC] + i % VEC;
-                if (col[i / VEC] >= D)
+                if ((unsigned)d >= (unsigned)D)
                     continue;
-                const float sum = t > 0 ? acc[d] + dw[i] : dw[i];
+                const float v = i % 2 ? dw[i / 2].y : dw[i / 2].x, sum = t > 0 ? acc[d] + v : v;
                 if (t == turns - 1)
                     out[d] = sum;
                 else
@@ -521,31 +664,48 @@ cudaError_t by_norm_types(int dtype, bool res_f32, F f)
     return res_f32 ? f((__half *)0, (float *)0) : f((__half *)0, (__half *)0);
 }
 
-// Persistent CTAs: as many as an SM holds of them, or one for each of its rows where there are fewer.
-template <typename K>
-int grid_of(K kernel, int64_t rows, const Split &sp)
+// Persistent CTAs, `per_sm` of them, or one for each of its rows where there are fewer.  Where a CTA takes several
+// turns its rows stay a multiple of 8 apart, so that they keep their shift.
+int grid_of(int64_t rows, const Split &sp, int per_sm)
 {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, sp.threads, 0) != cudaSuccess || per_sm < 1)
-        per_sm = 1;
-    return (int)std::min<int64_t>((rows + sp.rows - 1) / sp.rows, (int64_t)per_sm * sm_count());
+    const int64_t need = (rows + sp.rows - 1) / sp.rows, most = (int64_t)per_sm * sm_count() / 8 * 8;
+    return (int)std::min(need, most);
 }
 
-template <typename Tx, typename Tr, int VEC, bool QUANT>
+template <typename Tx, typename Tr, Quant Q, bool SHIFTED>
 cudaError_t fwd_rows(const NormArgs &a, cudaStream_t s)
 {
-    const Split sp = split_of(a.D);
-    auto kernel = norm_fwd_rows<Tx, Tr, VEC, QUANT>;
-    kernel<<<grid_of(kernel, a.rows, sp), sp.threads, 0, s>>>(a, sp);
+    auto kernel = norm_fwd_rows<Tx, Tr, Q, SHIFTED>;
+    const Split sp = split_of(a.D, 16 / sizeof(Tx));
+    static std::atomic<int> fit[17];   // CTAs an SM holds, by warps of a CTA (0: not asked yet)
+    std::atomic<int> &known = fit[sp.threads / 32];
+    int per_sm = known.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, sp.threads, 0) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        known.store(per_sm, std::memory_order_relaxed);
+    }
+    kernel<<<grid_of(a.rows, sp, per_sm), sp.threads, 0, s>>>(a, sp);
     return cudaGetLastError();
 }
 
+template <typename Tx, typename Tr, Quant Q>
+cudaError_t fwd(const NormArgs &a, cudaStream_t s)
+{
+    return a.D % (16 / (int)sizeof(Tx)) ? fwd_rows<Tx, Tr, Q, true>(a, s) : fwd_rows<Tx, Tr, Q, false>(a, s);
+}
+
+bool wide(int D, int vec) { return held_columns(D, vec) > kMaxHeld; }
+
 }  // namespace
 
-int norm_bwd_ctas(int64_t rows, int D)
+int norm_bwd_ctas(int64_t rows, int D, int dtype)
 {
-    const Split sp = split_of(D);
-    return (int)std::min<int64_t>(D > kMaxHeld ? rows : (rows + sp.rows - 1) / sp.rows, 2 * sm_count());
+    const int vec = dtype == GLA_F32 ? 4 : 8;
+    if (wide(D, vec))
+        return (int)std::min<int64_t>(rows, 2 * sm_count());
+    const Split sp = split_of(D, vec);
+    return grid_of(rows, sp, std::max(1, 512 / sp.threads));   // 128 registers a thread
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s)
@@ -553,14 +713,12 @@ cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
     return by_norm_types(dtype, res_f32, [&](auto x, auto r) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(r)> Tr;
-        if (a.D > kMaxHeld) {
+        if (wide(a.D, 16 / sizeof(Tx))) {
             norm_fwd_wide<Tx, Tr><<<(unsigned)std::min<int64_t>(a.rows, 16 * sm_count()), kThreads, 0, s>>>(a);
             return cudaGetLastError();
         }
-        constexpr int VEC = 16 / sizeof(Tx);
-        if (a.D % VEC == 0)   // rows start on 16-byte units
-            return a.scales ? fwd_rows<Tx, Tr, VEC, true>(a, s) : fwd_rows<Tx, Tr, VEC, false>(a, s);
-        return a.scales ? fwd_rows<Tx, Tr, 1, true>(a, s) : fwd_rows<Tx, Tr, 1, false>(a, s);
+        return !a.scales ? fwd<Tx, Tr, kPlain>(a, s)
+               : a.group ? fwd<Tx, Tr, kByGroup>(a, s) : fwd<Tx, Tr, kByRow>(a, s);
     });
 }
 
@@ -569,14 +727,13 @@ cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
     return by_norm_types(dtype, res_f32, [&](auto x, auto r) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(r)> Tr;
-        constexpr int VEC = 16 / sizeof(Tx);
-        const Split sp = split_of(a.D);
-        if (a.D > kMaxHeld)
+        const Split sp = split_of(a.D, 16 / sizeof(Tx));
+        if (wide(a.D, 16 / sizeof(Tx)))
             norm_bwd_wide<Tx, Tr><<<a.ctas, kThreads, 0, s>>>(a);
-        else if (a.D % VEC == 0)
-            norm_bwd_rows<Tx, Tr, VEC><<<a.ctas, sp.threads, 0, s>>>(a, sp);
+        else if (a.D % (16 / (int)sizeof(Tx)))
+            norm_bwd_rows<Tx, Tr, true><<<a.ctas, sp.threads, 0, s>>>(a, sp);
         else
-            norm_bwd_rows<Tx, Tr, 1><<<a.ctas, sp.threads, 0, s>>>(a, sp);
+            norm_bwd_rows<Tx, Tr, false><<<a.ctas, sp.threads, 0, s>>>(a, sp);
         return cudaGetLastError();
     });
 }

@@ -73,34 +73,6 @@ __device__ __forceinline__ bool sequence_rows(const ScanArgs &a, int n, int64_t 
     return ok;
 }
 
-// Two adjacent 16-bit values in a word.
-template <typename T>
-__device__ __forceinline__ float2 widen2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w)
-{
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 widen2<__half>(uint32_t w)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t narrow2(float2 v);
-template <>
-__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float2 v)
-{
-    const __nv_bfloat162 b = __float22bfloat162_rn(v);
-    return *reinterpret_cast<const uint32_t *>(&b);
-}
-template <>
-__device__ __forceinline__ uint32_t narrow2<__half>(float2 v)
-{
-    const __half2 b = __float22half2_rn(v);
-    return *reinterpret_cast<const uint32_t *>(&b);
-}
-
 // One R x kCols tile of a row-strided tensor in shared memory.  Rows whose bytes start and step in 16-byte units
 // (ALIGNED) lie as they are; others are copied from the 16-byte unit that holds their first byte, so every row has a
 // shift of its own.
@@ -216,29 +188,6 @@ struct Pair {
     }
 };
 
-// Two channels at a time: one instruction for both (the same roundings as one by one).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 __device__ __forceinline__ float2 decay2(float2 g) { return make_float2(decay(g.x), decay(g.y)); }
 
 // An affine map h -> A h + H of a lane's two channels.

@@ -426,6 +426,15 @@ def test_norm_backward(B, rows, D, types):
     assert dx.dtype == tx and dres.dtype == tr
 
 
+@pytest.mark.parametrize("types", [(TB, TB), (TH, T32), (T32, T32)], ids=lambda t: "-".join(KIND[x] for x in t))
+@pytest.mark.parametrize("rows,D", [(30001, 19), (9001, 130), (5001, 257), (3001, 517), (2001, 1001), (901, 2049), (701, 8001),
+                                    (700, 8186)])
+def test_norm_shifted_rows(B, rows, D, types):
+    """Rows that start anywhere in a 16-byte unit, several turns of the grid, every output."""
+    test_norm_forward(B, rows, D, types)
+    test_norm_backward(B, rows, D, types)
+
+
 @pytest.mark.parametrize("rows,D", [(20011, 136), (3001, 1024)])
 def test_norm_backward_many_rows(B, rows, D):
     dy, s, w = norm_inputs(TB, TB, rows, D, seed=23)
