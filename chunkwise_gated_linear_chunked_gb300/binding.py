@@ -369,14 +369,18 @@ _STATUS_BYTES = int(_lib.gla_scan_workspace_size())
 _stream_ws: dict = {}
 
 
-def stream_workspace(nbytes: int, device) -> torch.Tensor:
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle on a device, without a Stream object
+_current_device = torch._C._cuda_getDevice
+_capturing = torch.cuda.is_current_stream_capturing
+
+
+def stream_workspace(nbytes: int, device: int) -> torch.Tensor:
     """A zeroed device workspace of at least ``nbytes``, cached per device and current stream, so that calls on
     different streams never share one.  During a CUDA graph capture it is a fresh tensor instead: the graph zeroes
     it on every replay and owns its memory."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-    key = (device.index, stream)
+    key = (device, _raw_stream(device))
     ws = _stream_ws.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -391,36 +395,48 @@ def _on_stream(fn):
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise GlaError(GLA_ERR_INVALID_ARG, f"{fn.__name__}: the first argument must be a cuda tensor")
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+        if stream is None and first.get_device() == _current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.stream(stream), torch.cuda.device(first.device):
+            return fn(first, *args, **kw)
     return call
 
 
+def _all_like(t, others):
+    """Whether every tensor of ``others`` is contiguous and has t's dtype, shape and device, and t is contiguous."""
+    dtype, shape, device = t.dtype, t.shape, t.get_device()
+    for o in others:
+        if o.dtype is not dtype or o.shape != shape or o.get_device() != device or not o.is_contiguous():
+            return False
+    return t.is_contiguous()
+
+
 def _check(what, name, t, dtype, shape, device):
-    """``t`` is a contiguous tensor of this dtype, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    """``t`` is a contiguous tensor of this dtype and shape on cuda device number ``device``."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must be a contiguous {dtype} tensor of shape "
-                                            f"{tuple(shape)} on {device}")
+                                            f"{tuple(shape)} on cuda:{device}")
 
 
 def _row_stride(what, name, t, shape, device):
     """Elements between consecutive rows of a [..., D] tensor: the channels adjacent, the rows evenly spaced (a
     contiguous tensor, or a column range of one)."""
-    if t.shape != shape or t.device != device:
-        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must have shape {tuple(shape)} on {device}")
+    if t.shape != shape or t.get_device() != device:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must have shape {tuple(shape)} on cuda:{device}")
+    D = shape[-1]
     if t.is_contiguous():
-        return shape[-1]
-    D, ld = shape[-1], t.stride(-2)
-    even = all(t.stride(i) == ld * math.prod(shape[i + 1:-1]) or shape[i] == 1 for i in range(len(shape) - 2))
-    if shape[-2] == 1:   # a single row per sequence: the spacing is the outer dimension's
-        ld = next((t.stride(i) for i in range(len(shape) - 3, -1, -1) if shape[i] > 1), D)
-        even = all(t.stride(i) == ld * math.prod(shape[i + 1:-1]) or shape[i] == 1 for i in range(len(shape) - 2))
-    if (D > 1 and t.stride(-1) != 1) or ld < D or not even:
+        return D
+    # the innermost of the outer dimensions that has more than one row gives the spacing, and the others follow it
+    rows, ld = 1, None
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size > 1:
+            ld = stride if ld is None else ld
+            if stride != ld * rows:
+                ld = -1
+                break
+        rows *= size
+    ld = D if ld is None else ld
+    if (D > 1 and t.stride(-1) != 1) or ld < D:
         raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {name} must have adjacent channels and evenly spaced rows "
                                             f"(a contiguous tensor or a column range of one)")
     return ld
@@ -438,8 +454,8 @@ def _pack(what, shape, cu_seqlens, device):
     if cu_seqlens is None:
         return B, B, T, D
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
-            cu_seqlens.device != device or not cu_seqlens.is_contiguous():
-        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: cu_seqlens must be a contiguous int32 vector on {device}")
+            cu_seqlens.get_device() != device or not cu_seqlens.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: cu_seqlens must be a contiguous int32 vector on cuda:{device}")
     return cu_seqlens.numel() - 1, B, T, D
 
 
@@ -453,7 +469,7 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
     cu_seqlens: int32 [N+1] cuda offsets (B == 1).  out_dtype: x's type (default; fp32 beside an fp32 g) or fp32.
     out: optional [B, T, D] tensor for h.  stream=: the stream to run on.  Returns (h, ht fp32 [N, D] or None).
     """
-    shape, device = x.shape, x.device
+    shape, device = x.shape, x.get_device()
     N, B, T, D = _pack("gla_scan_fwd", shape, cu_seqlens, device)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else g.dtype
@@ -473,7 +489,7 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
         workspace = stream_workspace(_STATUS_BYTES, device)
     rc = _lib.gla_scan_fwd(x.data_ptr(), g.data_ptr(), out.data_ptr(), _at(initial_state), _at(ht), _at(cu_seqlens),
                            N, B, T, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
-                           torch.cuda.current_stream().cuda_stream)
+                           _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_fwd")
     return out, ht
@@ -488,7 +504,7 @@ def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=N
     None.  dx_dtype: x's type (default: g's).  dx, dg: optional tensors to write, which may be column ranges of one
     gradient.  Returns (dx, dg in g's type, dh0 fp32 [N, D] or None).
     """
-    shape, device = g.shape, g.device
+    shape, device = g.shape, g.get_device()
     N, B, T, D = _pack("gla_scan_bwd", shape, cu_seqlens, device)
     if dx_dtype is None:
         dx_dtype = g.dtype if dx is None else dx.dtype
@@ -519,7 +535,7 @@ def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=N
         workspace = stream_workspace(_STATUS_BYTES, device)
     rc = _lib.gla_scan_bwd(g.data_ptr(), h.data_ptr(), dh.data_ptr(), _at(initial_state), _at(dht), dx.data_ptr(),
                            dg.data_ptr(), _at(dh0), _at(cu_seqlens), N, B, T, D, ldg, lddx, lddg, code,
-                           workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_bwd")
     return dx, dg, dh0
@@ -534,7 +550,7 @@ def _pool(what, state, state_out, slots, B, tail, device):
     _check(what, "state", state, torch.float32, (S, *tail), device)
     if state_out is None:
         state_out = state
-    else:
+    elif not _all_like(state, (state_out,)):
         _check(what, "state_out", state_out, torch.float32, (S, *tail), device)
     if slots is not None:
         _check(what, "slots", slots, torch.int32, (B,), device)
@@ -551,7 +567,7 @@ def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace
     """
     if x.dim() != 2:
         raise GlaError(GLA_ERR_INVALID_ARG, f"gla_scan_step: x must be [B, D], got shape {tuple(x.shape)}")
-    shape, device = x.shape, x.device
+    shape, device = x.shape, x.get_device()
     B, D = shape
     if out_dtype is None:
         out_dtype = g.dtype
@@ -566,7 +582,7 @@ def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace
         workspace = stream_workspace(_STATUS_BYTES, device)
     rc = _lib.gla_scan_step(x.data_ptr(), g.data_ptr(), h.data_ptr(), state.data_ptr(), state_out.data_ptr(),
                             _at(slots), B, S, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
-                            torch.cuda.current_stream().cuda_stream)
+                            _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_step")
     return h
@@ -582,17 +598,18 @@ def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtyp
     """
     if q.dim() != 3 or v.dim() != 3:
         raise GlaError(GLA_ERR_INVALID_ARG, "gla_step: q, k, g must be [B, H, K] and v [B, H, V]")
-    device = q.device
+    device = q.get_device()
     B, H, K = q.shape
     V = v.shape[-1]
     out_dtype = out_dtype or torch.float32
     code = SCAN_CODE.get((q.dtype, g.dtype, out_dtype))
     if code is None:
         raise GlaError(GLA_ERR_UNSUPPORTED, f"gla_step dtypes q {q.dtype}, g {g.dtype} -> {out_dtype}")
-    _check("gla_step", "q", q, q.dtype, (B, H, K), device)
-    _check("gla_step", "k", k, q.dtype, (B, H, K), device)
-    _check("gla_step", "v", v, q.dtype, (B, H, V), device)
-    _check("gla_step", "g", g, g.dtype, (B, H, K), device)
+    if not (V == K and _all_like(q, (k, v, g))):   # the usual call at once, else one by one
+        _check("gla_step", "q", q, q.dtype, (B, H, K), device)
+        _check("gla_step", "k", k, q.dtype, (B, H, K), device)
+        _check("gla_step", "v", v, q.dtype, (B, H, V), device)
+        _check("gla_step", "g", g, g.dtype, (B, H, K), device)
     S, state_out = _pool("gla_step", state, state_out, slots, B, (H, K, V), device)
     o = torch.empty(B, H, V, dtype=out_dtype, device=device)
     if workspace is None:
@@ -600,7 +617,7 @@ def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtyp
     rc = _lib.gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), o.data_ptr(),
                        K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B, S,
                        H, K, V, code, workspace.data_ptr(), workspace.numel(),
-                       torch.cuda.current_stream().cuda_stream)
+                       _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_step")
     return o
@@ -617,9 +634,9 @@ def _norm_args(what, x, residual, weight, stream_dtype):
     if D == 0:
         raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: no columns")
     if residual is not None:
-        _check(what, "residual", residual, stream_dtype, x.shape, x.device)
+        _check(what, "residual", residual, stream_dtype, x.shape, x.get_device())
     if weight is not None:
-        _check(what, "weight", weight, torch.float32, (D,), x.device)
+        _check(what, "weight", weight, torch.float32, (D,), x.get_device())
     return x.numel() // D, D, code if stream_dtype == x.dtype else code | GLA_RES_F32
 
 
@@ -630,13 +647,13 @@ def norm_fwd(x, residual=None, weight=None, eps=1e-6):
     x: contiguous [..., D] fp32 / bf16 / fp16; residual: like x, or fp32; weight: fp32 [D] or None.
     Returns (y in x's type, s in the residual's type (x itself without a residual), rstd fp32 [...]).
     """
-    stream_dtype = x.dtype if residual is None else residual.dtype
+    stream_dtype, device = x.dtype if residual is None else residual.dtype, x.get_device()
     rows, D, code = _norm_args("gla_norm_fwd", x, residual, weight, stream_dtype)
     y = torch.empty_like(x)
     s = None if residual is None else torch.empty_like(residual)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     rc = _lib.gla_norm_fwd(x.data_ptr(), _at(residual), _at(weight), y.data_ptr(), _at(s), rstd.data_ptr(), rows, D,
-                           eps, code, torch.cuda.current_stream().cuda_stream)
+                           eps, code, _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_norm_fwd")
     return y, x if s is None else s, rstd
@@ -646,15 +663,15 @@ def norm_fwd(x, residual=None, weight=None, eps=1e-6):
 def norm_quant_fwd(x, residual=None, weight=None, eps=1e-6, group=0):
     """``norm_fwd`` with its output in 8 bits: y is q times its scale.  group: columns of one scale, 128, or 0 for
     one scale per row.  Returns (q float8_e4m3fn [..., D], scales fp32 [..., ceil(D / group)], s, rstd)."""
-    stream_dtype = x.dtype if residual is None else residual.dtype
+    stream_dtype, device = x.dtype if residual is None else residual.dtype, x.get_device()
     rows, D, code = _norm_args("gla_norm_quant_fwd", x, residual, weight, stream_dtype)
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=device)
     groups = -(-D // group) if group > 0 else 1
-    scales = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=x.device)
+    scales = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=device)
     s = None if residual is None else torch.empty_like(residual)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     rc = _lib.gla_norm_quant_fwd(x.data_ptr(), _at(residual), _at(weight), q.data_ptr(), scales.data_ptr(), _at(s),
-                                 rstd.data_ptr(), rows, D, eps, group, code, torch.cuda.current_stream().cuda_stream)
+                                 rstd.data_ptr(), rows, D, eps, group, code, _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_norm_quant_fwd")
     return q, scales, x if s is None else s, rstd
@@ -668,17 +685,18 @@ def norm_bwd(s, rstd, dy, weight=None, ds=None, want_dw=True, workspace=None):
     first two are one tensor when the types are the same.  ``want_dw=False`` skips dw (also None without a weight).
     """
     rows, D, code = _norm_args("gla_norm_bwd", dy, s, weight, s.dtype)
+    device = s.get_device()
     if ds is not None:
-        _check("gla_norm_bwd", "ds", ds, s.dtype, s.shape, s.device)
-    _check("gla_norm_bwd", "rstd", rstd, torch.float32, s.shape[:-1], s.device)
+        _check("gla_norm_bwd", "ds", ds, s.dtype, s.shape, device)
+    _check("gla_norm_bwd", "rstd", rstd, torch.float32, s.shape[:-1], device)
     dx = torch.empty_like(dy)
     dres = dx if s.dtype == dy.dtype else torch.empty_like(s)
-    dw = torch.empty(D, dtype=torch.float32, device=s.device) if want_dw and weight is not None else None
+    dw = torch.empty(D, dtype=torch.float32, device=device) if want_dw and weight is not None else None
     if workspace is None:
-        workspace = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(rows, D)), s.device)
+        workspace = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(rows, D)), device)
     rc = _lib.gla_norm_bwd(s.data_ptr(), rstd.data_ptr(), _at(weight), dy.data_ptr(), _at(ds), dx.data_ptr(),
                            None if dres is dx else dres.data_ptr(), _at(dw), rows, D, code, workspace.data_ptr(),
-                           workspace.numel(), torch.cuda.current_stream().cuda_stream)
+                           workspace.numel(), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_norm_bwd")
     return dx, dres, dw
