@@ -388,6 +388,20 @@ def stream_workspace(nbytes: int, device: int) -> torch.Tensor:
     return ws
 
 
+_status_ws: dict = {}
+
+
+def _status_workspace(device: int) -> torch.Tensor:
+    """The workspace of calls that keep nothing but the status word there, one per device: calls on any stream may
+    share it (they write it only to report an error)."""
+    ws = _status_ws.get(device)
+    if ws is None:
+        ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=device)
+        if not _capturing():   # a graph owns what is allocated during its capture
+            _status_ws[device] = ws
+    return ws
+
+
 def _on_stream(fn):
     """Runs a call on its ``stream`` argument (or the current stream) of its first tensor's device: the outputs and
     the workspace are then allocated on the stream that the kernels run on.  The inputs are the caller's to order."""
@@ -486,7 +500,7 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
         _check("gla_scan_fwd", "out", out, out_dtype, shape, device)
     ht = torch.empty(N, D, dtype=torch.float32, device=device) if output_final_state else None
     if workspace is None:
-        workspace = stream_workspace(_STATUS_BYTES, device)
+        workspace = _status_workspace(device)
     rc = _lib.gla_scan_fwd(x.data_ptr(), g.data_ptr(), out.data_ptr(), _at(initial_state), _at(ht), _at(cu_seqlens),
                            N, B, T, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
                            _raw_stream(device))
@@ -532,7 +546,7 @@ def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=N
         lddg = _row_stride("gla_scan_bwd", "dg", dg, shape, device)
     dh0 = torch.empty(N, D, dtype=torch.float32, device=device) if want_dh0 else None
     if workspace is None:
-        workspace = stream_workspace(_STATUS_BYTES, device)
+        workspace = _status_workspace(device)
     rc = _lib.gla_scan_bwd(g.data_ptr(), h.data_ptr(), dh.data_ptr(), _at(initial_state), _at(dht), dx.data_ptr(),
                            dg.data_ptr(), _at(dh0), _at(cu_seqlens), N, B, T, D, ldg, lddx, lddg, code,
                            workspace.data_ptr(), workspace.numel(), _raw_stream(device))
@@ -579,7 +593,7 @@ def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace
     S, state_out = _pool("gla_scan_step", state, state_out, slots, B, (D,), device)
     h = torch.empty(shape, dtype=out_dtype, device=device)
     if workspace is None:
-        workspace = stream_workspace(_STATUS_BYTES, device)
+        workspace = _status_workspace(device)
     rc = _lib.gla_scan_step(x.data_ptr(), g.data_ptr(), h.data_ptr(), state.data_ptr(), state_out.data_ptr(),
                             _at(slots), B, S, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
                             _raw_stream(device))
@@ -613,7 +627,7 @@ def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtyp
     S, state_out = _pool("gla_step", state, state_out, slots, B, (H, K, V), device)
     o = torch.empty(B, H, V, dtype=out_dtype, device=device)
     if workspace is None:
-        workspace = stream_workspace(_STATUS_BYTES, device)
+        workspace = _status_workspace(device)
     rc = _lib.gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), o.data_ptr(),
                        K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B, S,
                        H, K, V, code, workspace.data_ptr(), workspace.numel(),

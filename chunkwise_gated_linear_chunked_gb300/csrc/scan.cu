@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kCols = 64;       // channels of a CTA: two per lane
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 12;   // 65536 rows of 512 channels: 4 CTAs 174 us, 8: 96, 12: 73, but 14: 129 and 16: 115
 constexpr int kSlots = 2;       // tiles whose maps are in shared memory at a time
 
 __device__ __forceinline__ uint32_t cluster_rank()
