@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libgla (``include/gla.h``): argument marshalling only.
+"""Thin ctypes binding of libgla (``include/gla.h``): argument marshalling only.  The layer operators' usual calls
+take a shorter way to the same C functions, through the ``_calls`` module.
 
 Every step of the forward runs in libgla's CUDA kernels; torch supplies device memory and streams.  There is
 no CPU fallback: if ``_build/libgla.so`` is missing the import fails loudly (run
@@ -8,13 +9,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import threading
 
 import torch
 
-from .build import LIB
+from .build import LIB, calls_lib
 
 GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_ALIGNMENT, GLA_ERR_WORKSPACE, GLA_ERR_CUDA, \
     GLA_ERR_TIMEOUT, GLA_ERR_RANGE = range(8)
@@ -87,6 +89,21 @@ _lib.gla_norm_bwd.argtypes = [_p] * 8 + [_i64, _i, _i, _p, _sz, _p]
 _lib.gla_norm_bwd.restype = _i
 _lib.gla_norm_bwd_workspace_size.argtypes = [_i64, _i]
 _lib.gla_norm_bwd_workspace_size.restype = _sz
+
+
+
+
+def _load_calls():
+    path = calls_lib()
+    if not os.path.exists(path):
+        raise ImportError(f"_calls not built ({path}); call chunkwise_gated_linear_chunked_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_calls", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_calls = _load_calls()
 
 
 class GlaError(RuntimeError):
@@ -399,6 +416,7 @@ def _status_workspace(device: int) -> torch.Tensor:
         ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=device)
         if not _capturing():   # a graph owns what is allocated during its capture
             _status_ws[device] = ws
+            _calls.use_status(device, ws.data_ptr())
     return ws
 
 
@@ -406,9 +424,9 @@ def _on_stream(fn):
     """Runs a call on its ``stream`` argument (or the current stream) of its first tensor's device: the outputs and
     the workspace are then allocated on the stream that the kernels run on.  The inputs are the caller's to order."""
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(first, *args, stream, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise GlaError(GLA_ERR_INVALID_ARG, f"{fn.__name__}: the first argument must be a cuda tensor")
+            raise GlaError(GLA_ERR_INVALID_ARG, f"{fn.__name__[1:-8]}: the first argument must be a cuda tensor")
         if stream is None and first.get_device() == _current_device():
             return fn(first, *args, **kw)
         with torch.cuda.stream(stream), torch.cuda.device(first.device):
@@ -473,9 +491,8 @@ def _pack(what, shape, cu_seqlens, device):
     return cu_seqlens.numel() - 1, B, T, D
 
 
-@_on_stream
 def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None, out_dtype=None, out=None,
-             workspace=None):
+             workspace=None, stream=None):
     """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t on the GPU.
 
     x, g: [B, T, D], cuda, channels adjacent and rows evenly spaced (contiguous, or column ranges of one projection's
@@ -483,6 +500,16 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
     cu_seqlens: int32 [N+1] cuda offsets (B == 1).  out_dtype: x's type (default; fp32 beside an fp32 g) or fp32.
     out: optional [B, T, D] tensor for h.  stream=: the stream to run on.  Returns (h, ht fp32 [N, D] or None).
     """
+    if out is None and workspace is None and stream is None:
+        got = _calls.scan_fwd(x, g, initial_state, output_final_state, cu_seqlens, out_dtype)
+        if got is not None:
+            return got
+    return _scan_fwd_checked(x, g, initial_state, output_final_state, cu_seqlens, out_dtype, out, workspace,
+                             stream=stream)
+
+
+@_on_stream
+def _scan_fwd_checked(x, g, initial_state, output_final_state, cu_seqlens, out_dtype, out, workspace):
     shape, device = x.shape, x.get_device()
     N, B, T, D = _pack("gla_scan_fwd", shape, cu_seqlens, device)
     if out_dtype is None:
@@ -509,15 +536,24 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
     return out, ht
 
 
-@_on_stream
-def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=None, want_dh0=True, dx=None, dg=None,
-             workspace=None):
+def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=None, want_dh0=True, dx=None,
+             dg=None, workspace=None, stream=None):
     """Gradients of ``scan_fwd`` for L = sum(h * dh) + sum(ht * dht), from its gate g and its output h.
 
     g as for scan_fwd; h, dh: [B, T, D] contiguous, of the forward's out_dtype; initial_state, dht: fp32 [N, D] or
     None.  dx_dtype: x's type (default: g's).  dx, dg: optional tensors to write, which may be column ranges of one
     gradient.  Returns (dx, dg in g's type, dh0 fp32 [N, D] or None).
     """
+    if dx is None and dg is None and workspace is None and stream is None:
+        got = _calls.scan_bwd(g, h, dh, initial_state, dht, cu_seqlens, dx_dtype, want_dh0)
+        if got is not None:
+            return got
+    return _scan_bwd_checked(g, h, dh, initial_state, dht, cu_seqlens, dx_dtype, want_dh0, dx, dg, workspace,
+                             stream=stream)
+
+
+@_on_stream
+def _scan_bwd_checked(g, h, dh, initial_state, dht, cu_seqlens, dx_dtype, want_dh0, dx, dg, workspace):
     shape, device = g.shape, g.get_device()
     N, B, T, D = _pack("gla_scan_bwd", shape, cu_seqlens, device)
     if dx_dtype is None:
@@ -571,14 +607,22 @@ def _pool(what, state, state_out, slots, B, tail, device):
     return S, state_out
 
 
-@_on_stream
-def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace=None):
+def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace=None, stream=None):
     """One token of ``scan_fwd``'s recurrence for each of B sequences.
 
     x, g: [B, D] (types and strides as for scan_fwd); state: fp32 [S, D] pool, updated in place (or written to
     state_out, of which only the addressed rows are written); slots: int32 [B] cuda, the pool row of each sequence
     (-1: idle, its h is zeros), or None when S == B.  Returns h [B, D].
     """
+    if workspace is None and stream is None:
+        got = _calls.scan_step(x, g, state, slots, state_out, out_dtype)
+        if got is not None:
+            return got
+    return _scan_step_checked(x, g, state, slots, state_out, out_dtype, workspace, stream=stream)
+
+
+@_on_stream
+def _scan_step_checked(x, g, state, slots, state_out, out_dtype, workspace):
     if x.dim() != 2:
         raise GlaError(GLA_ERR_INVALID_ARG, f"gla_scan_step: x must be [B, D], got shape {tuple(x.shape)}")
     shape, device = x.shape, x.get_device()
@@ -602,14 +646,22 @@ def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace
     return h
 
 
-@_on_stream
-def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtype=None, workspace=None):
+def gla_step(q, k, v, g, state, scale=None, slots=None, state_out=None, out_dtype=None, workspace=None, stream=None):
     """One token of ``gla_fwd``'s recurrence for each of B sequences: S = diag(exp g) S + k^T v, o = scale q S.
 
     q, k, g: [B, H, K]; v: [B, H, V] (contiguous; types as for gla_fwd); state: fp32 [S, H, K, V] pool, updated in
     place (or written to state_out); slots as for scan_step.  out_dtype: fp32 (default) or q's type.
     Returns o [B, H, V].
     """
+    if workspace is None and stream is None:
+        got = _calls.gla_step(q, k, v, g, state, scale, slots, state_out, out_dtype)
+        if got is not None:
+            return got
+    return _gla_step_checked(q, k, v, g, state, scale, slots, state_out, out_dtype, workspace, stream=stream)
+
+
+@_on_stream
+def _gla_step_checked(q, k, v, g, state, scale, slots, state_out, out_dtype, workspace):
     if q.dim() != 3 or v.dim() != 3:
         raise GlaError(GLA_ERR_INVALID_ARG, "gla_step: q, k, g must be [B, H, K] and v [B, H, V]")
     device = q.get_device()
@@ -654,13 +706,21 @@ def _norm_args(what, x, residual, weight, stream_dtype):
     return x.numel() // D, D, code if stream_dtype == x.dtype else code | GLA_RES_F32
 
 
-@_on_stream
-def norm_fwd(x, residual=None, weight=None, eps=1e-6):
+def norm_fwd(x, residual=None, weight=None, eps=1e-6, stream=None):
     """Residual addition and root-mean-square norm over the last dimension: s = x + residual, y = s rstd weight.
 
     x: contiguous [..., D] fp32 / bf16 / fp16; residual: like x, or fp32; weight: fp32 [D] or None.
     Returns (y in x's type, s in the residual's type (x itself without a residual), rstd fp32 [...]).
     """
+    if stream is None:
+        got = _calls.norm_fwd(x, residual, weight, eps)
+        if got is not None:
+            return got
+    return _norm_fwd_checked(x, residual, weight, eps, stream=stream)
+
+
+@_on_stream
+def _norm_fwd_checked(x, residual, weight, eps):
     stream_dtype, device = x.dtype if residual is None else residual.dtype, x.get_device()
     rows, D, code = _norm_args("gla_norm_fwd", x, residual, weight, stream_dtype)
     y = torch.empty_like(x)
@@ -673,10 +733,18 @@ def norm_fwd(x, residual=None, weight=None, eps=1e-6):
     return y, x if s is None else s, rstd
 
 
-@_on_stream
-def norm_quant_fwd(x, residual=None, weight=None, eps=1e-6, group=0):
+def norm_quant_fwd(x, residual=None, weight=None, eps=1e-6, group=0, stream=None):
     """``norm_fwd`` with its output in 8 bits: y is q times its scale.  group: columns of one scale, 128, or 0 for
     one scale per row.  Returns (q float8_e4m3fn [..., D], scales fp32 [..., ceil(D / group)], s, rstd)."""
+    if stream is None:
+        got = _calls.norm_quant_fwd(x, residual, weight, eps, group)
+        if got is not None:
+            return got
+    return _norm_quant_fwd_checked(x, residual, weight, eps, group, stream=stream)
+
+
+@_on_stream
+def _norm_quant_fwd_checked(x, residual, weight, eps, group):
     stream_dtype, device = x.dtype if residual is None else residual.dtype, x.get_device()
     rows, D, code = _norm_args("gla_norm_quant_fwd", x, residual, weight, stream_dtype)
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=device)
@@ -691,13 +759,23 @@ def norm_quant_fwd(x, residual=None, weight=None, eps=1e-6, group=0):
     return q, scales, x if s is None else s, rstd
 
 
-@_on_stream
-def norm_bwd(s, rstd, dy, weight=None, ds=None, want_dw=True, workspace=None):
+def norm_bwd(s, rstd, dy, weight=None, ds=None, want_dw=True, workspace=None, stream=None):
     """Gradients of ``norm_fwd`` from its s and rstd, for the gradients dy of y and ds of s (or None).
 
     Returns (the gradient of x in dy's type, the gradient of the residual in s's type, dw fp32 [D] or None).  The
     first two are one tensor when the types are the same.  ``want_dw=False`` skips dw (also None without a weight).
     """
+    if workspace is None and stream is None and dy.is_cuda and dy.dim():
+        device, D = dy.get_device(), dy.shape[-1]
+        ws = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(dy.numel() // max(D, 1), D)), device)
+        got = _calls.norm_bwd(s, rstd, dy, weight, ds, want_dw, ws)
+        if got is not None:
+            return got
+    return _norm_bwd_checked(s, rstd, dy, weight, ds, want_dw, workspace, stream=stream)
+
+
+@_on_stream
+def _norm_bwd_checked(s, rstd, dy, weight, ds, want_dw, workspace):
     rows, D, code = _norm_args("gla_norm_bwd", dy, s, weight, s.dtype)
     device = s.get_device()
     if ds is not None:

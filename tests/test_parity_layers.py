@@ -615,3 +615,55 @@ def test_kernel_names(B):
             call()
         torch.cuda.synchronize()
         assert [n for n, _ in timer.results()] == names
+
+
+def test_short_and_checked_calls_agree(B):
+    """The usual calls go the short way (a workspace argument sends the same call the checked one), to the same results."""
+    x, g, h0, cu = (t.cuda() for t in scan_inputs((TB, TB), 1, 0, 96, [30, 0, 200], seed=40))
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    B.scan_fwd(x, g)   # the status workspace exists from here on
+    h, ht = B.scan_fwd(x, g, h0, cu_seqlens=cu)
+    pool, slots = torch.randn(5, 96, device="cuda"), torch.tensor([4, 1], dtype=torch.int32).cuda()
+    q = torch.randn(2, 3, 64, device="cuda").to(TH)
+    states = torch.randn(2, 3, 64, 64, device="cuda")
+    w, res = torch.randn(96, device="cuda"), torch.randn(1, 230, 96, device="cuda")
+    rows, x2 = x[0, :2].contiguous(), -x[0, 2:4].abs().contiguous()
+    short = [B._calls.scan_fwd(x, g, h0, True, cu, None), B._calls.scan_fwd(x, g, None, False, None, T32),
+             B._calls.scan_bwd(g, h, x, h0, ht, cu, None, True), B._calls.scan_bwd(g, h, x, None, None, None, TB, False),
+             B._calls.scan_step(rows, x2, pool.clone(), slots, None, T32),
+             B._calls.gla_step(q, q, q, -q.abs(), states.clone(), None, None, None, TH),
+             B._calls.gla_step(q, q, q, -q.abs(), states.clone(), 0.25, None, None, None),
+             B._calls.norm_fwd(x, res, w, 1e-6), B._calls.norm_fwd(x, None, None, 1e-6),
+             B._calls.norm_quant_fwd(x, res, w, 1e-6, 0), B._calls.norm_quant_fwd(x, None, w, 1e-6, 128),
+             B._calls.norm_bwd(res, res[..., 0].contiguous(), x, w, res, True, ws),
+             B._calls.norm_bwd(x, res[..., 0].contiguous(), x, w, None, False, ws)]
+    checked = [B._scan_fwd_checked(x, g, h0, True, cu, None, None, ws, stream=None),
+               B._scan_fwd_checked(x, g, None, False, None, T32, None, ws, stream=None),
+               B._scan_bwd_checked(g, h, x, h0, ht, cu, None, True, None, None, ws, stream=None),
+               B._scan_bwd_checked(g, h, x, None, None, None, TB, False, None, None, ws, stream=None),
+               B._scan_step_checked(rows, x2, pool.clone(), slots, None, T32, ws, stream=None),
+               B._gla_step_checked(q, q, q, -q.abs(), states.clone(), None, None, None, TH, ws, stream=None),
+               B._gla_step_checked(q, q, q, -q.abs(), states.clone(), 0.25, None, None, None, ws, stream=None),
+               B._norm_fwd_checked(x, res, w, 1e-6, stream=None), B._norm_fwd_checked(x, None, None, 1e-6, stream=None),
+               B._norm_quant_fwd_checked(x, res, w, 1e-6, 0, stream=None),
+               B._norm_quant_fwd_checked(x, None, w, 1e-6, 128, stream=None),
+               B._norm_bwd_checked(res, res[..., 0].contiguous(), x, w, res, True, ws, stream=None),
+               B._norm_bwd_checked(x, res[..., 0].contiguous(), x, w, None, False, ws, stream=None)]
+    for a, b in zip(short, checked):
+        a, b = (v if isinstance(v, tuple) else (v,) for v in (a, b))
+        assert len(a) == len(b)
+        for p, r in zip(a, b):
+            assert (p is None) == (r is None)
+            if p is not None:
+                assert p.dtype == r.dtype and p.shape == r.shape and torch.equal(p.float(), r.float())
+    out = B.norm_bwd(x, res[..., 0].contiguous(), x, weight=w)
+    assert out[0] is out[1]
+    for unusual in ((x.cpu(), g, None, True, None, None), (x[..., ::2], g, None, True, None, None),
+                    (x, g.float(), None, True, None, TB), (x, g[:, :5], None, True, None, None),
+                    (x, g, h0[:1], True, cu, None), (x, g, h0.half(), True, cu, None), (1, g, None, True, None, None),
+                    (x, g, None, True, cu.long(), None), (x[0], g[0], None, True, None, None)):
+        assert B._calls.scan_fwd(*unusual) is None
+    assert B._calls.gla_step(q, q, q, q, states[:1], None, None, None, None) is None
+    assert B._calls.gla_step(q, q, q, q, states, -1.0, None, None, None) is None
+    assert B._calls.norm_fwd(x, res.half(), w, 1e-6) is None
+    assert B._calls.norm_quant_fwd(x, None, w, 1e-6, 64) is None
