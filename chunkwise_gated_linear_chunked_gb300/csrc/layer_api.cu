@@ -376,7 +376,7 @@ extern "C" int gla_norm_bwd(const void *s, const float *rstd, const float *w, co
             return launch_norm_bwd(a, dtype & ~GLA_RES_F32, res_f32, st);
         }) != cudaSuccess)
         return GLA_ERR_CUDA;
-    if (dw && profiled(K_NORM_DW, st, [&] { return launch_norm_dw(a, st); }) != cudaSuccess)
+    if (dw && a.ctas != 1 && profiled(K_NORM_DW, st, [&] { return launch_norm_dw(a, st); }) != cudaSuccess)
         return GLA_ERR_CUDA;
     return GLA_OK;
 }

@@ -46,7 +46,7 @@ struct NormArgs {
     const void *x, *res, *s_in, *dy, *ds;
     const float *w, *rstd_in;
     void *y, *s, *dx, *dres;           // y: x's type, or e4m3 with scales
-    float *rstd, *scales, *dw, *part;  // part: partial sums of dw, one row per CTA
+    float *rstd, *scales, *dw, *part;  // part: partial sums of dw, one row per CTA (a single CTA writes dw itself)
     int64_t rows;
     int D, group, ctas;
     float eps;

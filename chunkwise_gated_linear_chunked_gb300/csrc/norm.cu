@@ -13,6 +13,7 @@
 
 #include "api_common.h"
 #include "layer_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gla {
 namespace {
@@ -432,12 +433,14 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
     constexpr bool kEarly = sizeof(Tr) == 2;   // registers for the next row beside the present one
     __shared__ Told told[2][16];
-    __shared__ float acc[2048];   // a CTA of several rows has at most so many columns
+    __shared__ float acc[kThreads * kHeld];
     const int l = threadIdx.x % sp.lanes, D = a.D;
     const Tr *s_in = static_cast<const Tr *>(a.s_in), *ds_in = static_cast<const Tr *>(a.ds);
     const Tx *dy_in = static_cast<const Tx *>(a.dy);
-    const int64_t stride = (int64_t)gridDim.x * sp.rows;
-    int64_t row = (int64_t)blockIdx.x * sp.rows + threadIdx.x / sp.lanes;
+    // a CTA's rows: adjacent ones, or (SHIFTED) a grid apart, a multiple of 8, so that all of them have the same shift
+    // and a column's sum is one lane's for each
+    const int64_t stride = (int64_t)gridDim.x * sp.rows, base = SHIFTED ? blockIdx.x : (int64_t)blockIdx.x * sp.rows;
+    int64_t row = base + threadIdx.x / sp.lanes * (SHIFTED ? (int64_t)gridDim.x : 1);
     Place at = {row * D, D, a.rows * D};
     int col[N];
     columns<VEC>(col, l, sp.lanes, SHIFTED ? (int)(row * D % VEC) : 0);
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     for (int i = 0; i < kHeld / 2; ++i)
         dw[i] = make_float2(0.f, 0.f);
     const float part = 1.f / D;
-    for (int64_t first = (int64_t)blockIdx.x * sp.rows, turn = 0; first < a.rows; first += stride, row += stride, ++turn) {
+    for (int64_t first = base, turn = 0; first < a.rows; first += stride, row += stride, ++turn) {
         if (!kEarly)
             fetch(row);
         const bool on = row < a.rows;
@@ -514,31 +517,28 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     }
     if (!a.dw)
         return;
-    // the CTA's sum of dw: over the rows of a warp at once where they hold the same columns, then one by one
-    const bool same = !SHIFTED && sp.lanes < 32;
-    if (same)
-        for (int m = sp.lanes; m < 32; m *= 2)
+    // the CTA's sum of dw: over the rows of a warp, then over the warps (or the rows of whole warps) in order
+    for (int m = sp.lanes; m < 32; m *= 2)
 #pragma unroll
-            for (int i = 0; i < kHeld / 2; ++i)
-                dw[i] = add2(dw[i], make_float2(__shfl_xor_sync(~0u, dw[i].x, m), __shfl_xor_sync(~0u, dw[i].y, m)));
-    float *out = a.part + (size_t)blockIdx.x * D;
-    const int width = same ? 32 : sp.lanes, turns = sp.threads / width, mine = threadIdx.x / width;
-    const bool lead = threadIdx.x % width < sp.lanes;
-    for (int t = 0; t < turns; ++t) {
-        if (t == mine && lead)
+        for (int i = 0; i < kHeld / 2; ++i)
+            dw[i] = add2(dw[i], make_float2(__shfl_xor_sync(~0u, dw[i].x, m), __shfl_xor_sync(~0u, dw[i].y, m)));
+    float *out = a.ctas == 1 ? a.dw : a.part + (size_t)blockIdx.x * D;
+    const int width = max(sp.lanes, 32), parts = sp.threads / width, mine = threadIdx.x / width;
+    if (threadIdx.x % width < sp.lanes)
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const int d = col[i / VEC] + i % VEC;
-                if ((unsigned)d >= (unsigned)D)
-                    continue;
-                const float v = i % 2 ? dw[i / 2].y : dw[i / 2].x, sum = t > 0 ? acc[d] + v : v;
-                if (t == turns - 1)
-                    out[d] = sum;
-                else
-                    acc[d] = sum;
-            }
-        if (turns > 1)
-            __syncthreads();
+        for (int i = 0; i < kHeld; ++i) {
+            const int d = col[i / VEC] + i % VEC;
+            if ((unsigned)d < (unsigned)D)
+                (parts > 1 ? acc + mine * D : out)[d] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
+        }
+    if (parts == 1)
+        return;
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += sp.threads) {
+        float sum = acc[d];
+        for (int i = 1; i < parts; ++i)
+            sum += acc[i * D + d];
+        out[d] = sum;
     }
 }
 
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_wide(NormArgs a)
     __shared__ float sh[kThreads / 32];
     const Tr *s = static_cast<const Tr *>(a.s_in), *ds = static_cast<const Tr *>(a.ds);
     const Tx *dy = static_cast<const Tx *>(a.dy);
-    float *part = a.part + (size_t)blockIdx.x * a.D;
+    float *part = a.ctas == 1 && a.dw ? a.dw : a.part + (size_t)blockIdx.x * a.D;
     for (int d = threadIdx.x; d < a.D; d += kThreads)
         part[d] = 0.f;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_wide(NormArgs a)
 __global__ void __launch_bounds__(1024) norm_dw_kernel(NormArgs a)
 {
     __shared__ float sh[32][33];
+    tc::grid_dep_wait();   // launched while norm_bwd's last CTAs still run
     const int c = threadIdx.x % 32, k = threadIdx.x / 32, d = blockIdx.x * 32 + c;
     float sum = 0.f;
     if (d < a.D)
@@ -670,6 +671,14 @@ int grid_of(int64_t rows, const Split &sp, int per_sm)
 {
     const int64_t need = (rows + sp.rows - 1) / sp.rows, most = (int64_t)per_sm * sm_count() / 8 * 8;
     return (int)std::min(need, most);
+}
+
+// The backward's: a multiple of 8 where rows are shifted and several to a CTA.
+int bwd_grid(int64_t rows, int D, int vec)
+{
+    const Split sp = split_of(D, vec);
+    const int ctas = grid_of(rows, sp, std::max(1, 512 / sp.threads));   // 128 registers a thread
+    return D % vec && sp.rows > 1 ? (ctas + 7) / 8 * 8 : ctas;
 }
 
 template <typename Tx, typename Tr, Quant Q, bool SHIFTED>
@@ -704,8 +713,7 @@ int norm_bwd_ctas(int64_t rows, int D, int dtype)
     const int vec = dtype == GLA_F32 ? 4 : 8;
     if (wide(D, vec))
         return (int)std::min<int64_t>(rows, 2 * sm_count());
-    const Split sp = split_of(D, vec);
-    return grid_of(rows, sp, std::max(1, 512 / sp.threads));   // 128 registers a thread
+    return bwd_grid(rows, D, vec);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s)
@@ -740,8 +748,16 @@ cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
 
 cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s)
 {
-    norm_dw_kernel<<<(a.D + 31) / 32, 1024, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.D + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_dw_kernel, a);
 }
 
 }  // namespace gla

@@ -9,6 +9,7 @@
 // The backward is the same chain from the last row to the first: mu_t = a_t (dh_t + mu_{t+1}).
 //
 // Every input is read once and every output written once.  The order of all sums is fixed by the shape.
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -73,95 +74,103 @@ __device__ __forceinline__ bool sequence_rows(const ScanArgs &a, int n, int64_t 
     return ok;
 }
 
-// One R x kCols tile of a row-strided tensor in shared memory.  Rows whose bytes start and step in 16-byte units
-// (ALIGNED) lie as they are; others are copied from the 16-byte unit that holds their first byte, so every row has a
-// shift of its own.
-template <typename T, int R, bool ALIGNED>
+// How rows lie in memory: on whole 16-byte units; elsewhere, but with their channels in whole pairs; anywhere.
+enum Rows { kUnits, kPairs, kAnywhere };
+
+// One R x kCols tile of a row-strided tensor in shared memory.  Rows on whole 16-byte units lie as they are; others are
+// copied from the unit that holds their first byte, so every row has a shift of its own.
+template <typename T, int R, Rows ROWS>
 struct Tile {
-    static constexpr int kUnits = kCols * (int)sizeof(T) / 16 + (ALIGNED ? 0 : 1);
-    static constexpr int kPitch = kUnits * 16;
+    static constexpr int kWhole = kCols * (int)sizeof(T) / 16, kRow = kWhole + (ROWS == kUnits ? 0 : 1);   // units
+    static constexpr int kPitch = kRow * 16;
     static constexpr int kBytes = R * kPitch;
 
     // Row j of the tile is row r0 + DIR j of the sequence (src: its first row at the tile's first channel); rows
-    // outside [0, len) and channels from `cols` on are zeros.  A thread copies
-    // from one 16-byte column of the tile.
+    // outside [0, len) and channels from `cols` on are zeros.  A thread copies from one 16-byte column of the tile.
     template <int DIR>
     static __device__ __forceinline__ void load(char *dst, const T *src, int64_t ld, int r0, int len, int cols)
     {
-        const int width = min(kCols, cols) * (int)sizeof(T);
-        if constexpr (ALIGNED) {
-            constexpr int kStep = kThreads / kUnits;   // rows between a thread's copies
-            const int u = threadIdx.x % kUnits, j0 = threadIdx.x / kUnits;
-            const bool in = 16 * u < width;
-            const T *p = src + (int64_t)(r0 + DIR * j0) * ld + 16 / (int)sizeof(T) * u;
-            char *q = dst + j0 * kPitch + 16 * u;
-            if (width == kPitch && (unsigned)r0 < (unsigned)len && (unsigned)(r0 + DIR * (R - 1)) < (unsigned)len) {
+        constexpr int kStep = kThreads / kRow;   // rows between a thread's copies
+        const int u = threadIdx.x % kRow, j0 = threadIdx.x / kRow;
+        const bool all = cols >= kCols && (unsigned)r0 < (unsigned)len && (unsigned)(r0 + DIR * (R - 1)) < (unsigned)len;
+        const char *p = reinterpret_cast<const char *>(src) + (int64_t)(r0 + DIR * j0) * ld * (int)sizeof(T);
+        const int64_t step = (int64_t)DIR * kStep * ld * (int)sizeof(T);
+        char *q = dst + j0 * kPitch + 16 * u;
+        if constexpr (ROWS == kUnits) {
+            p += 16 * u;
+            if (all) {
 #pragma unroll
                 for (int j = 0; j < R; j += kStep)
-                    copy16(q + j * kPitch, p + DIR * (int64_t)j * ld);
+                    copy16(q + j * kPitch, p + j / kStep * step);
                 return;
             }
+            const bool in = 16 * u < cols * (int)sizeof(T);
 #pragma unroll
             for (int j = 0; j < R; j += kStep) {
-                const int r = r0 + DIR * (j0 + j);
-                const bool ok = in && (unsigned)r < (unsigned)len;
-                copy16(q, ok ? p : src, ok ? 16 : 0);
-                p += DIR * kStep * ld;
+                const bool ok = in && (unsigned)(r0 + DIR * (j0 + j)) < (unsigned)len;
+                copy16(q, ok ? p : reinterpret_cast<const char *>(src) - (reinterpret_cast<uintptr_t>(src) & 15), ok ? 16 : 0);
+                p += step;
                 q += kStep * kPitch;
             }
         } else {
-            constexpr int kStep = kThreads / kUnits;
-            const int u = threadIdx.x % kUnits, j0 = threadIdx.x / kUnits;
             if (j0 >= kStep)
                 return;
+            const int width = min(kCols, cols) * (int)sizeof(T);
 #pragma unroll
-            for (int j = j0; j < R; j += kStep) {
-                const int r = r0 + DIR * j;
-                const bool ok = (unsigned)r < (unsigned)len;
-                const char *p = reinterpret_cast<const char *>(src + (ok ? r * ld : 0));
+            for (int j = 0; j < (R + kStep - 1) / kStep * kStep; j += kStep) {
                 const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-                const int bytes = ok ? max(0, min(16, shift + width - 16 * u)) : 0;
-                copy16(dst + j * kPitch + 16 * u, p - shift + (bytes ? 16 * u : 0), bytes);
+                if (R % kStep == 0 || j0 + j < R) {
+                    if (all) {   // the last unit holds as many bytes of the row as its first bytes are shifted by
+                        const int bytes = u < kWhole ? 16 : shift;
+                        copy16(q, p - shift + (bytes ? 16 * u : 0), bytes);
+                    } else {
+                        const bool ok = (unsigned)(r0 + DIR * (j0 + j)) < (unsigned)len;
+                        const int bytes = ok ? max(0, min(16, shift + width - 16 * u)) : 0;
+                        const char *from = ok ? p : reinterpret_cast<const char *>(src);
+                        copy16(q, from - (reinterpret_cast<uintptr_t>(from) & 15) + (bytes ? 16 * u : 0), bytes);
+                    }
+                }
+                p += step;
+                q += kStep * kPitch;
             }
         }
     }
 
-    // The lane's two channels of row j (row r of the sequence): 2 l and 2 l + 1, or l and l + 32 where rows are shifted.
+    // The lane's two channels of row j (row r of the sequence): 2 l and 2 l + 1, or l and l + 32 for rows anywhere.
     static __device__ __forceinline__ float2 read(const char *tile, int j, const T *src, int64_t ld, int r)
     {
         const int lane = threadIdx.x & 31;
         const char *row = tile + j * kPitch;
-        if constexpr (ALIGNED) {
-            if constexpr (sizeof(T) == 4)
-                return *reinterpret_cast<const float2 *>(row + 8 * lane);
-            else
-                return widen2<T>(*reinterpret_cast<const uint32_t *>(row + 4 * lane));
-        } else {
-            // only the low bits of the address count (rows outside the sequence are zeros at any shift)
-            const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(src) + (uint32_t)r * (uint32_t)ld * (uint32_t)sizeof(T);
-            const T *p = reinterpret_cast<const T *>(row + (at & 15));
+        if constexpr (ROWS != kUnits)   // only the low bits of the address count (rows outside are zeros at any shift)
+            row += ((uint32_t)reinterpret_cast<uintptr_t>(src) + (uint32_t)r * (uint32_t)ld * (uint32_t)sizeof(T)) & 15;
+        if constexpr (ROWS == kAnywhere) {
+            const T *p = reinterpret_cast<const T *>(row);
             return make_float2(widen(p[lane]), widen(p[lane + 32]));
+        } else if constexpr (sizeof(T) == 4) {
+            return *reinterpret_cast<const float2 *>(row + 8 * lane);
+        } else {
+            return widen2<T>(*reinterpret_cast<const uint32_t *>(row + 4 * lane));
         }
     }
 };
 
 // The lane's two channels, and the stores of a pair.
-template <bool ALIGNED>
+template <bool PAIRED>
 struct Pair {
     int d[2];
     bool on[2];
     __device__ __forceinline__ Pair(int d0, int D)
     {
         const int lane = threadIdx.x & 31;
-        d[0] = d0 + (ALIGNED ? 2 * lane : lane);
-        d[1] = d0 + (ALIGNED ? 2 * lane + 1 : lane + 32);
+        d[0] = d0 + (PAIRED ? 2 * lane : lane);
+        d[1] = d0 + (PAIRED ? 2 * lane + 1 : lane + 32);
         on[0] = d[0] < D;
         on[1] = d[1] < D;
     }
     template <bool WHOLE, typename T>   // WHOLE: both channels exist
     __device__ __forceinline__ void store(T *row, float2 v) const
     {
-        if constexpr (ALIGNED) {
+        if constexpr (PAIRED) {
             if (!WHOLE && !on[0])
                 return;
             if constexpr (sizeof(T) == 4)
@@ -313,13 +322,13 @@ __device__ __forceinline__ float2 receive(Shared &sh, const float4 *ctas, float2
 }
 
 // What a CTA does with its tiles.  Position p of the forward's walk is row p of the sequence.
-template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT_>
+template <typename Tx, typename Tg, typename To, Rows ROWS, int RPT_>
 struct Forward {
     static constexpr int RPT = RPT_, R = kWarps * RPT;
-    typedef Tile<Tx, R, ALIGNED> TX;
-    typedef Tile<Tg, R, ALIGNED> TG;
+    typedef Tile<Tx, R, ROWS> TX;
+    typedef Tile<Tg, R, ROWS> TG;
     static constexpr int kStage = TX::kBytes + TG::kBytes;
-    typedef Pair<ALIGNED> Lane;
+    typedef Pair<ROWS != kAnywhere> Lane;
     Map row[RPT];
     const Tx *x;
     const Tg *g;
@@ -370,13 +379,13 @@ struct Forward {
 };
 
 // Position p of the backward's walk is row len - 1 - p; its state is mu.
-template <typename Tx, typename Tg, typename To, bool ALIGNED, int RPT_>
+template <typename Tx, typename Tg, typename To, Rows ROWS, int RPT_>
 struct Backward {
     static constexpr int RPT = RPT_, R = kWarps * RPT;
-    typedef Tile<Tg, R, ALIGNED> TG;
-    typedef Tile<To, R, ALIGNED> TO;
+    typedef Tile<Tg, R, ROWS> TG;
+    typedef Tile<To, R, ROWS> TO;
     static constexpr int kStage = TG::kBytes + 2 * TO::kBytes;
-    typedef Pair<ALIGNED> Lane;
+    typedef Pair<ROWS != kAnywhere> Lane;
     float2 dec[RPT], up[RPT];
     const Tg *g;
     const To *h, *dh;
@@ -671,9 +680,11 @@ cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kernel, a, tiles, S);
 }
 
-// Whether rows of `elem`-byte elements start and step in 16-byte units, or in whole pairs of channels.
-bool units16(int64_t ld, int D, int elem) { return ld * elem % 16 == 0 && (int64_t)D * elem % 16 == 0; }
-bool pairs(int64_t ld, int D) { return ld % 2 == 0 && D % 2 == 0; }
+// How rows that start `ld` elements of `elem` bytes apart, D of them channels, lie in memory.
+Rows rows_of(int64_t ld, int D, int elem)
+{
+    return ld * elem % 16 == 0 && (int64_t)D * elem % 16 == 0 ? kUnits : ld % 2 == 0 && D % 2 == 0 ? kPairs : kAnywhere;
+}
 
 // How a call's sequences are shared out: those of at most `rows` rows to threads that walk alone, the others to the
 // tiles.  Alone is better for 16 rows at most (512 x 16 rows of 2048 channels: 19 us against 130), and for up to 128
@@ -693,18 +704,18 @@ Share share_out(const ScanArgs &a)
     return alone ? Share{a.T, false} : Share{-1, true};
 }
 
-template <typename Tx, typename Tg, typename To, bool ALIGNED>
+template <typename Tx, typename Tg, typename To, Rows ROWS>
 cudaError_t fwd_tiles(const ScanArgs &a, cudaStream_t s)
 {
     // rows of a thread: the more the fewer exchanges, as registers and shared memory allow for two CTAs an SM
-    return launch_tiles<Forward<Tx, Tg, To, ALIGNED, sizeof(Tx) + sizeof(Tg) == 4 ? 16 : 8>>(a, s);
+    return launch_tiles<Forward<Tx, Tg, To, ROWS, sizeof(Tx) + sizeof(Tg) == 4 ? 16 : 8>>(a, s);
 }
 
-template <typename Tx, typename Tg, typename To, bool ALIGNED>
+template <typename Tx, typename Tg, typename To, Rows ROWS>
 cudaError_t bwd_tiles(const ScanArgs &a, cudaStream_t s)
 {
     constexpr int kBytes = sizeof(Tg) + 2 * sizeof(To);
-    return launch_tiles<Backward<Tx, Tg, To, ALIGNED, ALIGNED ? (kBytes == 6 ? 16 : 8) : (kBytes == 12 ? 4 : 8)>>(a, s);
+    return launch_tiles<Backward<Tx, Tg, To, ROWS, ROWS == kUnits ? (kBytes == 6 ? 16 : 8) : (kBytes == 12 ? 4 : 8)>>(a, s);
 }
 
 }  // namespace
@@ -717,9 +728,10 @@ cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s)
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
+        const Rows rows = std::max(rows_of(a.ldx, a.D, sizeof(Tx)), rows_of(a.ldg, a.D, sizeof(Tg)));
         if (share.rows >= 0) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
-            if (pairs(a.ldx, a.D) && pairs(a.ldg, a.D))
+            if (rows != kAnywhere)
                 scan_fwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
             else
                 scan_fwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
@@ -727,8 +739,8 @@ cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s)
             if (e != cudaSuccess || !share.tiles)
                 return e;
         }
-        const bool ok = units16(a.ldx, a.D, sizeof(Tx)) && units16(a.ldg, a.D, sizeof(Tg));
-        return ok ? fwd_tiles<Tx, Tg, To, true>(a, s) : fwd_tiles<Tx, Tg, To, false>(a, s);
+        return rows == kUnits ? fwd_tiles<Tx, Tg, To, kUnits>(a, s)
+               : rows == kPairs ? fwd_tiles<Tx, Tg, To, kPairs>(a, s) : fwd_tiles<Tx, Tg, To, kAnywhere>(a, s);
     });
 }
 
@@ -740,9 +752,11 @@ cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s)
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
+        const Rows rows = std::max({rows_of(a.ldg, a.D, sizeof(Tg)), rows_of(a.D, a.D, sizeof(To)),
+                                    rows_of(a.lddx, a.D, sizeof(Tx)), rows_of(a.lddg, a.D, sizeof(Tg))});
         if (share.rows >= 0) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
-            if (pairs(a.ldg, a.D) && pairs(a.lddx, a.D) && pairs(a.lddg, a.D))
+            if (rows != kAnywhere)
                 scan_bwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
             else
                 scan_bwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
@@ -750,9 +764,8 @@ cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s)
             if (e != cudaSuccess || !share.tiles)
                 return e;
         }
-        const bool ok = units16(a.ldg, a.D, sizeof(Tg)) && units16(a.D, a.D, sizeof(To)) &&
-                        units16(a.lddx, a.D, sizeof(Tx)) && units16(a.lddg, a.D, sizeof(Tg));
-        return ok ? bwd_tiles<Tx, Tg, To, true>(a, s) : bwd_tiles<Tx, Tg, To, false>(a, s);
+        return rows == kUnits ? bwd_tiles<Tx, Tg, To, kUnits>(a, s)
+               : rows == kPairs ? bwd_tiles<Tx, Tg, To, kPairs>(a, s) : bwd_tiles<Tx, Tg, To, kAnywhere>(a, s);
     });
 }
 
