@@ -10,6 +10,7 @@
 //
 // Every input is read once and every output written once.  The order of all sums is fixed by the shape.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -630,6 +631,36 @@ struct Fit {
     int clusters[128][kMaxCluster + 1] = {};
 };
 
+// CTAs of a cluster, for `units` (sequence, channel tile) pairs of `rows` rows (a pack's mean): as many as run at once,
+// up to one time slice of R rows each.  Where not even two each do, the clusters come in waves, and the shorter their
+// walks, the less the last wave costs; on the other side are a start of about 1.5 tiles' time and an exchange of about
+// 0.03 for each further CTA.  A last wave costs at least 0.6 of a full one (CTAs that share an SM no longer still wait
+// for their own tiles).  The lengths of a pack differ, which leaves about half a walk at the end.  Measured for 1, 2
+// and 4 CTAs, in us: 256 units of 4096 rows 70, 68, 69 (backward 116, 110, 111); 160 of 4096: 51, 58, 50; 1024 of 1024:
+// 62, 76, 97; 512 of a pack of 128 to 8192 rows: 197, 182, 184.
+int cluster_size(const int *fit, int64_t units, int64_t rows, int R, bool pack)
+{
+    int S = 1;
+    for (int c = 2; c <= kMaxCluster && (c - 1) * R < rows; ++c)
+        if (fit[c] >= units)
+            S = c;
+    if (S > 1)
+        return S;
+    double best = 0;
+    for (int c : {1, 2, 4}) {
+        if (fit[c] <= 0 || (c > 1 && (c - 1) * R >= rows))
+            continue;
+        const double walk = (double)((rows + c * R - 1) / (c * R)) * (1 + 0.03 * (c - 1)) + 1.5;
+        const double full = (double)units / fit[c], whole = std::floor(full), part = full - whole;
+        const double waves = pack ? full + 0.5 : full <= 1 ? 1 : whole + (part > 0 ? std::max(part, 0.6) : 0);
+        if (c == 1 || waves * walk < best) {
+            best = waves * walk;
+            S = c;
+        }
+    }
+    return S;
+}
+
 template <typename Role>
 cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
 {
@@ -667,15 +698,9 @@ cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
         cudaGetLastError();
         fit.known[dev] = true;
     }
-    // As many CTAs a sequence as run at once, up to one time slice each.  More would wait for a second wave, whose
-    // clusters start when the first have ended: 8 x 4096 rows of 2048 channels, backward, run in 115 us with 256 CTAs
-    // and in 152 us with 512.
     const int tiles = (a.D + kCols - 1) / kCols;
     const int64_t units = (int64_t)a.N * tiles;
-    int S = 1;
-    for (int c = 2; c <= kMaxCluster && (c - 1) * Role::R < a.T; ++c)
-        if (fit.clusters[dev][c] >= units)
-            S = c;
+    const int S = cluster_size(fit.clusters[dev], units, a.cu ? a.T / a.N : a.T, Role::R, a.cu != nullptr);
     shape(units, S);
     return cudaLaunchKernelEx(&cfg, kernel, a, tiles, S);
 }

@@ -124,6 +124,23 @@ def test_scan_pack_of_many_lengths(B, types, D):
         within(y, r, t, name)
 
 
+@pytest.mark.parametrize("types,Bn,T,D", [((TB, TB, TB), 24, 2100, 1000), ((TB, T32, T32), 10, 3000, 998)],
+                         ids=["bf16", "f32-gate"])
+def test_scan_more_tiles_than_run_at_once(B, types, Bn, T, D):
+    """So many (sequence, channel tile) pairs that clusters come in waves."""
+    x, g, h0, _ = scan_inputs(types, Bn, T, D, seed=32)
+    g_d, h0_d = g.cuda(), h0.cuda()
+    h, ht = B.scan_fwd(x.cuda(), g_d, initial_state=h0_d, out_dtype=types[2])
+    ref, ref_t, tol, tol_t = lo.scan_fwd(f64(x), f64(g), f64(h0))
+    within(h, ref, tol, "h")
+    within(ht, ref_t, tol_t, "ht")
+    dh = torch.randn(h.shape, generator=torch.Generator().manual_seed(33)).to(types[2])
+    grads = B.scan_bwd(g_d, h, dh.cuda(), initial_state=h0_d, dx_dtype=types[0])
+    refs, tols = lo.scan_bwd(f64(g), f64(h), f64(dh), f64(h0))
+    for name, y, r, t in zip(("dx", "dg", "dh0"), grads, refs, tols):
+        within(y, r, t, name)
+
+
 def test_scan_many_batches_of_few_rows(B):
     for T in (1, 2, 9, 17):
         x, g, h0, _ = scan_inputs((TH, TH), 301, T, 72, seed=T)
