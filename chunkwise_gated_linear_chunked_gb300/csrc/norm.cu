@@ -8,6 +8,11 @@
 // Memory is read and written in whole 16-byte units whatever D is.  A row starts k values into such a unit; a thread's
 // vectors lie on units, so vector v holds columns VEC v - k and up, and the two vectors that hang over the row's ends
 // go value by value.  Rows a multiple of VEC apart have the same k, so a thread keeps its columns (and its weights).
+//
+// Bound by HBM: 65536 rows of 4096 columns in 16 bits with a residual 335 us (6.4 TB/s), e4m3 in groups of 128 with an
+// fp32 residual, 16384 x 2048, 58 us (6.4), the backward of 32768 x 2048 89 us (6.0), rows of 1001 columns 94 us (5.6)
+// and 134 us (3.9).  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower (86 -> 93 us
+// at 65536 x 1024).
 #include <algorithm>
 #include <atomic>
 

@@ -8,7 +8,12 @@
 // in shared memory) and writes them.  The cluster walks the sequence S * R rows at a time and carries the state.
 // The backward is the same chain from the last row to the first: mu_t = a_t (dh_t + mu_{t+1}).
 //
-// Every input is read once and every output written once.  The order of all sums is fixed by the shape.
+// Every input is read once and every output written once.  The order of all sums is fixed by the shape (and the SMs).
+//
+// HBM bounds it where there is enough to do: 65536 rows of 4096 channels, 16 bits, 250-265 us (6.1-6.4 TB/s; a copy
+// runs at 6.8), the backward of 65536 x 2048 217 us (6.2).  A tile of 128 rows by 64 channels costs a CTA 0.9 us alone
+// and 2 us beside another on its SM (16.6 instructions an element, 25 in the backward), an exchange between CTAs 0.45;
+// few channels of long sequences are bound by that chain (65536 x 512: 73 us), short ones by starting it.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -544,7 +549,7 @@ struct Two {
 
 
 // Few rows, or so many channels that they alone fill the GPU: a thread walks two channels of a sequence, kAhead rows
-// at a time.
+// at a time, whose loads are under way together (512 x 64 rows of 2048 channels, 16 bits: 64 us, 6.3 TB/s).
 constexpr int kAhead = 8;
 
 template <typename Tx, typename Tg, typename To, bool PAIRED>

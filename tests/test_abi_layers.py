@@ -145,3 +145,15 @@ def test_norm_bwd_refusals(gla):
     assert gla.lib().gla_norm_bwd_workspace_size(100, 0) == 0
     assert gla.lib().gla_norm_bwd_workspace_size(100, 20000) == 0
     assert gla.lib().gla_norm_bwd_workspace_size(100, 64) >= 256
+
+
+def test_earlier_entry_points_refuse_the_layers_types(gla):
+    """fp16 outputs (GLA_F16_OF16) belong to the recurrence and the one-token updates only."""
+    lib, ws = gla.lib(), 64 * A
+    assert lib.gla_fwd(A, 2 * A, 3 * A, 4 * A, 5 * A, 0.1, None, None, None, 2, 2, 100, 2, 64, 64, 64, gla.GLA_F16_OF16, ws,
+                       1 << 40, None) == gla.GLA_ERR_UNSUPPORTED
+    assert gla.workspace_size(2, 100, 2, 64, 64, 2, 64, gla.GLA_F16_OF16) == 0
+    assert gla.bwd_workspace_size(2, 100, 2, 64, 64, 2, 64, gla.GLA_F16_OF16) == 0
+    assert lib.gla_wy_fwd(A, 2 * A, 3 * A, 4 * A, None, 5 * A, 6 * A, None, 2, 2, 100, 2, 2, 64, 64, 64, gla.GLA_F16_OF16, ws,
+                          1 << 40, None) == gla.GLA_ERR_UNSUPPORTED
+    assert lib.gla_chunk_local_cumsum(A, 2 * A, None, 1, 1, 10, 1, 64, 64, gla.GLA_F16_OF16, None) == gla.GLA_ERR_UNSUPPORTED
