@@ -45,7 +45,7 @@ enum KernelId {
     K_BWD_SUMS = 8, K_BWD_SCAN = 9, K_BWD_GRADS = 10, K_BWD_DG = 11, K_TTT = 12, K_WY = 13,
     K_WY_TC = 14, K_BWD_SUMS_TC = 15, K_BWD_GRADS_TC = 16, K_TTT_TC = 17,
     K_SCAN_FWD = 18, K_SCAN_BWD = 19, K_SCAN_STEP = 20, K_GLA_STEP = 21, K_NORM_FWD = 22, K_NORM_QUANT = 23,
-    K_NORM_BWD = 24, K_NORM_DW = 25
+    K_NORM_BWD = 24, K_NORM_DW = 25, K_SCAN_FWD_ROWS = 26, K_SCAN_BWD_ROWS = 27
 };
 
 // Launch one kernel through `fn`, bracketed by the profiling events when they are armed.

@@ -378,6 +378,8 @@ extern "C" const char *gla_kernel_name(int kernel_id)
     case K_NORM_QUANT: return "norm_quant_fwd";
     case K_NORM_BWD: return "norm_bwd";
     case K_NORM_DW: return "norm_dw";
+    case K_SCAN_FWD_ROWS: return "scan_fwd_rows";
+    case K_SCAN_BWD_ROWS: return "scan_bwd_rows";
     default: return "unknown";
     }
 }

@@ -140,7 +140,14 @@ extern "C" int gla_scan_fwd(const void *x, const void *g, void *h, const float *
     a.N = N; a.T = T; a.D = D; a.ldx = ldx; a.ldg = ldg;
     a.status = static_cast<int *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return profiled(K_SCAN_FWD, s, [&] { return launch_scan_fwd(a, dtype, s); }) == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+    const ScanShare share = scan_share(a);
+    a.alone = share.rows;
+    if (share.rows >= 0 &&
+        profiled(K_SCAN_FWD_ROWS, s, [&] { return launch_scan_fwd(a, dtype, true, s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    if (share.tiles && profiled(K_SCAN_FWD, s, [&] { return launch_scan_fwd(a, dtype, false, s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    return GLA_OK;
 }
 
 extern "C" int gla_scan_bwd(const void *g, const void *h, const void *dh, const float *h0, const float *dht, void *dx,
@@ -178,7 +185,14 @@ extern "C" int gla_scan_bwd(const void *g, const void *h, const void *dh, const 
     a.N = N; a.T = T; a.D = D; a.ldg = ldg; a.lddx = lddx; a.lddg = lddg;
     a.status = static_cast<int *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return profiled(K_SCAN_BWD, s, [&] { return launch_scan_bwd(a, dtype, s); }) == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+    const ScanShare share = scan_share(a);
+    a.alone = share.rows;
+    if (share.rows >= 0 &&
+        profiled(K_SCAN_BWD_ROWS, s, [&] { return launch_scan_bwd(a, dtype, true, s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    if (share.tiles && profiled(K_SCAN_BWD, s, [&] { return launch_scan_bwd(a, dtype, false, s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    return GLA_OK;
 }
 
 extern "C" int gla_scan_step(const void *x, const void *g, void *h, const float *h0, float *ht, const int32_t *slots,

@@ -52,8 +52,15 @@ struct NormArgs {
     float eps;
 };
 
-cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s);
-cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s);
+// A recurrence's sequences of at most `rows` rows go to the kernel whose threads walk alone (none: -1), and what is left
+// (if any can be) to the one that cuts the time axis into tiles.
+struct ScanShare {
+    int rows;
+    bool tiles;
+};
+ScanShare scan_share(const ScanArgs &a);
+cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, bool alone, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, bool alone, cudaStream_t s);
 cudaError_t launch_scan_step(const StepArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_gla_step(const StepArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStream_t s);

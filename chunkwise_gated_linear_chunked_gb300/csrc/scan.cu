@@ -15,6 +15,7 @@
 // and 2 us beside another on its SM (16.6 instructions an element, 25 in the backward), an exchange between CTAs 0.45;
 // few channels of long sequences are bound by that chain (65536 x 512: 73 us), short ones by starting it.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(128) scan_bwd_rows(ScanArgs a, int tiles)
 // Clusters of S = 1..kMaxCluster CTAs of a kernel that the current device runs at once.
 struct Fit {
     std::mutex mu;
-    bool known[128] = {};
+    std::atomic<bool> known[128] = {};
     int clusters[128][kMaxCluster + 1] = {};
 };
 
@@ -689,19 +690,19 @@ cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
         cfg.gridDim = dim3((unsigned)(units * S));
         cfg.dynamicSmemBytes = STAGES * Role::kStage + (S > 1 ? kSlots * S * 512 : 0);
     };
-    std::lock_guard<std::mutex> lock(fit.mu);
-    if (!fit.known[dev]) {
+    if (!fit.known[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(fit.mu);
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       STAGES * Role::kStage + kSlots * kMaxCluster * 512)) != cudaSuccess)
             return e;
         for (int S = 1; S <= kMaxCluster; ++S) {
             shape(1, S);
-            if (cudaOccupancyMaxActiveClusters(&fit.clusters[dev][S], kernel, &cfg) != cudaSuccess)
-                fit.clusters[dev][S] = 0;   // a size this device does not have
+            int n = 0;
+            fit.clusters[dev][S] = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
         }
         cudaGetLastError();
-        fit.known[dev] = true;
+        fit.known[dev].store(true, std::memory_order_release);
     }
     const int tiles = (a.D + kCols - 1) / kCols;
     const int64_t units = (int64_t)a.N * tiles;
@@ -714,24 +715,6 @@ cudaError_t launch_tiles(const ScanArgs &a, cudaStream_t s)
 Rows rows_of(int64_t ld, int D, int elem)
 {
     return ld * elem % 16 == 0 && (int64_t)D * elem % 16 == 0 ? kUnits : ld % 2 == 0 && D % 2 == 0 ? kPairs : kAnywhere;
-}
-
-// How a call's sequences are shared out: those of at most `rows` rows to threads that walk alone, the others to the
-// tiles.  Alone is better for 16 rows at most (512 x 16 rows of 2048 channels: 19 us against 130), and for up to 128
-// where there are enough channels to fill the GPU (256 x 128 rows of 2048 channels: 69 us against 83; 64 x 128 rows of
-// 1024: 20 against 15).  The lengths of a pack are not known here: one of many sequences takes both kernels, each
-// leaving the other's sequences alone; a pack of fewer takes the tiles, which split a long sequence too.
-struct Share {
-    int rows;
-    bool tiles;
-};
-Share share_out(const ScanArgs &a)
-{
-    const int64_t channels = (int64_t)a.N * a.D;
-    if (a.cu)
-        return channels >= 8 * kCols * (int64_t)sm_count() ? Share{64, true} : Share{-1, true};
-    const bool alone = a.T <= 16 || (a.T <= 128 && channels >= 2048 * (int64_t)a.T);
-    return alone ? Share{a.T, false} : Share{-1, true};
 }
 
 template <typename Tx, typename Tg, typename To, Rows ROWS>
@@ -750,49 +733,55 @@ cudaError_t bwd_tiles(const ScanArgs &a, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s)
+// How a call's sequences are shared out: those of at most `rows` rows to threads that walk alone, the others to the
+// tiles.  Alone is better for 16 rows at most (512 x 16 rows of 2048 channels: 19 us against 130), and for up to 128
+// where there are enough channels to fill the GPU (256 x 128 rows of 2048 channels: 69 us against 83; 64 x 128 rows of
+// 1024: 20 against 15).  The lengths of a pack are not known here: one of many sequences takes both kernels, each
+// leaving the other's sequences alone; a pack of fewer takes the tiles, which split a long sequence too.
+ScanShare scan_share(const ScanArgs &a)
 {
-    const Share share = share_out(a);
-    a.alone = share.rows;
+    const int64_t channels = (int64_t)a.N * a.D;
+    if (a.cu)
+        return channels >= 8 * kCols * (int64_t)sm_count() ? ScanShare{64, true} : ScanShare{-1, true};
+    const bool alone = a.T <= 16 || (a.T <= 128 && channels >= 2048 * (int64_t)a.T);
+    return alone ? ScanShare{a.T, false} : ScanShare{-1, true};
+}
+
+cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, bool alone, cudaStream_t s)
+{
     return by_types(dtype, [&](auto x, auto g, auto o) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
         const Rows rows = std::max(rows_of(a.ldx, a.D, sizeof(Tx)), rows_of(a.ldg, a.D, sizeof(Tg)));
-        if (share.rows >= 0) {
+        if (alone) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
             if (rows != kAnywhere)
                 scan_fwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
             else
                 scan_fwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            const cudaError_t e = cudaGetLastError();
-            if (e != cudaSuccess || !share.tiles)
-                return e;
+            return cudaGetLastError();
         }
         return rows == kUnits ? fwd_tiles<Tx, Tg, To, kUnits>(a, s)
                : rows == kPairs ? fwd_tiles<Tx, Tg, To, kPairs>(a, s) : fwd_tiles<Tx, Tg, To, kAnywhere>(a, s);
     });
 }
 
-cudaError_t launch_scan_bwd(ScanArgs a, int dtype, cudaStream_t s)
+cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, bool alone, cudaStream_t s)
 {
-    const Share share = share_out(a);
-    a.alone = share.rows;
     return by_types(dtype, [&](auto x, auto g, auto o) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
         const Rows rows = std::max({rows_of(a.ldg, a.D, sizeof(Tg)), rows_of(a.D, a.D, sizeof(To)),
                                     rows_of(a.lddx, a.D, sizeof(Tx)), rows_of(a.lddg, a.D, sizeof(Tg))});
-        if (share.rows >= 0) {
+        if (alone) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
             if (rows != kAnywhere)
                 scan_bwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
             else
                 scan_bwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            const cudaError_t e = cudaGetLastError();
-            if (e != cudaSuccess || !share.tiles)
-                return e;
+            return cudaGetLastError();
         }
         return rows == kUnits ? bwd_tiles<Tx, Tg, To, kUnits>(a, s)
                : rows == kPairs ? bwd_tiles<Tx, Tg, To, kPairs>(a, s) : bwd_tiles<Tx, Tg, To, kAnywhere>(a, s);

@@ -315,11 +315,13 @@ size_t gla_wy_workspace_size(int T, int N, int chunk, int varlen);
  *               GLA_F16_GF32 (f16, f32, f32)
  *   workspace   gla_scan_workspace_size() bytes, 256-byte aligned, zeroed before first use: the status word.  A
  *               sequence with bad offsets (cu_seqlens must run from 0 to T without decreasing) is reported there
- *               (gla_get_status) and skipped
+ *               (gla_get_status) and skipped; a bounded wait that ran out is reported as GLA_ERR_TIMEOUT (the
+ *               outputs of that call are then void)
  *
  * g is usually <= 0 but may be any value: the recurrence is evaluated as written, and infinities and NaN spread as
  * they would step by step, except that a segment's total decay multiplies the state that enters it (a state of
- * infinity that meets a total decay of 0 becomes NaN).  Results do not depend on timing (no atomics).
+ * infinity that meets a total decay of 0 becomes NaN).  A decay is within 2^-22 + |g| 2^-24 (relative) of exp(g).
+ * Results do not depend on timing (no atomics).
  */
 int gla_scan_fwd(const void *x, const void *g, void *h, const float *h0, float *ht, const int32_t *cu_seqlens, int N,
                  int B, int T, int D, int64_t ldx, int64_t ldg, int dtype, void *workspace, size_t workspace_bytes,

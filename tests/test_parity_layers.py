@@ -622,7 +622,12 @@ def test_binding_refusals(B):
 def test_kernel_names(B):
     x, w = torch.randn(2, 40, 64, device="cuda"), torch.ones(64, device="cuda")
     timer = B.KernelTimer()
-    for call, names in ((lambda: B.scan_fwd(x, -x.abs()), ["scan_fwd"]), (lambda: B.scan_bwd(x, x, x), ["scan_bwd"]),
+    cu = torch.arange(0, 2001, 2, dtype=torch.int32, device="cuda")   # enough sequences for both kernels
+    pack = torch.randn(1, 2000, 128, device="cuda")
+    for call, names in ((lambda: B.scan_fwd(pack, -pack.abs(), cu_seqlens=cu), ["scan_fwd_rows", "scan_fwd"]),
+                        (lambda: B.scan_bwd(pack, pack, pack, cu_seqlens=cu), ["scan_bwd_rows", "scan_bwd"]),
+                        (lambda: B.scan_fwd(x[:, :9].contiguous(), x[:, :9].contiguous()), ["scan_fwd_rows"]),
+                        (lambda: B.scan_fwd(x, -x.abs()), ["scan_fwd"]), (lambda: B.scan_bwd(x, x, x), ["scan_bwd"]),
                         (lambda: B.scan_step(x[0], x[0], x[0].clone()), ["scan_step"]),
                         (lambda: B.gla_step(x, x, x, x, torch.zeros(2, 40, 64, 64, device="cuda")), ["gla_step"]),
                         (lambda: B.norm_fwd(x, weight=w), ["norm_fwd"]),
