@@ -333,6 +333,7 @@ __global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) n
 {
     constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
     __shared__ Told told[2][16];
+    tc::grid_dep_wait();
     const int l = threadIdx.x % sp.lanes;
     const Tx *x_in = static_cast<const Tx *>(a.x);
     const Tr *res_in = static_cast<const Tr *>(a.res);
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     constexpr bool kEarly = sizeof(Tr) == 2;   // registers for the next row beside the present one
     __shared__ Told told[2][16];
     __shared__ float acc[kThreads * kHeld];
+    tc::grid_dep_wait();
     const int l = threadIdx.x % sp.lanes, D = a.D;
     const Tr *s_in = static_cast<const Tr *>(a.s_in), *ds_in = static_cast<const Tr *>(a.ds);
     const Tx *dy_in = static_cast<const Tx *>(a.dy);
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_wide(NormArgs a)
 __global__ void __launch_bounds__(1024) norm_dw_kernel(NormArgs a)
 {
     __shared__ float sh[32][33];
-    tc::grid_dep_wait();   // launched while norm_bwd's last CTAs still run
+    tc::grid_dep_wait();
     const int c = threadIdx.x % 32, k = threadIdx.x / 32, d = blockIdx.x * 32 + c;
     float sum = 0.f;
     if (d < a.D)
@@ -699,8 +701,7 @@ cudaError_t fwd_rows(const NormArgs &a, cudaStream_t s)
             per_sm = 1;
         known.store(per_sm, std::memory_order_relaxed);
     }
-    kernel<<<grid_of(a.rows, sp, per_sm), sp.threads, 0, s>>>(a, sp);
-    return cudaGetLastError();
+    return launch_early(kernel, grid_of(a.rows, sp, per_sm), sp.threads, s, a, sp);
 }
 
 template <typename Tx, typename Tr, Quant Q>
@@ -744,25 +745,16 @@ cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
         if (wide(a.D, 16 / sizeof(Tx)))
             norm_bwd_wide<Tx, Tr><<<a.ctas, kThreads, 0, s>>>(a);
         else if (a.D % (16 / (int)sizeof(Tx)))
-            norm_bwd_rows<Tx, Tr, true><<<a.ctas, sp.threads, 0, s>>>(a, sp);
+            return launch_early(norm_bwd_rows<Tx, Tr, true>, a.ctas, sp.threads, s, a, sp);
         else
-            norm_bwd_rows<Tx, Tr, false><<<a.ctas, sp.threads, 0, s>>>(a, sp);
+            return launch_early(norm_bwd_rows<Tx, Tr, false>, a.ctas, sp.threads, s, a, sp);
         return cudaGetLastError();
     });
 }
 
 cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.D + 31) / 32);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_dw_kernel, a);
+    return launch_early(norm_dw_kernel, (a.D + 31) / 32, 1024, s, a);
 }
 
 }  // namespace gla

@@ -556,6 +556,7 @@ constexpr int kAhead = 8;
 template <typename Tx, typename Tg, typename To, bool PAIRED>
 __global__ void __launch_bounds__(128) scan_fwd_rows(ScanArgs a, int tiles)
 {
+    tc::grid_dep_wait();
     const int n = blockIdx.x / tiles, c = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5), d0 = c * kCols;
     int64_t begin;
     int len;
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(128) scan_fwd_rows(ScanArgs a, int tiles)
 template <typename Tx, typename Tg, typename To, bool PAIRED>
 __global__ void __launch_bounds__(128) scan_bwd_rows(ScanArgs a, int tiles)
 {
+    tc::grid_dep_wait();
     const int n = blockIdx.x / tiles, c = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5), d0 = c * kCols;
     int64_t begin;
     int len;
@@ -756,11 +758,8 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, int dtype, bool alone, cudaStream
         const Rows rows = std::max(rows_of(a.ldx, a.D, sizeof(Tx)), rows_of(a.ldg, a.D, sizeof(Tg)));
         if (alone) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
-            if (rows != kAnywhere)
-                scan_fwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            else
-                scan_fwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            return cudaGetLastError();
+            return rows != kAnywhere ? launch_early(scan_fwd_rows<Tx, Tg, To, true>, a.N * tiles, 128, s, a, tiles)
+                                     : launch_early(scan_fwd_rows<Tx, Tg, To, false>, a.N * tiles, 128, s, a, tiles);
         }
         return rows == kUnits ? fwd_tiles<Tx, Tg, To, kUnits>(a, s)
                : rows == kPairs ? fwd_tiles<Tx, Tg, To, kPairs>(a, s) : fwd_tiles<Tx, Tg, To, kAnywhere>(a, s);
@@ -777,11 +776,8 @@ cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, bool alone, cudaStream
                                     rows_of(a.lddx, a.D, sizeof(Tx)), rows_of(a.lddg, a.D, sizeof(Tg))});
         if (alone) {
             const int tiles = (a.D + 4 * kCols - 1) / (4 * kCols);
-            if (rows != kAnywhere)
-                scan_bwd_rows<Tx, Tg, To, true><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            else
-                scan_bwd_rows<Tx, Tg, To, false><<<a.N * tiles, 128, 0, s>>>(a, tiles);
-            return cudaGetLastError();
+            return rows != kAnywhere ? launch_early(scan_bwd_rows<Tx, Tg, To, true>, a.N * tiles, 128, s, a, tiles)
+                                     : launch_early(scan_bwd_rows<Tx, Tg, To, false>, a.N * tiles, 128, s, a, tiles);
         }
         return rows == kUnits ? bwd_tiles<Tx, Tg, To, kUnits>(a, s)
                : rows == kPairs ? bwd_tiles<Tx, Tg, To, kPairs>(a, s) : bwd_tiles<Tx, Tg, To, kAnywhere>(a, s);

@@ -4,6 +4,7 @@
 
 #include "gla_internal.h"
 #include "layer_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gla {
 namespace {
@@ -38,6 +39,7 @@ struct alignas(4 * sizeof(T)) Four {
 template <typename Tx, typename Tg, typename To, bool FOUR>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(StepArgs a, int tiles)
 {
+    tc::grid_dep_wait();
     const int b = blockIdx.x / tiles, d = (blockIdx.x - b * tiles) * 4 * kThreads + threadIdx.x * (FOUR ? 4 : 1);
     const int s = state_of(a, b);
     const Tx *x = static_cast<const Tx *>(a.x) + b * a.ldx + d;
@@ -90,6 +92,7 @@ __global__ void __launch_bounds__(kThreads) gla_step_kernel(StepArgs a, int tile
     constexpr int kRows = kThreads / 8, kTurns = K / kRows;   // rows of a turn
     __shared__ float4 akq[K];                                 // decay, key and query of each row
     __shared__ float4 part[kThreads / 32][8];
+    tc::grid_dep_wait();
     const int bh = blockIdx.x / tiles, b = bh / a.H, head = bh - b * a.H;
     const int lane8 = threadIdx.x % 8, row0 = threadIdx.x / 8, c = (blockIdx.x - bh * tiles) * kCols + 4 * lane8;
     const int slot = state_of(a, b);
@@ -152,10 +155,9 @@ cudaError_t launch_scan_step(const StepArgs &a, int dtype, cudaStream_t s)
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
         if (four)
-            scan_step_kernel<Tx, Tg, To, true><<<a.B * tiles, kThreads, 0, s>>>(a, tiles);
+            return launch_early(scan_step_kernel<Tx, Tg, To, true>, a.B * tiles, kThreads, s, a, tiles);
         else
-            scan_step_kernel<Tx, Tg, To, false><<<a.B * tiles, kThreads, 0, s>>>(a, tiles);
-        return cudaGetLastError();
+            return launch_early(scan_step_kernel<Tx, Tg, To, false>, a.B * tiles, kThreads, s, a, tiles);
     });
 }
 
@@ -167,10 +169,9 @@ cudaError_t launch_gla_step(const StepArgs &a, int dtype, cudaStream_t s)
         typedef std::remove_pointer_t<decltype(g)> Tg;
         typedef std::remove_pointer_t<decltype(o)> To;
         if (a.K == 128)
-            gla_step_kernel<Tx, Tg, To, 128><<<a.B * a.H * tiles, kThreads, 0, s>>>(a, tiles);
+            return launch_early(gla_step_kernel<Tx, Tg, To, 128>, a.B * a.H * tiles, kThreads, s, a, tiles);
         else
-            gla_step_kernel<Tx, Tg, To, 64><<<a.B * a.H * tiles, kThreads, 0, s>>>(a, tiles);
-        return cudaGetLastError();
+            return launch_early(gla_step_kernel<Tx, Tg, To, 64>, a.B * a.H * tiles, kThreads, s, a, tiles);
     });
 }
 
