@@ -10,9 +10,10 @@
 // go value by value.  Rows a multiple of VEC apart have the same k, so a thread keeps its columns (and its weights).
 //
 // Bound by HBM: 65536 rows of 4096 columns in 16 bits with a residual 335 us (6.4 TB/s), e4m3 in groups of 128 with an
-// fp32 residual, 16384 x 2048, 58 us (6.4), the backward of 32768 x 2048 89 us (6.0), rows of 1001 columns 94 us (5.6)
-// and 134 us (3.9).  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower (86 -> 93 us
-// at 65536 x 1024).
+// fp32 residual, 16384 x 2048, 57 us (6.5), the backward of 32768 x 2048 89 us (6.0), 65536 rows of 1001 columns 85 us
+// (6.2), their backward 105 us (5.0).  Groups of 128 of shifted rows are bound by instructions: 146 us at 65536 x 1001,
+// where 65536 x 1000 takes 72 us.  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower
+// (86 -> 93 us at 65536 x 1024).
 #include <algorithm>
 #include <atomic>
 
@@ -35,6 +36,17 @@ __device__ __forceinline__ float max_nan(float a, float b)
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+
+// 1 / v to a unit in the last place.
+__device__ __forceinline__ float reciprocal(float v)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The scale of values of which the largest is `most`.
+__device__ __forceinline__ float scale_of(float most) { return max_nan(most * (1.f / kE4m3Max), kScaleMin); }
 
 // Threads of a row and rows of a CTA.
 struct Split {
@@ -67,10 +79,44 @@ struct Place {
 template <int VEC, bool SHIFTED>
 __device__ __forceinline__ bool over(int c, int D) { return SHIFTED && (c < 0 || c + VEC > D); }   // the vector at c
 
+// Stores the values of a vector of eight (E; two of them a P, four a Q) at column c that lie in [0, D), in at most three
+// pieces: those past its first k are a piece of one where k is odd, then one of two, then the last four.
+template <typename E, typename P, typename Q>
+__device__ __forceinline__ void put_end(E *p, Q lo, Q hi, int c, int D)
+{
+    auto from = [&](int i) { return (i < 4 ? lo : hi) >> (8 * sizeof(E) * (i & 3)); };
+    if (c < 0 && c + 8 > D) {
+        for (int i = -c; i < D - c; ++i)
+            p[i] = (E)from(i);
+    } else if (c < 0) {
+        int k = -c;
+        if (k & 1) {
+            p[k] = (E)from(k);
+            ++k;
+        }
+        if (k & 2) {
+            *reinterpret_cast<P *>(p + k) = (P)from(k);
+            k += 2;
+        }
+        if (k == 4)
+            *reinterpret_cast<Q *>(p + 4) = hi;
+    } else if (c < D) {
+        const int e = D - c;
+        if (e & 4)
+            *reinterpret_cast<Q *>(p) = lo;
+        if (e & 2)
+            *reinterpret_cast<P *>(p + (e & 4)) = (P)from(e & 4);
+        if (e & 1)
+            p[e - 1] = (E)from(e - 1);
+    }
+}
+
 // A thread's part of a row as it lies in memory: N vectors of VEC values.  SHIFTED: some vectors hang over the row's
 // ends.  Of 32-bit values they are loaded one by one.  Of 16-bit values, two a register, that would make every load wait
-// to be put together; they are loaded like the others (their other values are the neighbouring rows') and mended when
-// they are used, and what would reach over the tensor's end is loaded only then.
+// to be put together; they are loaded like the others (their other values are the neighbouring rows') and masked when
+// they are used, and what would reach over the tensor's end is loaded only then.  Masks kept in registers and ends
+// stored in pieces of one, two and four took 65536 x 1001 from 93 to 85 us, its backward from 138 to 105, against a
+// test for each value.
 template <typename T, int VEC, bool SHIFTED>
 struct Part {
     static constexpr int N = kHeld / VEC;
@@ -93,19 +139,21 @@ struct Part {
                     ok ? reinterpret_cast<const uint4 *>(p + at.at + col[j])[i] : make_uint4(0, 0, 0, 0);
         }
     }
-    __device__ __forceinline__ void mend(const T *p, const Place &at, const int (&col)[N])
+    // Zeros for what is not the row's (`keep`: see keep_own), and the values that `load` left out at the tensor's end.
+    __device__ __forceinline__ void mend(const T *p, const Place &at, const int (&col)[N], const uint32_t (&keep)[kHeld / 2])
     {
+        if constexpr (!kOneByOne) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (!kOneByOne && over<VEC, SHIFTED>(col[j], at.D)) {
-                const bool late = at.at + col[j] + VEC > at.end;
+            for (int i = 0; i < kHeld / 2; ++i)
+                reinterpret_cast<uint32_t *>(v)[i] &= keep[i];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if ((unsigned)(col[j] + i) >= (unsigned)at.D)
-                        v[j * VEC + i] = T(0.f);
-                    else if (late)
-                        v[j * VEC + i] = p[at.at + col[j] + i];
-            }
+            for (int j = 0; j < N; ++j)
+                if (col[j] < at.D && at.at + col[j] + VEC > at.end)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if ((unsigned)(col[j] + i) < (unsigned)at.D)
+                            v[j * VEC + i] = p[at.at + col[j] + i];
+        }
     }
     __device__ __forceinline__ void zero()
     {
@@ -134,10 +182,15 @@ struct Part {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             if (over<VEC, SHIFTED>(col[j], at.D)) {
+                if constexpr (sizeof(T) == 2 && VEC == 8) {
+                    const uint64_t *half = reinterpret_cast<const uint64_t *>(v + j * VEC);
+                    put_end<uint16_t, uint32_t>(reinterpret_cast<uint16_t *>(p + at.at + col[j]), half[0], half[1], col[j], at.D);
+                } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if ((unsigned)(col[j] + i) < (unsigned)at.D)
-                        p[at.at + col[j] + i] = v[j * VEC + i];
+                    for (int i = 0; i < VEC; ++i)
+                        if ((unsigned)(col[j] + i) < (unsigned)at.D)
+                            p[at.at + col[j] + i] = v[j * VEC + i];
+                }
             } else if (col[j] < at.D) {
 #pragma unroll
                 for (int i = 0; i < VEC * (int)sizeof(T) / 16; ++i)
@@ -157,6 +210,16 @@ __device__ __forceinline__ void columns(int (&col)[kHeld / VEC], int l, int lane
         col[j] = (lanes < 32 ? j * lanes + l : (l / 32 * N + j) * 32 + l % 32) * VEC - k;
 }
 
+// Masks of a thread's 16-bit values, two a word, that are its row's own.
+template <int VEC>
+__device__ __forceinline__ void keep_own(uint32_t (&keep)[kHeld / 2], const int (&col)[kHeld / VEC], int D)
+{
+    auto own = [&](int i) { return (unsigned)(col[i / VEC] + i % VEC) < (unsigned)D; };
+#pragma unroll
+    for (int i = 0; i < kHeld / 2; ++i)
+        keep[i] = (own(2 * i) ? 0xffffu : 0u) | (own(2 * i + 1) ? 0xffff0000u : 0u);
+}
+
 template <int VEC>
 __device__ __forceinline__ void load_weights(float2 (&w)[kHeld / 2], const float *p, const int (&col)[kHeld / VEC], int D)
 {
@@ -167,6 +230,13 @@ __device__ __forceinline__ void load_weights(float2 (&w)[kHeld / 2], const float
 #pragma unroll
     for (int i = 0; i < kHeld / 2; ++i)
         w[i] = make_float2(one(2 * i), one(2 * i + 1));
+}
+
+// Over a warp, in one instruction: 92 -> 87 us for e4m3 rows of 65536 x 1001 against five exchanges.
+__device__ __forceinline__ float max_warp(float m)
+{
+    asm volatile("redux.sync.max.NaN.f32 %0, %0, -1;" : "+f"(m));
+    return m;
 }
 
 __device__ __forceinline__ float max_lanes(float m, int lanes)   // over groups of so many adjacent lanes
@@ -190,7 +260,7 @@ __device__ __forceinline__ void reduce_row(Told &t, int lanes, Told *told)
     for (int m = min(lanes, 32) / 2; m; m >>= 1)
         t.sum += __shfl_xor_sync(~0u, t.sum, m);
     if (MAX)
-        t.most = max_lanes(t.most, min(lanes, 32));
+        t.most = lanes >= 32 ? max_warp(t.most) : max_lanes(t.most, min(lanes, 32));
     if (lanes <= 32)
         return;
     const int warp = threadIdx.x / 32, count = lanes / 32, first = warp / count * count;
@@ -243,7 +313,7 @@ struct Groups {
                 else
                     m[j] = max_nan(m[j], size(j * VEC + i));
             }
-            m[j] = max_lanes(m[j], G);
+            m[j] = G == 32 ? max_warp(m[j]) : max_lanes(m[j], G);
         }
         t.head = before[0];                                   // lane 0's is what counts
         t.last = __shfl_sync(~0u, m[N - 1], 31);
@@ -261,14 +331,14 @@ struct Groups {
     // reciprocals, of the vectors' own columns and of the k before.
     __device__ __forceinline__ void scale(float *out, int groups, float rstd, int l, int lanes, int k, const Told *told)
     {
-        auto of = [&](float most) { return max_nan(most * rstd / kE4m3Max, kScaleMin); };
+        auto of = [&](float most) { return scale_of(most * rstd); };
         if (lanes < 32) {
 #pragma unroll
             for (int g = 0; g < kFew; ++g) {
                 m[g] = of(m[g]);
                 if (l == 0 && g < groups)
                     out[g] = m[g];
-                m[g] = 1.f / m[g];
+                m[g] = reciprocal(m[g]);
             }
             return;
         }
@@ -286,13 +356,13 @@ struct Groups {
             const int g = (in_row * N + j) * (32 / G) + lane / G;
             if (lane % G == 0 && g < groups)
                 out[g] = m[j];
-            m[j] = 1.f / m[j];
+            m[j] = reciprocal(m[j]);
         }
         if (k) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float down = __shfl_sync(~0u, m[j], 0);   // first group of this block
-                const float back = j ? __shfl_sync(~0u, m[j ? j - 1 : 0], 31) : 1.f / of(prior);   // last before it
+                const float back = j ? __shfl_sync(~0u, m[j ? j - 1 : 0], 31) : reciprocal(of(prior));   // last before it
                 before[j] = lane >= G ? down : back;
             }
         }
@@ -314,10 +384,15 @@ __device__ __forceinline__ void put_e4m3(uint8_t *p, const Place &at, int c, con
     for (int i = 0; i < VEC / 2; ++i)
         b[i] = __nv_cvt_float2_to_fp8x2(v[i], __NV_SATFINITE, __NV_E4M3);
     if (over<VEC, SHIFTED>(c, at.D)) {
+        if constexpr (VEC == 8) {
+            const uint32_t *half = reinterpret_cast<const uint32_t *>(b);
+            put_end<uint8_t, uint16_t>(p + at.at + c, half[0], half[1], c, at.D);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if ((unsigned)(c + i) < (unsigned)at.D)
-                p[at.at + c + i] = reinterpret_cast<const uint8_t *>(b)[i];
+            for (int i = 0; i < VEC; ++i)
+                if ((unsigned)(c + i) < (unsigned)at.D)
+                    p[at.at + c + i] = reinterpret_cast<const uint8_t *>(b)[i];
+        }
     } else if (c < at.D) {
         if constexpr (VEC == 8)
             *reinterpret_cast<uint2 *>(p + at.at + c) = *reinterpret_cast<const uint2 *>(b);
@@ -328,8 +403,12 @@ __device__ __forceinline__ void put_e4m3(uint8_t *p, const Place &at, int c, con
 
 enum Quant { kPlain, kByRow, kByGroup };
 
+// Registers: as many as hold the row and the next one without spilling.  Groups of unshifted 16-bit rows go faster with
+// three CTAs of 256 threads, at 80, than with two, at 96 (81 -> 72 us at 65536 x 1000, though 78 -> 81 at 29127 x 2304);
+// those of shifted rows do not (146 -> 152 us at 65536 x 1001).
 template <typename Tx, typename Tr, Quant Q, bool SHIFTED>
-__global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) norm_fwd_rows(NormArgs a, Split sp)
+__global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup && SHIFTED ? 96 : 80) : Q == kByRow ? 128 : 112)
+norm_fwd_rows(NormArgs a, Split sp)
 {
     constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
     __shared__ Told told[2][16];
@@ -343,6 +422,8 @@ __global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) n
     Place at = {row * a.D, a.D, a.rows * a.D};
     int col[N];
     columns<VEC>(col, l, sp.lanes, k);
+    uint32_t keep[kHeld / 2];
+    keep_own<VEC>(keep, col, a.D);
     Part<Tx, VEC, SHIFTED> x;
     Part<Tr, VEC, SHIFTED> res;
     res.zero();
@@ -365,9 +446,9 @@ __global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) n
         const bool on = row < a.rows;
         at.at = row * a.D;
         if (SHIFTED && on) {
-            x.mend(x_in, at, col);
+            x.mend(x_in, at, col, keep);
             if (res_in)
-                res.mend(res_in, at, col);
+                res.mend(res_in, at, col, keep);
         }
         float2 v[kHeld / 2], sq = make_float2(0.f, 0.f);
         Told t = {};
@@ -411,7 +492,7 @@ __global__ void __maxnreg__(sizeof(Tr) == 2 ? (Q == kByGroup ? 96 : 80) : 112) n
                 y.store(static_cast<Tx *>(a.y), at, col);
         } else {
             if constexpr (Q == kByRow) {
-                const float scale = max_nan(t.most * rstd / kE4m3Max, kScaleMin), inv = 1.f / scale;
+                const float scale = scale_of(t.most * rstd), inv = reciprocal(scale);
                 if (on && l == 0)
                     a.scales[row - stride] = scale;
 #pragma unroll
@@ -451,6 +532,8 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     Place at = {row * D, D, a.rows * D};
     int col[N];
     columns<VEC>(col, l, sp.lanes, SHIFTED ? (int)(row * D % VEC) : 0);
+    uint32_t keep[kHeld / 2];
+    keep_own<VEC>(keep, col, D);
     Part<Tr, VEC, SHIFTED> s, ds;
     Part<Tx, VEC, SHIFTED> dy;
     float rstd = 0.f;
@@ -482,10 +565,10 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
         const bool on = row < a.rows;
         at.at = row * D;
         if (SHIFTED && on) {
-            s.mend(s_in, at, col);
-            dy.mend(dy_in, at, col);
+            s.mend(s_in, at, col, keep);
+            dy.mend(dy_in, at, col, keep);
             if (ds_in)
-                ds.mend(ds_in, at, col);
+                ds.mend(ds_in, at, col, keep);
         }
         const float r = rstd;
         float2 n[kHeld / 2], g[kHeld / 2], up[kHeld / 2], c = make_float2(0.f, 0.f);
@@ -595,8 +678,8 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_wide(NormArgs a)
                 float m = 0.f;
                 for (int d = lo + threadIdx.x; d < hi; d += kThreads)
                     m = max_nan(m, fabsf(normed(d)));
-                const float scale = max_nan(block_reduce(m, sh, max_nan) / kE4m3Max, kScaleMin);
-                inv = 1.f / scale;
+                const float scale = scale_of(block_reduce(m, sh, max_nan));
+                inv = reciprocal(scale);
                 if (threadIdx.x == 0)
                     a.scales[row * groups + c] = scale;
             }
@@ -732,7 +815,7 @@ cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
             return cudaGetLastError();
         }
         return !a.scales ? fwd<Tx, Tr, kPlain>(a, s)
-               : a.group ? fwd<Tx, Tr, kByGroup>(a, s) : fwd<Tx, Tr, kByRow>(a, s);
+               : a.group && a.group < a.D ? fwd<Tx, Tr, kByGroup>(a, s) : fwd<Tx, Tr, kByRow>(a, s);
     });
 }
 

@@ -452,6 +452,34 @@ def test_norm_shifted_rows(B, rows, D, types):
     test_norm_backward(B, rows, D, types)
 
 
+@pytest.mark.parametrize("types", [(TB, TB), (TH, T32), (T32, T32)], ids=lambda t: "-".join(KIND[x] for x in t))
+@pytest.mark.parametrize("rows,D", [(2, 3), (3, 1), (7, 2), (11, 3), (2, 5)])
+def test_norm_rows_shorter_than_a_unit(B, rows, D, types):
+    """Several rows in one 16-byte unit, the tensor's end inside it."""
+    test_norm_forward(B, rows, D, types)
+    test_norm_backward(B, rows, D, types)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("tx", [TB, T32], ids=KIND.get)
+@pytest.mark.parametrize("D", [3, 203, 1001])
+def test_norm_shifted_rows_beside_nan(B, D, tx, group):
+    """What a row reads of its neighbours' 16-byte units does not reach it: ordinary rows keep their bits."""
+    x, res, w = (t.cuda() for t in norm_inputs(tx, tx, 9, D, seed=33))
+    ok = torch.arange(9) % 2 == 0
+
+    def run():
+        y, s, rstd = B.norm_fwd(x, residual=res, weight=w)
+        q, scales, _, _ = B.norm_quant_fwd(x, residual=res, weight=w, group=group)
+        dx, _, _ = B.norm_bwd(s, rstd, x, weight=w, ds=res)
+        return [t[ok] for t in (y, s, rstd, q.view(torch.uint8), scales, dx)]
+
+    clean = run()
+    x[~ok], res[~ok] = float("nan"), float("inf")
+    for a, b in zip(clean, run()):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("rows,D", [(20011, 136), (3001, 1024)])
 def test_norm_backward_many_rows(B, rows, D):
     dy, s, w = norm_inputs(TB, TB, rows, D, seed=23)
