@@ -84,79 +84,86 @@ __device__ __forceinline__ bool sequence_rows(const ScanArgs &a, int n, int64_t 
 // How rows lie in memory: on whole 16-byte units; elsewhere, but with their channels in whole pairs; anywhere.
 enum Rows { kUnits, kPairs, kAnywhere };
 
-// One R x kCols tile of a row-strided tensor in shared memory.  Rows on whole 16-byte units lie as they are; others are
-// copied from the unit that holds their first byte, so every row has a shift of its own.
-template <typename T, int R, Rows ROWS>
+// One R x kCols tile of a row-strided tensor in shared memory: row j is row r0 + DIR j of the sequence.  Rows on whole
+// 16-byte units lie as they are.  Others start anywhere in a unit and are copied by units, from the one that holds their
+// first byte; their pitch in shared memory differs from the step in memory by a multiple of 16, so that every row
+// starts as far into a unit as in memory and row j is found at a fixed step from row 0 (an address worked out for each
+// row and copy was 17% more instructions; 16 bits, 2 x 8192 rows of 1539 channels: forward 50 -> 47 us,
+// with twelve rows a thread the backward 86 -> 74).
+template <typename T, int R, Rows ROWS, int DIR>
 struct Tile {
-    static constexpr int kWhole = kCols * (int)sizeof(T) / 16, kRow = kWhole + (ROWS == kUnits ? 0 : 1);   // units
-    static constexpr int kPitch = kRow * 16;
-    static constexpr int kBytes = R * kPitch;
+    static constexpr int kElem = (int)sizeof(T), kWhole = kCols * kElem / 16;   // units of a row that starts on one
+    static constexpr int kPitch = 16 * kWhole + (ROWS == kUnits ? 0 : 16);      // the least pitch
+    static constexpr int kBytes = ROWS == kUnits ? R * kPitch : (R * (kPitch + 16 - kElem) + 31) / 16 * 16;
+    const T *src;     // the sequence's first row at the tile's first channel
+    int64_t ld;       // bytes between rows
+    int pitch;
 
-    // Row j of the tile is row r0 + DIR j of the sequence (src: its first row at the tile's first channel); rows
-    // outside [0, len) and channels from `cols` on are zeros.  A thread copies from one 16-byte column of the tile.
-    template <int DIR>
-    static __device__ __forceinline__ void load(char *dst, const T *src, int64_t ld, int r0, int len, int cols)
+    __device__ __forceinline__ Tile(const T *src, int64_t stride)
+        : src(src), ld(stride * kElem), pitch(ROWS == kUnits ? kPitch : kPitch + (int)(DIR * ld & 15)) {}
+    // Bytes into a unit at which row r starts (only the low bits of its address count).
+    __device__ __forceinline__ int shift(int r) const
     {
-        constexpr int kStep = kThreads / kRow;   // rows between a thread's copies
-        const int u = threadIdx.x % kRow, j0 = threadIdx.x / kRow;
-        const bool all = cols >= kCols && (unsigned)r0 < (unsigned)len && (unsigned)(r0 + DIR * (R - 1)) < (unsigned)len;
-        const char *p = reinterpret_cast<const char *>(src) + (int64_t)(r0 + DIR * j0) * ld * (int)sizeof(T);
-        const int64_t step = (int64_t)DIR * kStep * ld * (int)sizeof(T);
-        char *q = dst + j0 * kPitch + 16 * u;
-        if constexpr (ROWS == kUnits) {
-            p += 16 * u;
-            if (all) {
+        return ROWS == kUnits ? 0 : (int)(((uint32_t)reinterpret_cast<uintptr_t>(src) + (uint32_t)r * (uint32_t)ld) & 15);
+    }
+
+    // Rows outside [0, len) are zeros; channels from `cols` on are anything.  A thread copies from one unit of the rows
+    // kStep apart, which start equally far into a unit; the units past kWhole that shifted rows end in go one a thread.
+    __device__ __forceinline__ void load(char *dst, int r0, int len, int cols) const
+    {
+        constexpr int kStep = kThreads / kWhole;
+        static_assert(R % kStep == 0 && kStep * kElem % 16 == 0 && R <= kThreads);
+        const char *base = reinterpret_cast<const char *>(src);
+        const int lead = shift(r0), width = min(kCols, cols) * kElem;
+        const bool all = (unsigned)r0 < (unsigned)len && (unsigned)(r0 + DIR * (R - 1)) < (unsigned)len;
+        auto unit = [&](int j) { return dst + ((lead + j * pitch) & ~15); };   // row j's first
+        auto bytes = [&](int sh, int u) { return max(0, min(16, sh + width - 16 * u)); };
+        const int u = threadIdx.x % kWhole, j0 = threadIdx.x / kWhole, r = r0 + DIR * j0, sh = shift(r), n = bytes(sh, u);
+        const char *p = base + r * ld - sh + 16 * u;
+        const int64_t step = (int64_t)DIR * kStep * ld;
+        char *q = unit(j0) + 16 * u;
+        if (ROWS == kUnits && all && cols >= kCols) {
+#pragma unroll
+            for (int j = 0; j < R; j += kStep)
+                copy16(q + j * pitch, p + j / kStep * step);
+        } else if (ROWS != kUnits && all) {
+            if (n > 0)
 #pragma unroll
                 for (int j = 0; j < R; j += kStep)
-                    copy16(q + j * kPitch, p + j / kStep * step);
-                return;
-            }
-            const bool in = 16 * u < cols * (int)sizeof(T);
+                    copy16(q + j * pitch, p + j / kStep * step, n);
+        } else {
 #pragma unroll
             for (int j = 0; j < R; j += kStep) {
-                const bool ok = in && (unsigned)(r0 + DIR * (j0 + j)) < (unsigned)len;
-                copy16(q, ok ? p : reinterpret_cast<const char *>(src) - (reinterpret_cast<uintptr_t>(src) & 15), ok ? 16 : 0);
+                const bool ok = n > 0 && (unsigned)(r + DIR * j) < (unsigned)len;
+                copy16(q + j * pitch, ok ? p : base - shift(0), ok ? n : 0);
                 p += step;
-                q += kStep * kPitch;
             }
-        } else {
-            if (j0 >= kStep)
-                return;
-            const int width = min(kCols, cols) * (int)sizeof(T);
-#pragma unroll
-            for (int j = 0; j < (R + kStep - 1) / kStep * kStep; j += kStep) {
-                const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-                if (R % kStep == 0 || j0 + j < R) {
-                    if (all) {   // the last unit holds as many bytes of the row as its first bytes are shifted by
-                        const int bytes = u < kWhole ? 16 : shift;
-                        copy16(q, p - shift + (bytes ? 16 * u : 0), bytes);
-                    } else {
-                        const bool ok = (unsigned)(r0 + DIR * (j0 + j)) < (unsigned)len;
-                        const int bytes = ok ? max(0, min(16, shift + width - 16 * u)) : 0;
-                        const char *from = ok ? p : reinterpret_cast<const char *>(src);
-                        copy16(q, from - (reinterpret_cast<uintptr_t>(from) & 15) + (bytes ? 16 * u : 0), bytes);
-                    }
-                }
-                p += step;
-                q += kStep * kPitch;
-            }
+        }
+        if (ROWS != kUnits && threadIdx.x < R) {
+            const int j = threadIdx.x, r = r0 + DIR * j, sh = shift(r), n = bytes(sh, kWhole);
+            const bool ok = n > 0 && (all || (unsigned)r < (unsigned)len);
+            if (ok || !all)
+                copy16(unit(j) + 16 * kWhole, ok ? base + r * ld - sh + 16 * kWhole : base - shift(0), ok ? n : 0);
         }
     }
 
-    // The lane's two channels of row j (row r of the sequence): 2 l and 2 l + 1, or l and l + 32 for rows anywhere.
-    static __device__ __forceinline__ float2 read(const char *tile, int j, const T *src, int64_t ld, int r)
+    // Where the tile's rows from j on are, row j being row r of the sequence; then the lane's two channels of the row i
+    // further on: 2 l and 2 l + 1, or l and l + 32 for rows anywhere.
+    __device__ __forceinline__ const char *at(const char *tile, int j, int r) const
     {
         const int lane = threadIdx.x & 31;
-        const char *row = tile + j * kPitch;
-        if constexpr (ROWS != kUnits)   // only the low bits of the address count (rows outside are zeros at any shift)
-            row += ((uint32_t)reinterpret_cast<uintptr_t>(src) + (uint32_t)r * (uint32_t)ld * (uint32_t)sizeof(T)) & 15;
+        return tile + shift(r - DIR * j) + j * pitch + (ROWS == kAnywhere ? kElem : 2 * kElem) * lane;
+    }
+    __device__ __forceinline__ float2 read(const char *rows, int i) const
+    {
+        const char *row = rows + i * pitch;
         if constexpr (ROWS == kAnywhere) {
             const T *p = reinterpret_cast<const T *>(row);
-            return make_float2(widen(p[lane]), widen(p[lane + 32]));
-        } else if constexpr (sizeof(T) == 4) {
-            return *reinterpret_cast<const float2 *>(row + 8 * lane);
+            return make_float2(widen(p[0]), widen(p[32]));
+        } else if constexpr (kElem == 4) {
+            return *reinterpret_cast<const float2 *>(row);
         } else {
-            return widen2<T>(*reinterpret_cast<const uint32_t *>(row + 4 * lane));
+            return widen2<T>(*reinterpret_cast<const uint32_t *>(row));
         }
     }
 };
@@ -332,35 +339,36 @@ __device__ __forceinline__ float2 receive(Shared &sh, const float4 *ctas, float2
 template <typename Tx, typename Tg, typename To, Rows ROWS, int RPT_>
 struct Forward {
     static constexpr int RPT = RPT_, R = kWarps * RPT;
-    typedef Tile<Tx, R, ROWS> TX;
-    typedef Tile<Tg, R, ROWS> TG;
+    typedef Tile<Tx, R, ROWS, 1> TX;
+    typedef Tile<Tg, R, ROWS, 1> TG;
     static constexpr int kStage = TX::kBytes + TG::kBytes;
     typedef Pair<ROWS != kAnywhere> Lane;
     Map row[RPT];
-    const Tx *x;
-    const Tg *g;
+    const TX x;
+    const TG g;
     To *h;
     int len;
     bool full;   // the tile's channels all exist
 
     __device__ __forceinline__ Forward(const ScanArgs &a, int64_t begin, int len, int d0, const Lane &, int64_t)
-        : x(static_cast<const Tx *>(a.x) + begin * a.ldx + d0), g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0),
-          h(static_cast<To *>(a.h) + begin * a.D), len(len), full(d0 + kCols <= a.D) {}
+        : x(static_cast<const Tx *>(a.x) + begin * a.ldx + d0, a.ldx),
+          g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0, a.ldg), h(static_cast<To *>(a.h) + begin * a.D), len(len), full(d0 + kCols <= a.D) {}
     static __device__ __forceinline__ const float *start(const ScanArgs &a) { return a.h0; }
     static __device__ __forceinline__ float *end(const ScanArgs &a) { return a.ht; }
     __device__ __forceinline__ void load(const ScanArgs &a, char *st, int p, int d0) const
     {
-        TX::template load<1>(st, x, a.ldx, p, len, a.D - d0);
-        TG::template load<1>(st + TX::kBytes, g, a.ldg, p, len, a.D - d0);
+        x.load(st, p, len, a.D - d0);
+        g.load(st + TX::kBytes, p, len, a.D - d0);
     }
     // Positions p.. of the walk, rows j.. of the tile.
-    __device__ __forceinline__ Map fold(const ScanArgs &a, const char *st, int p, int j)
+    __device__ __forceinline__ Map fold(const char *st, int p, int j)
     {
+        const char *gs = g.at(st + TX::kBytes, j, p), *xs = x.at(st, j, p);
         Map own;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            row[i].A = decay2(TG::read(st + TX::kBytes, j + i, g, a.ldg, p + i));
-            row[i].H = TX::read(st, j + i, x, a.ldx, p + i);
+            row[i].A = decay2(g.read(gs, i));
+            row[i].H = x.read(xs, i);
             own.then(row[i]);
         }
         return own;
@@ -389,13 +397,13 @@ struct Forward {
 template <typename Tx, typename Tg, typename To, Rows ROWS, int RPT_>
 struct Backward {
     static constexpr int RPT = RPT_, R = kWarps * RPT;
-    typedef Tile<Tg, R, ROWS> TG;
-    typedef Tile<To, R, ROWS> TO;
+    typedef Tile<Tg, R, ROWS, -1> TG;
+    typedef Tile<To, R, ROWS, -1> TO;
     static constexpr int kStage = TG::kBytes + 2 * TO::kBytes;
     typedef Pair<ROWS != kAnywhere> Lane;
     float2 dec[RPT], up[RPT];
-    const Tg *g;
-    const To *h, *dh;
+    const TG g;
+    const TO h, dh;
     Tx *dx;
     Tg *dg;
     int len;
@@ -403,26 +411,28 @@ struct Backward {
     const float2 h0;
 
     __device__ __forceinline__ Backward(const ScanArgs &a, int64_t begin, int len, int d0, const Lane &lane, int64_t state)
-        : g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0), h(static_cast<const To *>(a.h_in) + begin * a.D + d0),
-          dh(static_cast<const To *>(a.dh) + begin * a.D + d0), dx(static_cast<Tx *>(a.dx) + begin * a.lddx),
+        : g(static_cast<const Tg *>(a.g) + begin * a.ldg + d0, a.ldg),
+          h(static_cast<const To *>(a.h_in) + begin * a.D + d0, a.D),
+          dh(static_cast<const To *>(a.dh) + begin * a.D + d0, a.D), dx(static_cast<Tx *>(a.dx) + begin * a.lddx),
           dg(static_cast<Tg *>(a.dg) + begin * a.lddg), len(len), full(d0 + kCols <= a.D), h0(lane.state(a.h0, state)) {}
     static __device__ __forceinline__ const float *start(const ScanArgs &a) { return a.dht; }
     static __device__ __forceinline__ float *end(const ScanArgs &a) { return a.dh0; }
     __device__ __forceinline__ void load(const ScanArgs &a, char *st, int p, int d0) const
     {
         const int r = len - 1 - p;
-        TG::template load<-1>(st, g, a.ldg, r, len, a.D - d0);
-        TO::template load<-1>(st + TG::kBytes, dh, a.D, r, len, a.D - d0);
-        TO::template load<-1>(st + TG::kBytes + TO::kBytes, h, a.D, r - 1, len, a.D - d0);
+        g.load(st, r, len, a.D - d0);
+        dh.load(st + TG::kBytes, r, len, a.D - d0);
+        h.load(st + TG::kBytes + TO::kBytes, r - 1, len, a.D - d0);
     }
-    __device__ __forceinline__ Map fold(const ScanArgs &a, const char *st, int p, int j)
+    __device__ __forceinline__ Map fold(const char *st, int p, int j)
     {
         const int r = len - 1 - p;
+        const char *gs = g.at(st, j, r), *ds = dh.at(st + TG::kBytes, j, r);
         Map own;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            dec[i] = decay2(TG::read(st, j + i, g, a.ldg, r - i));
-            up[i] = TO::read(st + TG::kBytes, j + i, dh, a.D, r - i);
+            dec[i] = decay2(g.read(gs, i));
+            up[i] = dh.read(ds, i);
             own.A = mul2(own.A, dec[i]);
             own.H = mul2(dec[i], add2(own.H, up[i]));
         }
@@ -433,9 +443,10 @@ struct Backward {
     {
         Tx *to_x = dx + (int64_t)r * a.lddx;
         Tg *to_g = dg + (int64_t)r * a.lddg;
+        const char *hs = h.at(st + TG::kBytes + TO::kBytes, j, r - 1);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float2 prev = TO::read(st + TG::kBytes + TO::kBytes, j + i, h, a.D, r - i - 1);
+            float2 prev = h.read(hs, i);
             if (!WHOLE && i == r)
                 prev = h0;
             const float2 lam = add2(up[i], mu);
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_tiles(ScanArgs a, int tiles,
         load(t + STAGES - 1);
         const char *st = smem + t % STAGES * Role::kStage;
         const int p = t * step + rank * R + w * RPT;
-        publish(sh, ctas, role.fold(a, st, p, w * RPT), t, S, rank);
+        publish(sh, ctas, role.fold(st, p, w * RPT), t, S, rank);
         role.emit(a, st, receive(sh, ctas, carry, t, S, rank), p, w * RPT, lane);
     }
     if (Role::end(a) && rank == 0 && w == 0)
@@ -645,7 +656,7 @@ struct Fit {
 // 0.03 for each further CTA.  A last wave costs at least 0.6 of a full one (CTAs that share an SM no longer still wait
 // for their own tiles).  The lengths of a pack differ, which leaves about half a walk at the end.  Measured for 1, 2
 // and 4 CTAs, in us: 256 units of 4096 rows 70, 68, 69 (backward 116, 110, 111); 160 of 4096: 51, 58, 50; 1024 of 1024:
-// 62, 76, 97; 512 of a pack of 128 to 8192 rows: 197, 182, 184.
+// 62, 76, 97; 512 of a pack of 128 to 8192 rows: 197, 182, 184 (at 8 rows a thread; 177 at 16).
 int cluster_size(const int *fit, int64_t units, int64_t rows, int R, bool pack)
 {
     int S = 1;
@@ -722,15 +733,19 @@ Rows rows_of(int64_t ld, int D, int elem)
 template <typename Tx, typename Tg, typename To, Rows ROWS>
 cudaError_t fwd_tiles(const ScanArgs &a, cudaStream_t s)
 {
-    // rows of a thread: the more the fewer exchanges, as registers and shared memory allow for two CTAs an SM
-    return launch_tiles<Forward<Tx, Tg, To, ROWS, sizeof(Tx) + sizeof(Tg) == 4 ? 16 : 8>>(a, s);
+    // Rows of a thread: the more the fewer exchanges, as registers and shared memory allow for two CTAs an SM; better
+    // than a third tile under way (fp32, 5 x 41830 rows of 128 channels: 8 rows 93 us, 12 rows 75).
+    constexpr int kBytes = sizeof(Tx) + sizeof(Tg);
+    return launch_tiles<Forward<Tx, Tg, To, ROWS, ROWS == kUnits ? (kBytes == 8 ? 12 : 16)
+                                                                 : kBytes == 4 ? 16 : kBytes == 6 ? 12 : 10>>(a, s);
 }
 
 template <typename Tx, typename Tg, typename To, Rows ROWS>
 cudaError_t bwd_tiles(const ScanArgs &a, cudaStream_t s)
 {
     constexpr int kBytes = sizeof(Tg) + 2 * sizeof(To);
-    return launch_tiles<Backward<Tx, Tg, To, ROWS, ROWS == kUnits ? (kBytes == 6 ? 16 : 8) : (kBytes == 12 ? 4 : 8)>>(a, s);
+    return launch_tiles<Backward<Tx, Tg, To, ROWS, ROWS == kUnits ? (kBytes == 6 ? 16 : 8)   // likewise
+                                                                  : kBytes == 6 ? 12 : kBytes == 10 ? 8 : 6>>(a, s);
 }
 
 }  // namespace
