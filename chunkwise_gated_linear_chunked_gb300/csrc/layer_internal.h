@@ -147,11 +147,12 @@ __device__ __forceinline__ float decay(float g)
 // threads waits for first thing (grid_dep_wait): about 0.4 us less a kernel in a chain of short ones (gla_step of one
 // sequence and 8 heads in a CUDA graph: 2.05 -> 1.63 us).
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, A... args)
+cudaError_t launch_early_shared(void (*kernel)(P...), unsigned grid, unsigned block, size_t shared, cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -159,6 +160,11 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, cu
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, A... args)
+{
+    return launch_early_shared(kernel, grid, block, 0, s, args...);
 }
 
 // Calls f with null pointers of the (x, gate, output) types of a recurrence dtype code.

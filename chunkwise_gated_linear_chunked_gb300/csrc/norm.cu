@@ -10,8 +10,8 @@
 // go value by value.  Rows a multiple of VEC apart have the same k, so a thread keeps its columns (and its weights).
 //
 // Bound by HBM: 65536 rows of 4096 columns in 16 bits with a residual 335 us (6.4 TB/s), e4m3 in groups of 128 with an
-// fp32 residual, 16384 x 2048, 57 us (6.5), the backward of 32768 x 2048 89 us (6.0), 65536 rows of 1001 columns 85 us
-// (6.2), their backward 105 us (5.0).  Groups of 128 of shifted rows are bound by instructions: 146 us at 65536 x 1001,
+// fp32 residual, 16384 x 2048, 57 us (6.5), the backward of 32768 x 2048 84 us (6.4), 65536 rows of 1001 columns 85 us
+// (6.2), their backward 103 us (5.1).  Groups of 128 of shifted rows are bound by instructions: 146 us at 65536 x 1001,
 // where 65536 x 1000 takes 72 us.  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower
 // (86 -> 93 us at 65536 x 1024).
 #include <algorithm>
@@ -67,6 +67,22 @@ Split split_of(int D, int vec)
     s.rows = s.lanes < kThreads ? kThreads / s.lanes : 1;
     s.threads = s.rows * s.lanes;
     return s;
+}
+
+// BYTES of global memory to shared memory, or zeros.  CACHED: by way of L1, for a thread whose next copy is the other
+// half of a sector (fp32 beside 16-bit values: 65536 x 1000 from 225 to 171 us).
+template <int BYTES, bool CACHED = false>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool ok)
+{
+    if constexpr (CACHED)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+                     : "memory");
+    else if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0)
+                     : "memory");
 }
 
 // A row's place: its first value's number in the tensor, its columns, and the tensor's values.
@@ -160,6 +176,35 @@ struct Part {
 #pragma unroll
         for (int i = 0; i < kHeld * (int)sizeof(T) / 16; ++i)
             reinterpret_cast<uint4 *>(v)[i] = make_uint4(0, 0, 0, 0);
+    }
+    // The same by way of shared memory, into units of the thread's own, `step` apart: ask starts the copies (and zeros
+    // what lies outside), take reads them once they have arrived.
+    static constexpr int kUnits = kHeld * (int)sizeof(T) / 16;
+    static __device__ __forceinline__ void ask(uint4 *slot, int step, const T *p, const Place &at, const int (&col)[N])
+    {
+        constexpr int kEach = VEC * (int)sizeof(T) / 16;   // units of a vector
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (kOneByOne && over<VEC, SHIFTED>(col[j], at.D)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const bool ok = (unsigned)(col[j] + i) < (unsigned)at.D;
+                    copy_async<4>(reinterpret_cast<T *>(slot + (j * kEach + i / 4) * step) + i % 4, ok ? p + at.at + col[j] + i : p,
+                                  ok);
+                }
+                continue;
+            }
+            const bool ok = col[j] < at.D && (!SHIFTED || kOneByOne || at.at + col[j] + VEC <= at.end);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                copy_async<16, (kEach > 1)>(slot + (j * kEach + i) * step, ok ? p + at.at + col[j] + i * (16 / (int)sizeof(T)) : p, ok);
+        }
+    }
+    __device__ __forceinline__ void take(const uint4 *slot, int step)
+    {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            reinterpret_cast<uint4 *>(v)[i] = slot[i * step];
     }
     __device__ __forceinline__ float2 pair(int i) const   // values 2 i and 2 i + 1
     {
@@ -514,15 +559,35 @@ norm_fwd_rows(NormArgs a, Split sp)
     }
 }
 
-template <typename Tx, typename Tr, bool SHIFTED>
+// How many rows a thread asks for before their turn by way of shared memory, and the units of 16 bytes that it holds of
+// each.
+template <typename Tr>
+constexpr int kAhead = sizeof(Tr) == 2 ? 2 : 1;
+template <typename Tx, typename Tr>
+constexpr int kRowUnits = kHeld * (2 * (int)sizeof(Tr) + (int)sizeof(Tx)) / 16;
+
+// Whether rows go by way of shared memory: where a CTA has several turns of rows so wide that few are under way.  In us
+// by registers and by shared memory: 16 bits 65536 x 1000 89 and 92, 32768 x 2048 89 and 84, 13107 x 5120 112 and 101
+// (but 9586 x 7000 103 and 108); fp32 65536 x 1001 173 and 181, 14913 x 4500 216 and 179; 16 bits with an fp32 residual
+// 29127 x 2304 171 and 176, 13107 x 5120 234 and 169.  One row of 2880: 4.0 and 4.6.
+template <typename Tx, typename Tr>
+bool by_shared(const NormArgs &a, const Split &sp)
+{
+    return sp.lanes >= (sizeof(Tx) == sizeof(Tr) ? 128 : 256) && a.rows > (int64_t)a.ctas * sp.rows;
+}
+
+template <typename Tx, typename Tr, bool SHIFTED, bool SHARED>
 __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
 {
     constexpr int VEC = 16 / sizeof(Tx), N = kHeld / VEC;
-    constexpr bool kEarly = sizeof(Tr) == 2;   // registers for the next row beside the present one
+    // rows asked for before their turn; by registers one, where there are registers for it beside the present one
+    constexpr int AHEAD = SHARED ? kAhead<Tr> : sizeof(Tr) == 2 ? 1 : 0;
+    typedef Part<Tr, VEC, SHIFTED> PR;
+    typedef Part<Tx, VEC, SHIFTED> PX;
     __shared__ Told told[2][16];
-    __shared__ float acc[kThreads * kHeld];
+    extern __shared__ uint4 staged[];   // SHARED: by row asked for, unit and thread; after the rows the sums of dw
     tc::grid_dep_wait();
-    const int l = threadIdx.x % sp.lanes, D = a.D;
+    const int l = threadIdx.x % sp.lanes, D = a.D, threads = sp.threads;
     const Tr *s_in = static_cast<const Tr *>(a.s_in), *ds_in = static_cast<const Tr *>(a.ds);
     const Tx *dy_in = static_cast<const Tx *>(a.dy);
     // a CTA's rows: adjacent ones, or (SHIFTED) a grid apart, a multiple of 8, so that all of them have the same shift
@@ -534,13 +599,29 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
     columns<VEC>(col, l, sp.lanes, SHIFTED ? (int)(row * D % VEC) : 0);
     uint32_t keep[kHeld / 2];
     keep_own<VEC>(keep, col, D);
-    Part<Tr, VEC, SHIFTED> s, ds;
-    Part<Tx, VEC, SHIFTED> dy;
+    PR s, ds;
+    PX dy;
     float rstd = 0.f;
     ds.zero();
-    auto fetch = [&](int64_t r) {
-        if (r < a.rows) {
-            const Place to = {r * D, D, at.end};
+    auto slot = [&](int turn, int unit) {
+        return staged + (turn % (AHEAD ? AHEAD : 1) * kRowUnits<Tx, Tr> + unit) * threads + threadIdx.x;
+    };
+    auto rstd_of = [&](int turn) {
+        return reinterpret_cast<float *>(staged + AHEAD * kRowUnits<Tx, Tr> * threads) + turn % (AHEAD ? AHEAD : 1) * threads +
+               threadIdx.x;
+    };
+    auto fetch = [&](int64_t r, int turn) {
+        const Place to = {r * D, D, at.end};
+        if constexpr (SHARED) {
+            if (r < a.rows) {
+                PR::ask(slot(turn, 0), threads, s_in, to, col);
+                PX::ask(slot(turn, PR::kUnits), threads, dy_in, to, col);
+                if (ds_in)
+                    PR::ask(slot(turn, PR::kUnits + PX::kUnits), threads, ds_in, to, col);
+                copy_async<4>(rstd_of(turn), a.rstd_in + r, true);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else if (r < a.rows) {
             s.load(s_in, to, col);
             dy.load(dy_in, to, col);
             if (ds_in)
@@ -551,19 +632,34 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
             dy.zero();
         }
     };
-    if (kEarly)
-        fetch(row);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        fetch(row + i * stride, i);
     float2 w[kHeld / 2], dw[kHeld / 2];
     load_weights<VEC>(w, a.w, col, D);
 #pragma unroll
     for (int i = 0; i < kHeld / 2; ++i)
         dw[i] = make_float2(0.f, 0.f);
     const float part = 1.f / D;
-    for (int64_t first = base, turn = 0; first < a.rows; first += stride, row += stride, ++turn) {
-        if (!kEarly)
-            fetch(row);
+    int turn = 0;
+    for (int64_t first = base; first < a.rows; first += stride, row += stride, ++turn) {
+        if (AHEAD == 0)
+            fetch(row, turn);
         const bool on = row < a.rows;
         at.at = row * D;
+        if constexpr (SHARED) {   // the thread's own copies: nobody else waits for them
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+            s.zero();
+            dy.zero();
+            ds.zero();
+            if (on) {
+                s.take(slot(turn, 0), threads);
+                dy.take(slot(turn, PR::kUnits), threads);
+                if (ds_in)
+                    ds.take(slot(turn, PR::kUnits + PX::kUnits), threads);
+                rstd = *rstd_of(turn);
+            }
+        }
         if (SHIFTED && on) {
             s.mend(s_in, at, col, keep);
             dy.mend(dy_in, at, col, keep);
@@ -581,8 +677,8 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
             g[i] = mul2(g[i], w[i]);
             c = fma2(g[i], n[i], c);
         }
-        if (kEarly)
-            fetch(row + stride);
+        if (AHEAD > 0)
+            fetch(row + AHEAD * stride, turn);
         Told t = {};
         t.sum = c.x + c.y;
         reduce_row<false>(t, sp.lanes, told[turn & 1]);
@@ -591,14 +687,14 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
         for (int i = 0; i < kHeld / 2; ++i)
             up[i] = fma2(make_float2(r, r), fma2(n[i], make_float2(mean, mean), g[i]), up[i]);
         if (on && a.dx) {
-            Part<Tx, VEC, SHIFTED> out;
+            PX out;
 #pragma unroll
             for (int i = 0; i < kHeld / 2; ++i)
                 out.set(i, up[i]);
             out.store(static_cast<Tx *>(a.dx), at, col);
         }
         if (on && a.dres) {
-            Part<Tr, VEC, SHIFTED> out;
+            PR out;
 #pragma unroll
             for (int i = 0; i < kHeld / 2; ++i)
                 out.set(i, up[i]);
@@ -613,6 +709,8 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
         for (int i = 0; i < kHeld / 2; ++i)
             dw[i] = add2(dw[i], make_float2(__shfl_xor_sync(~0u, dw[i].x, m), __shfl_xor_sync(~0u, dw[i].y, m)));
     float *out = a.ctas == 1 ? a.dw : a.part + (size_t)blockIdx.x * D;
+    float *acc = reinterpret_cast<float *>(staged);
+    __syncthreads();   // every thread is done with its copies
     const int width = max(sp.lanes, 32), parts = sp.threads / width, mine = threadIdx.x / width;
     if (threadIdx.x % width < sp.lanes)
 #pragma unroll
@@ -793,6 +891,29 @@ cudaError_t fwd(const NormArgs &a, cudaStream_t s)
     return a.D % (16 / (int)sizeof(Tx)) ? fwd_rows<Tx, Tr, Q, true>(a, s) : fwd_rows<Tx, Tr, Q, false>(a, s);
 }
 
+template <typename Tx, typename Tr, bool SHIFTED>
+cudaError_t bwd_rows(const NormArgs &a, cudaStream_t s)
+{
+    const Split sp = split_of(a.D, 16 / sizeof(Tx));
+    if (!by_shared<Tx, Tr>(a, sp))
+        return launch_early_shared(norm_bwd_rows<Tx, Tr, SHIFTED, false>, a.ctas, sp.threads,
+                                   sp.rows > 1 || sp.lanes < 32 ? sp.threads * kHeld * sizeof(float) : 0, s, a, sp);
+    auto shared = [](int threads) { return kAhead<Tr> * threads * (kRowUnits<Tx, Tr> * 16 + (int)sizeof(float)); };
+    auto kernel = norm_bwd_rows<Tx, Tr, SHIFTED, true>;
+    static std::atomic<bool> sized[128];   // by device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= 128)
+        return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (!sized[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared(512));
+        if (e != cudaSuccess)
+            return e;
+        sized[dev].store(true, std::memory_order_relaxed);
+    }
+    return launch_early_shared(kernel, a.ctas, sp.threads, shared(sp.threads), s, a, sp);
+}
+
 bool wide(int D, int vec) { return held_columns(D, vec) > kMaxHeld; }
 
 }  // namespace
@@ -824,13 +945,12 @@ cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, bool res_f32, cudaStre
     return by_norm_types(dtype, res_f32, [&](auto x, auto r) {
         typedef std::remove_pointer_t<decltype(x)> Tx;
         typedef std::remove_pointer_t<decltype(r)> Tr;
-        const Split sp = split_of(a.D, 16 / sizeof(Tx));
         if (wide(a.D, 16 / sizeof(Tx)))
             norm_bwd_wide<Tx, Tr><<<a.ctas, kThreads, 0, s>>>(a);
         else if (a.D % (16 / (int)sizeof(Tx)))
-            return launch_early(norm_bwd_rows<Tx, Tr, true>, a.ctas, sp.threads, s, a, sp);
+            return bwd_rows<Tx, Tr, true>(a, s);
         else
-            return launch_early(norm_bwd_rows<Tx, Tr, false>, a.ctas, sp.threads, s, a, sp);
+            return bwd_rows<Tx, Tr, false>(a, s);
         return cudaGetLastError();
     });
 }

@@ -453,6 +453,14 @@ def test_norm_shifted_rows(B, rows, D, types):
 
 
 @pytest.mark.parametrize("types", [(TB, TB), (TH, T32), (T32, T32)], ids=lambda t: "-".join(KIND[x] for x in t))
+@pytest.mark.parametrize("rows,D", [(3001, 2048), (1301, 4096), (700, 4104), (457, 8192), (305, 8176)])
+def test_norm_wide_rows_in_turns(B, rows, D, types):
+    """Rows on whole units, several to a CTA one after the other, the last turn with fewer of them."""
+    test_norm_forward(B, rows, D, types)
+    test_norm_backward(B, rows, D, types)
+
+
+@pytest.mark.parametrize("types", [(TB, TB), (TH, T32), (T32, T32)], ids=lambda t: "-".join(KIND[x] for x in t))
 @pytest.mark.parametrize("rows,D", [(2, 3), (3, 1), (7, 2), (11, 3), (2, 5)])
 def test_norm_rows_shorter_than_a_unit(B, rows, D, types):
     """Several rows in one 16-byte unit, the tensor's end inside it."""
