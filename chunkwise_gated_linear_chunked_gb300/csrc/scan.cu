@@ -252,8 +252,9 @@ __device__ __forceinline__ void close_cluster(Shared &sh, int *status)
 }
 
 // This warp's map of tile t.  The last warp composes the CTA's and pushes it to every CTA of the cluster (`ctas`, S
-// rows a slot): 512 bytes a CTA, counted by the receiver's barrier.  The slot's last readers are past it: a CTA pushes tile t after it has
-// received tile t - 1, hence after every CTA has pushed t - 1, which each does after reading tile t - 2.
+// rows a slot): 512 bytes a CTA, counted by the receiver's barrier.  The slot's last readers are past it: a CTA pushes
+// tile t after it has received tile t - 1, hence after every CTA has pushed t - 1, which each does after reading tile
+// t - 2.
 __device__ __forceinline__ void publish(Shared &sh, float4 *ctas, const Map &own, int t, int S, uint32_t rank)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slot = t % kSlots;

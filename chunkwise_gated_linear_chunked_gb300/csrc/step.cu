@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(StepArgs a, int til
 
 // S' = diag(a) S + k^T v and o = scale q S' touch every state element once, so a CTA takes K rows by 32 columns: small
 // enough that 8 heads of one sequence already make 32 CTAs, and all of a thread's K / 16 loads of 16 bytes are under
-// way at once (16 KB a CTA).  128 sequences of 16 heads, 128 x 256: 81.5 us, 6.6 TB/s; one of 8 heads: 1.65 us.  Eight lanes hold a row's columns, so a warp covers four rows; the sum
-// over rows that o takes is finished over the lanes and then over the four warps.
+// way at once (16 KB a CTA).  128 sequences of 16 heads, 128 x 256: 81 us, 6.7 TB/s; one of 8 heads: 1.65 us.  Eight
+// lanes hold a row's columns, so a warp covers four rows; the sum over rows that o takes is finished over the lanes and
+// then over the four warps.
 template <typename Tx, typename Tg, typename To, int K>
 __global__ void __launch_bounds__(kThreads) gla_step_kernel(StepArgs a, int tiles)
 {
