@@ -1,8 +1,8 @@
 // Vector-state gated linear recurrence, forward and backward, in one pass over the data.
 //
 // h_t = a_t h_{t-1} + x_t with a_t = exp(g_t) is a chain of affine maps, and maps compose: rows r..s together take
-// the entering state h to A h + H, with A the product of their decays and H the state they reach from zero.  So the
-// time axis is cut: a thread folds RPT consecutive rows of two channels into (A, H), the CTA composes its warps'
+// the entering state h to A h + H, with A their total decay and H the state they reach from zero.  So the time axis is
+// cut: a thread folds RPT consecutive rows of two channels into (A, H), the CTA composes its warps'
 // maps, a cluster of S CTAs composes its CTAs' maps through distributed shared memory, and the state entering every
 // thread's rows follows; the thread then runs its rows again from that state (decays kept in registers, inputs still
 // in shared memory) and writes them.  The cluster walks the sequence S * R rows at a time and carries the state.
@@ -16,6 +16,7 @@
 // few channels of long sequences are bound by that chain (65536 x 512: 73 us), short ones by starting it.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -211,20 +212,32 @@ struct Pair {
     }
 };
 
-__device__ __forceinline__ float2 decay2(float2 g) { return make_float2(decay(g.x), decay(g.y)); }
+__device__ __forceinline__ float2 exp2_fast2(float2 t) { return make_float2(exp2_fast(t.x), exp2_fast(t.y)); }
+__device__ __forceinline__ float2 log2_decay(float2 g) { return mul2(g, make_float2(kLog2e, kLog2e)); }
+__device__ __forceinline__ float2 decay2(float2 g) { return exp2_fast2(log2_decay(g)); }
 
-// An affine map h -> A h + H of a lane's two channels.
+// An affine map h -> a (a h) + H of a lane's two channels.  a is the root of the rows' total decay A, from the sum of
+// their gates, and at most the largest fp32 value.  Gates may rise and fall by more than an exponential's range and
+// still leave the states in theirs; then A may be no fp32 value (or, as a product of decays, come back from 0 or infinity
+// as something else), but its root is one wherever a normal h leaves A h in range, and a (a h) is right in one rounding
+// more.  An h of zero stays zero, whatever a is.
 struct Map {
-    float2 A, H;
-    __device__ __forceinline__ Map() : A{1.f, 1.f}, H{0.f, 0.f} {}
-    __device__ __forceinline__ Map(float4 v) : A{v.x, v.y}, H{v.z, v.w} {}
-    __device__ __forceinline__ float4 packed() const { return make_float4(A.x, A.y, H.x, H.y); }
-    __device__ __forceinline__ void then(const Map &m)   // this map, then m
+    float2 a, H;
+    __device__ __forceinline__ Map() : a{1.f, 1.f}, H{0.f, 0.f} {}
+    __device__ __forceinline__ Map(float4 v) : a{v.x, v.y}, H{v.z, v.w} {}
+    __device__ __forceinline__ float4 packed() const { return make_float4(a.x, a.y, H.x, H.y); }
+    __device__ __forceinline__ void set_decay(float2 sum)   // of the rows' log2 decays
     {
-        A = mul2(A, m.A);
-        H = fma2(m.A, H, m.H);
+        a = exp2_fast2(mul2(sum, make_float2(0.5f, 0.5f)));
+        bound();
     }
-    __device__ __forceinline__ float2 operator()(float2 h) const { return fma2(A, h, H); }
+    __device__ __forceinline__ void bound() { a = make_float2(fminf(a.x, FLT_MAX), fminf(a.y, FLT_MAX)); }
+    __device__ __forceinline__ void then(const Map &m)   // this map, then m (bound() after the last)
+    {
+        a = mul2(a, m.a);
+        H = m(H);
+    }
+    __device__ __forceinline__ float2 operator()(float2 h) const { return fma2(a, mul2(a, h), H); }
 };
 
 struct Shared {
@@ -279,10 +292,11 @@ __device__ __forceinline__ void publish(Shared &sh, float4 *ctas, const Map &own
     for (int i = 0; i < kWarps - 1; ++i)
         all.then(sh.warps[slot][i][lane]);
     all.then(own);
+    all.bound();
     for (int i = 0; i < S; ++i)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
                          remote(ctas + (slot * S + rank) * 32 + lane, i)),
-                     "f"(all.A.x), "f"(all.A.y), "f"(all.H.x), "f"(all.H.y), "r"(remote(&sh.full[slot], i))
+                     "f"(all.a.x), "f"(all.a.y), "f"(all.H.x), "f"(all.H.y), "r"(remote(&sh.full[slot], i))
                      : "memory");
 }
 
@@ -344,7 +358,7 @@ struct Forward {
     typedef Tile<Tg, R, ROWS, 1> TG;
     static constexpr int kStage = TX::kBytes + TG::kBytes;
     typedef Pair<ROWS != kAnywhere> Lane;
-    Map row[RPT];
+    float2 dec[RPT], in[RPT];
     const TX x;
     const TG g;
     To *h;
@@ -366,12 +380,16 @@ struct Forward {
     {
         const char *gs = g.at(st + TX::kBytes, j, p), *xs = x.at(st, j, p);
         Map own;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            row[i].A = decay2(g.read(gs, i));
-            row[i].H = x.read(xs, i);
-            own.then(row[i]);
+            const float2 t = log2_decay(g.read(gs, i));
+            dec[i] = exp2_fast2(t);
+            in[i] = x.read(xs, i);
+            sum = add2(sum, t);
+            own.H = fma2(dec[i], own.H, in[i]);
         }
+        own.set_decay(sum);
         return own;
     }
     template <bool WHOLE>
@@ -380,7 +398,7 @@ struct Forward {
         To *at = h + (int64_t)p * a.D;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            s = row[i](s);
+            s = fma2(dec[i], s, in[i]);
             if (WHOLE || p + i < len)
                 lane.template store<WHOLE>(at + (int64_t)i * a.D, s);
         }
@@ -430,13 +448,16 @@ struct Backward {
         const int r = len - 1 - p;
         const char *gs = g.at(st, j, r), *ds = dh.at(st + TG::kBytes, j, r);
         Map own;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            dec[i] = decay2(g.read(gs, i));
+            const float2 t = log2_decay(g.read(gs, i));
+            dec[i] = exp2_fast2(t);
             up[i] = dh.read(ds, i);
-            own.A = mul2(own.A, dec[i]);
+            sum = add2(sum, t);
             own.H = mul2(dec[i], add2(own.H, up[i]));
         }
+        own.set_decay(sum);
         return own;
     }
     template <bool WHOLE>

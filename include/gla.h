@@ -318,9 +318,14 @@ size_t gla_wy_workspace_size(int T, int N, int chunk, int varlen);
  *               (gla_get_status) and skipped; a bounded wait that ran out is reported as GLA_ERR_TIMEOUT (the
  *               outputs of that call are then void)
  *
- * g is usually <= 0 but may be any value: the recurrence is evaluated as written, and infinities and NaN spread as
- * they would step by step, except that a segment's total decay multiplies the state that enters it (a state of
- * infinity that meets a total decay of 0 becomes NaN).  A decay is within 2^-22 + |g| 2^-24 (relative) of exp(g).
+ * g is usually <= 0 but may be any value whose exponential is an fp32 number.  The recurrence is evaluated as written,
+ * also where sums of gates leave an exponential's range and come back: h_t is the sum of its rows' shares
+ * exp(g_{s+1} + .. + g_t) x_s, and as long as none of them passes fp32's largest value on the way, h_t is right to the
+ * roundings of that sum (a share that falls below fp32's normal numbers on the way may count as 0).  Once one has, what
+ * follows in that channel is void (infinite, NaN, or finite again where the gates fall).  Infinities and NaN of the inputs spread as they would step by step, except that a segment's total decay
+ * multiplies the state that enters it: a state of infinity becomes NaN where that decay is below 2^-252.
+ * A decay is within (2^-22 + |g| 2^-24) exp(g) + 2^-126 of exp(g): subnormal decays are 0.  The total decay of up to 16
+ * rows is the exponential of the fp32 sum of their gates.
  * Results do not depend on timing (no atomics).
  */
 int gla_scan_fwd(const void *x, const void *g, void *h, const float *h0, float *ht, const int32_t *cu_seqlens, int N,
