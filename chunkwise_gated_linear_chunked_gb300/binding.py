@@ -383,26 +383,10 @@ SCAN_CODE = {(torch.float32, torch.float32, torch.float32): GLA_F32,
              (torch.float16, torch.float32, torch.float32): GLA_F16_GF32}
 _NORM_CODE = {torch.float32: GLA_F32, torch.bfloat16: GLA_BF16, torch.float16: GLA_F16}
 _STATUS_BYTES = int(_lib.gla_scan_workspace_size())
-_stream_ws: dict = {}
-
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle on a device, without a Stream object
 _current_device = torch._C._cuda_getDevice
 _capturing = torch.cuda.is_current_stream_capturing
-
-
-def stream_workspace(nbytes: int, device: int) -> torch.Tensor:
-    """A zeroed device workspace of at least ``nbytes``, cached per device and current stream, so that calls on
-    different streams never share one.  During a CUDA graph capture it is a fresh tensor instead: the graph zeroes
-    it on every replay and owns its memory."""
-    if _capturing():
-        return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-    key = (device, _raw_stream(device))
-    ws = _stream_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _stream_ws[key] = ws
-    return ws
 
 
 _status_ws: dict = {}
@@ -764,11 +748,10 @@ def norm_bwd(s, rstd, dy, weight=None, ds=None, want_dw=True, workspace=None, st
 
     Returns (the gradient of x in dy's type, the gradient of the residual in s's type, dw fp32 [D] or None).  The
     first two are one tensor when the types are the same.  ``want_dw=False`` skips dw (also None without a weight).
+    workspace: one of the caller's, for one call at a time (default: memory of the call's own).
     """
-    if workspace is None and stream is None and dy.is_cuda and dy.dim():
-        device, D = dy.get_device(), dy.shape[-1]
-        ws = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(dy.numel() // max(D, 1), D)), device)
-        got = _calls.norm_bwd(s, rstd, dy, weight, ds, want_dw, ws)
+    if workspace is None and stream is None:
+        got = _calls.norm_bwd(s, rstd, dy, weight, ds, want_dw, None)
         if got is not None:
             return got
     return _norm_bwd_checked(s, rstd, dy, weight, ds, want_dw, workspace, stream=stream)
@@ -785,7 +768,8 @@ def _norm_bwd_checked(s, rstd, dy, weight, ds, want_dw, workspace):
     dres = dx if s.dtype == dy.dtype else torch.empty_like(s)
     dw = torch.empty(D, dtype=torch.float32, device=device) if want_dw and weight is not None else None
     if workspace is None:
-        workspace = stream_workspace(int(_lib.gla_norm_bwd_workspace_size(rows, D)), device)
+        # of this call alone: its two launches meet there, and another thread's may come between them on one stream
+        workspace = torch.empty(int(_lib.gla_norm_bwd_workspace_size(rows, D)), dtype=torch.uint8, device=device)
     rc = _lib.gla_norm_bwd(s.data_ptr(), rstd.data_ptr(), _at(weight), dy.data_ptr(), _at(ds), dx.data_ptr(),
                            None if dres is dx else dres.data_ptr(), _at(dw), rows, D, code, workspace.data_ptr(),
                            workspace.numel(), _raw_stream(device))

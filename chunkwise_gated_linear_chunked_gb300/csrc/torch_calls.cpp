@@ -348,7 +348,7 @@ PyObject *norm_quant_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// norm_bwd(s, rstd, dy, weight, ds, want_dw, workspace)
+// norm_bwd(s, rstd, dy, weight, ds, want_dw, workspace or None)
 PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
@@ -356,7 +356,7 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (n != 7)
         return none();
     const at::Tensor *s = c.take(a[0]), *rstd = c.take(a[1]), *dy = c.take(a[2]), *w = c.take(a[3], true),
-                     *ds = c.take(a[4], true), *ws = c.take(a[6]);
+                     *ds = c.take(a[4], true), *given = c.take(a[6], true);
     if (!c.ok)
         return none();
     const Norm m = norm(c, dy, s, w);
@@ -372,9 +372,11 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
         dres = empty(s->sizes(), *s, s->scalar_type());
     if (w && PyObject_IsTrue(a[5]))
         dw = empty({m.D}, *s, at::kFloat);
+    // the partial sums' memory is this call's own, as another thread may be between its two launches on this stream
+    const at::Tensor ws = given ? *given : empty({(int64_t)gla_norm_bwd_workspace_size(m.rows, (int)m.D)}, *s, at::kByte);
     const int rc = gla_norm_bwd(s->data_ptr(), floats(rstd), floats(w), dy->data_ptr(), at_of(ds), dx.data_ptr(),
                                 same ? nullptr : dres.data_ptr(), dw.defined() ? floats(&dw) : nullptr, m.rows, (int)m.D,
-                                m.code, ws->data_ptr(), (size_t)ws->numel() * ws->element_size(), c.stream());
+                                m.code, ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), c.stream());
     if (rc != GLA_OK)
         return none();
     PyObject *first = wrap(dx), *second = nullptr, *third = first ? wrap(std::move(dw)) : nullptr;
