@@ -29,7 +29,7 @@ EXPORTS = ("gla_fwd", "gla_fwd_workspace_size", "gla_get_status", "gla_strerror"
            "gla_bwd_workspace_size", "gla_ttt_linear_fwd", "gla_ttt_workspace_size", "gla_wy_fwd",
            "gla_wy_workspace_size", "gla_fwd_host", "gla_fwd_host_workspace_size", "gla_scan_fwd", "gla_scan_bwd",
            "gla_scan_step", "gla_scan_workspace_size", "gla_step", "gla_norm_fwd", "gla_norm_quant_fwd",
-           "gla_norm_bwd", "gla_norm_bwd_workspace_size")
+           "gla_norm_bwd", "gla_norm_bwd_workspace_size", "gla_scan_shared_workspace")
 
 if not os.path.exists(LIB):
     raise ImportError(f"libgla.so not built ({LIB}); call chunkwise_gated_linear_chunked_gb300.build.build()")
@@ -79,6 +79,8 @@ _lib.gla_scan_step.argtypes = [_p] * 6 + [_i] * 3 + [_i64] * 2 + [_i, _p, _sz, _
 _lib.gla_scan_step.restype = _i
 _lib.gla_scan_workspace_size.argtypes = []
 _lib.gla_scan_workspace_size.restype = _sz
+_lib.gla_scan_shared_workspace.argtypes = []
+_lib.gla_scan_shared_workspace.restype = _p
 _lib.gla_step.argtypes = [_p] * 5 + [_f] + [_p] * 3 + [_i] * 6 + [_p, _sz, _p]
 _lib.gla_step.restype = _i
 _lib.gla_norm_fwd.argtypes = [_p] * 6 + [_i64, _i, _f, _i, _p]
@@ -386,22 +388,29 @@ _STATUS_BYTES = int(_lib.gla_scan_workspace_size())
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle on a device, without a Stream object
 _current_device = torch._C._cuda_getDevice
-_capturing = torch.cuda.is_current_stream_capturing
+_shared_status: dict = {}   # by device: the address of the library's own status workspace
 
 
-_status_ws: dict = {}
+def _status_workspace(workspace, device: int):
+    """(address, bytes) of a call's status workspace on the current device: the caller's, or the library's own, which
+    calls on any stream share (they write it only to report an error)."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    at = _shared_status.get(device)
+    if at is None:
+        at = _shared_status[device] = _lib.gla_scan_shared_workspace()
+    return at, _STATUS_BYTES
 
 
-def _status_workspace(device: int) -> torch.Tensor:
-    """The workspace of calls that keep nothing but the status word there, one per device: calls on any stream may
-    share it (they write it only to report an error)."""
-    ws = _status_ws.get(device)
-    if ws is None:
-        ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=device)
-        if not _capturing():   # a graph owns what is allocated during its capture
-            _status_ws[device] = ws
-            _calls.use_status(device, ws.data_ptr())
-    return ws
+def layer_status(device=None, stream=None) -> int:
+    """What the kernels of ``scan_fwd``, ``scan_bwd``, ``scan_step`` and ``gla_step`` calls without a workspace of their
+    own have reported on a device (default: the current one) since the last look: GLA_OK, or the code of the first error,
+    which this call clears.  Waits for ``stream`` (default: the current one); what runs on other streams may report
+    later.  One word serves all streams; a call's own ``workspace`` (256 zeroed bytes) and ``get_status`` tell its errors
+    apart."""
+    with torch.cuda.device(device):
+        at, _ = _status_workspace(None, torch.cuda.current_device())
+        return int(_lib.gla_get_status(at, _stream_handle(stream)))
 
 
 def _on_stream(fn):
@@ -483,6 +492,8 @@ def scan_fwd(x, g, initial_state=None, output_final_state=True, cu_seqlens=None,
     output); both fp32, bf16 or fp16, or a 16-bit x with an fp32 g.  initial_state: fp32 [N, D] or None.
     cu_seqlens: int32 [N+1] cuda offsets (B == 1).  out_dtype: x's type (default; fp32 beside an fp32 g) or fp32.
     out: optional [B, T, D] tensor for h.  stream=: the stream to run on.  Returns (h, ht fp32 [N, D] or None).
+    Offsets are checked on the device: a sequence whose offsets are bad is left out (its outputs are undefined) and
+    reported, see ``layer_status``.
     """
     if out is None and workspace is None and stream is None:
         got = _calls.scan_fwd(x, g, initial_state, output_final_state, cu_seqlens, out_dtype)
@@ -510,11 +521,8 @@ def _scan_fwd_checked(x, g, initial_state, output_final_state, cu_seqlens, out_d
     else:
         _check("gla_scan_fwd", "out", out, out_dtype, shape, device)
     ht = torch.empty(N, D, dtype=torch.float32, device=device) if output_final_state else None
-    if workspace is None:
-        workspace = _status_workspace(device)
     rc = _lib.gla_scan_fwd(x.data_ptr(), g.data_ptr(), out.data_ptr(), _at(initial_state), _at(ht), _at(cu_seqlens),
-                           N, B, T, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
-                           _raw_stream(device))
+                           N, B, T, D, ldx, ldg, code, *_status_workspace(workspace, device), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_fwd")
     return out, ht
@@ -526,7 +534,7 @@ def scan_bwd(g, h, dh, initial_state=None, dht=None, cu_seqlens=None, dx_dtype=N
 
     g as for scan_fwd; h, dh: [B, T, D] contiguous, of the forward's out_dtype; initial_state, dht: fp32 [N, D] or
     None.  dx_dtype: x's type (default: g's).  dx, dg: optional tensors to write, which may be column ranges of one
-    gradient.  Returns (dx, dg in g's type, dh0 fp32 [N, D] or None).
+    gradient.  Returns (dx, dg in g's type, dh0 fp32 [N, D] or None).  Bad offsets as for scan_fwd.
     """
     if dx is None and dg is None and workspace is None and stream is None:
         got = _calls.scan_bwd(g, h, dh, initial_state, dht, cu_seqlens, dx_dtype, want_dh0)
@@ -565,11 +573,9 @@ def _scan_bwd_checked(g, h, dh, initial_state, dht, cu_seqlens, dx_dtype, want_d
     else:
         lddg = _row_stride("gla_scan_bwd", "dg", dg, shape, device)
     dh0 = torch.empty(N, D, dtype=torch.float32, device=device) if want_dh0 else None
-    if workspace is None:
-        workspace = _status_workspace(device)
     rc = _lib.gla_scan_bwd(g.data_ptr(), h.data_ptr(), dh.data_ptr(), _at(initial_state), _at(dht), dx.data_ptr(),
                            dg.data_ptr(), _at(dh0), _at(cu_seqlens), N, B, T, D, ldg, lddx, lddg, code,
-                           workspace.data_ptr(), workspace.numel(), _raw_stream(device))
+                           *_status_workspace(workspace, device), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_bwd")
     return dx, dg, dh0
@@ -596,7 +602,8 @@ def scan_step(x, g, state, slots=None, state_out=None, out_dtype=None, workspace
 
     x, g: [B, D] (types and strides as for scan_fwd); state: fp32 [S, D] pool, updated in place (or written to
     state_out, of which only the addressed rows are written); slots: int32 [B] cuda, the pool row of each sequence
-    (-1: idle, its h is zeros), or None when S == B.  Returns h [B, D].
+    (-1: idle, its h is zeros; any other slot outside the pool likewise, and reported, see ``layer_status``), or None
+    when S == B.  Returns h [B, D].
     """
     if workspace is None and stream is None:
         got = _calls.scan_step(x, g, state, slots, state_out, out_dtype)
@@ -620,10 +627,8 @@ def _scan_step_checked(x, g, state, slots, state_out, out_dtype, workspace):
     ldg = _row_stride("gla_scan_step", "g", g, shape, device)
     S, state_out = _pool("gla_scan_step", state, state_out, slots, B, (D,), device)
     h = torch.empty(shape, dtype=out_dtype, device=device)
-    if workspace is None:
-        workspace = _status_workspace(device)
     rc = _lib.gla_scan_step(x.data_ptr(), g.data_ptr(), h.data_ptr(), state.data_ptr(), state_out.data_ptr(),
-                            _at(slots), B, S, D, ldx, ldg, code, workspace.data_ptr(), workspace.numel(),
+                            _at(slots), B, S, D, ldx, ldg, code, *_status_workspace(workspace, device),
                             _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_scan_step")
@@ -662,12 +667,9 @@ def _gla_step_checked(q, k, v, g, state, scale, slots, state_out, out_dtype, wor
         _check("gla_step", "g", g, g.dtype, (B, H, K), device)
     S, state_out = _pool("gla_step", state, state_out, slots, B, (H, K, V), device)
     o = torch.empty(B, H, V, dtype=out_dtype, device=device)
-    if workspace is None:
-        workspace = _status_workspace(device)
     rc = _lib.gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), o.data_ptr(),
                        K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B, S,
-                       H, K, V, code, workspace.data_ptr(), workspace.numel(),
-                       _raw_stream(device))
+                       H, K, V, code, *_status_workspace(workspace, device), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, "gla_step")
     return o

@@ -16,6 +16,8 @@ constexpr size_t kStatusBytes = 256;
 constexpr int kMaxNormD = 16384;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
+__device__ __align__(256) char g_shared_status[kStatusBytes];   // one a device, zero from the start
+
 struct TypeSizes {
     size_t x, g, o;
 };
@@ -107,6 +109,12 @@ int check_scan_shape(int N, int B, int T, int D, bool varlen, std::initializer_l
 using namespace gla;
 
 extern "C" size_t gla_scan_workspace_size(void) { return kStatusBytes; }
+
+extern "C" void *gla_scan_shared_workspace(void)
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_shared_status) == cudaSuccess ? p : nullptr;
+}
 
 extern "C" int gla_scan_fwd(const void *x, const void *g, void *h, const float *h0, float *ht,
                             const int32_t *cu_seqlens, int N, int B, int T, int D, int64_t ldx, int64_t ldg, int dtype,

@@ -18,7 +18,15 @@ namespace {
 
 constexpr int kDevices = 128;
 constexpr size_t kStatusBytes = 256;
-void *g_status[kDevices] = {};   // status workspaces, handed over by use_status (binding.py keeps them alive)
+
+// The library's own status workspace on the current device, or nullptr.
+void *status(int device)
+{
+    static void *known[kDevices] = {};   // the interpreter's lock is held
+    if (!known[device])
+        known[device] = gla_scan_shared_workspace();
+    return known[device];
+}
 
 // One call's tensors: whether all of them are usual.
 struct Call {
@@ -141,7 +149,7 @@ PyObject *scan_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
         return none();
     const at::ScalarType type = dtype_or(a[5], g->scalar_type(), c);
     const int code = scan_code(x->scalar_type(), g->scalar_type(), type), N = sequences(c, *x, cu);
-    c.need(code >= 0 && g->sizes() == x->sizes() && g_status[c.device]);
+    c.need(code >= 0 && g->sizes() == x->sizes() && status(c.device));
     if (!c.ok)
         return none();
     const int64_t D = x->size(2);
@@ -152,7 +160,7 @@ PyObject *scan_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (PyObject_IsTrue(a[3]))
         ht = empty({N, D}, *x, at::kFloat);
     const int rc = gla_scan_fwd(x->data_ptr(), g->data_ptr(), h.data_ptr(), floats(h0), ht.defined() ? floats(&ht) : nullptr,
-                                ints(cu), N, (int)x->size(0), (int)x->size(1), (int)D, D, D, code, g_status[c.device],
+                                ints(cu), N, (int)x->size(0), (int)x->size(1), (int)D, D, D, code, status(c.device),
                                 kStatusBytes, c.stream());
     return rc == GLA_OK ? tuple_of(std::move(h), std::move(ht)) : none();
     END_HANDLE_TH_ERRORS
@@ -171,7 +179,7 @@ PyObject *scan_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
         return none();
     const at::ScalarType type = dtype_or(a[6], g->scalar_type(), c);
     const int code = scan_code(type, g->scalar_type(), h->scalar_type()), N = sequences(c, *g, cu);
-    c.need(code >= 0 && h->sizes() == g->sizes() && g_status[c.device]);
+    c.need(code >= 0 && h->sizes() == g->sizes() && status(c.device));
     c.like(dh, *g, h->scalar_type());
     if (!c.ok)
         return none();
@@ -185,7 +193,7 @@ PyObject *scan_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
         dh0 = empty({N, D}, *g, at::kFloat);
     const int rc = gla_scan_bwd(g->data_ptr(), h->data_ptr(), dh->data_ptr(), floats(h0), floats(dht), dx.data_ptr(),
                                 dg.data_ptr(), dh0.defined() ? floats(&dh0) : nullptr, ints(cu), N, (int)g->size(0),
-                                (int)g->size(1), (int)D, D, D, D, code, g_status[c.device], kStatusBytes, c.stream());
+                                (int)g->size(1), (int)D, D, D, D, code, status(c.device), kStatusBytes, c.stream());
     return rc == GLA_OK ? tuple_of(std::move(dx), std::move(dg), std::move(dh0)) : none();
     END_HANDLE_TH_ERRORS
 }
@@ -203,7 +211,7 @@ int64_t pool(Call &c, const at::Tensor *state, const at::Tensor *out, const at::
         c.shaped(slots, {B}, at::kInt);
     else
         c.need(state->size(0) == B);
-    c.need(g_status[c.device]);
+    c.need(status(c.device));
     return state->size(0);
 }
 
@@ -228,7 +236,7 @@ PyObject *scan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
         return none();
     at::Tensor h = empty(x->sizes(), *x, type);
     const int rc = gla_scan_step(x->data_ptr(), g->data_ptr(), h.data_ptr(), floats(state), floats(out ? out : state),
-                                 ints(slots), (int)B, (int)S, (int)D, D, D, code, g_status[c.device], kStatusBytes,
+                                 ints(slots), (int)B, (int)S, (int)D, D, D, code, status(c.device), kStatusBytes,
                                  c.stream());
     return rc == GLA_OK ? wrap(std::move(h)) : none();
     END_HANDLE_TH_ERRORS
@@ -261,7 +269,7 @@ PyObject *step(PyObject *, PyObject *const *a, Py_ssize_t n)
     at::Tensor o = empty({B, H, V}, *q, type);
     const int rc = gla_step(q->data_ptr(), k->data_ptr(), v->data_ptr(), g->data_ptr(), o.data_ptr(), (float)scale,
                             floats(state), floats(out ? out : state), ints(slots), (int)B, (int)S, (int)H, (int)K, (int)V,
-                            code, g_status[c.device], kStatusBytes, c.stream());
+                            code, status(c.device), kStatusBytes, c.stream());
     return rc == GLA_OK ? wrap(std::move(o)) : none();
     END_HANDLE_TH_ERRORS
 }
@@ -390,24 +398,10 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// use_status(device, address): the status workspace of calls on a device.
-PyObject *use_status(PyObject *, PyObject *const *a, Py_ssize_t n)
-{
-    if (n == 2) {
-        const long device = PyLong_AsLong(a[0]);
-        void *p = PyLong_AsVoidPtr(a[1]);
-        if (PyErr_Occurred())
-            return nullptr;
-        if (device >= 0 && device < kDevices)
-            g_status[device] = p;
-    }
-    Py_RETURN_NONE;
-}
-
 #define CALL(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL("scan_fwd", scan_fwd), CALL("scan_bwd", scan_bwd), CALL("scan_step", scan_step),
                          CALL("gla_step", step), CALL("norm_fwd", norm_fwd), CALL("norm_quant_fwd", norm_quant_fwd),
-                         CALL("norm_bwd", norm_bwd), CALL("use_status", use_status), {nullptr, nullptr, 0, nullptr}};
+                         CALL("norm_bwd", norm_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -227,6 +227,8 @@ def main():
     out = generate(Server(model, 32, a.eight_bit), prompts, slots, 64)
     follow = torch.randperm(VOCAB, generator=torch.Generator().manual_seed(7)).cuda()
     right = (out[:, 1:] == follow[out[:, :-1]]).float().mean()
+    if binding.layer_status() != binding.GLA_OK:
+        raise SystemExit("a kernel reported bad slots or offsets")
     print(f"64 tokens for 16 sequences in {time.perf_counter() - start:.2f} s; {100 * right:.0f} % follow the rule")
 
 

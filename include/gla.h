@@ -351,6 +351,12 @@ int gla_scan_bwd(const void *g, const void *h, const void *dh, const float *h0, 
 /* Bytes of device workspace gla_scan_fwd, gla_scan_bwd, gla_scan_step and gla_step need (the status word). */
 size_t gla_scan_workspace_size(void);
 
+/* Such a workspace on the CURRENT device that the library itself holds (static device memory, zero when it is loaded), for
+ * callers that keep none; NULL without a device.  May be asked for during a stream capture.  All its users share the
+ * status word, whatever their streams and threads: gla_get_status then tells that one of their calls since the last look
+ * failed, not which. */
+void *gla_scan_shared_workspace(void);
+
 /*
  * gla_scan_step — one token of the recurrence above for each of B sequences, with the states in a pool:
  *
