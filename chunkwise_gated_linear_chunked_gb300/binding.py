@@ -1,5 +1,5 @@
 """Thin ctypes binding of libgla (``include/gla.h``): argument marshalling only.  The layer operators' usual calls
-take a shorter way to the same C functions, through the ``_calls`` module.
+take a shorter way to the same C functions, through the ``_calls`` module, where it could be built.
 
 Every step of the forward runs in libgla's CUDA kernels; torch supplies device memory and streams.  There is
 no CPU fallback: if ``_build/libgla.so`` is missing the import fails loudly (run
@@ -93,15 +93,21 @@ _lib.gla_norm_bwd_workspace_size.argtypes = [_i64, _i]
 _lib.gla_norm_bwd_workspace_size.restype = _sz
 
 
+class _NoCalls:
+    """Stands for the ``_calls`` module where it is missing (no host compiler, another torch than it was built for): every
+    call is left to the checked functions."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
 
 
 def _load_calls():
-    path = calls_lib()
-    if not os.path.exists(path):
-        raise ImportError(f"_calls not built ({path}); call chunkwise_gated_linear_chunked_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("_calls", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    spec = importlib.util.spec_from_file_location("_calls", calls_lib())
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:
+        return _NoCalls()
     return module
 
 
