@@ -566,14 +566,17 @@ constexpr int kAhead = sizeof(Tr) == 2 ? 2 : 1;
 template <typename Tx, typename Tr>
 constexpr int kRowUnits = kHeld * (2 * (int)sizeof(Tr) + (int)sizeof(Tx)) / 16;
 
-// Whether rows go by way of shared memory: where a CTA has several turns of rows so wide that few are under way.  In us
-// by registers and by shared memory: 16 bits 65536 x 1000 89 and 92, 32768 x 2048 89 and 84, 13107 x 5120 112 and 101
-// (but 9586 x 7000 103 and 108); fp32 65536 x 1001 173 and 181, 14913 x 4500 216 and 179; 16 bits with an fp32 residual
-// 29127 x 2304 171 and 176, 13107 x 5120 234 and 169.  One row of 2880: 4.0 and 4.6.
+// Whether rows go by way of shared memory: where a CTA has several turns of rows so wide that few are under way, and, of
+// 16-bit rows of more than 256 threads (one CTA an SM), only those in whole 32-byte sectors.  In us by registers and by
+// shared memory, 67 million values: 16 bits 2048 columns 87 and 82, 4096: 89 and 85, 5120: 110 and 99, 8000: 96 and 88, but
+// 4500: 139 and 145, 7000: 100 and 106, 8184: 95 and 103; fp32 2048: 159 and 153, 4500: 213 and 177, 8184: 173 and 165; 16
+// bits with an fp32 residual 3000: 188 and 188, 3600: 181 and 166, 4500: 283 and 210, 8184: 206 and 169 (4096 alone goes the
+// other way, 171 and 184).  65536 x 1000 in 16 bits 89 and 92; one row of 2880: 4.0 and 4.6.
 template <typename Tx, typename Tr>
 bool by_shared(const NormArgs &a, const Split &sp)
 {
-    return sp.lanes >= (sizeof(Tx) == sizeof(Tr) ? 128 : 256) && a.rows > (int64_t)a.ctas * sp.rows;
+    const bool sectors = sizeof(Tr) == 4 || sp.lanes <= 256 || a.D % 16 == 0;
+    return sectors && sp.lanes >= (sizeof(Tx) == sizeof(Tr) ? 128 : 256) && a.rows > (int64_t)a.ctas * sp.rows;
 }
 
 template <typename Tx, typename Tr, bool SHIFTED, bool SHARED>
