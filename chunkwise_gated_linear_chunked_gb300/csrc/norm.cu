@@ -1,9 +1,9 @@
 // Residual addition and root-mean-square norm: forward (fp32 / 16-bit or e4m3 output) and backward.
 //
-// Up to 8176 columns a row lives in registers, 16 values a thread: it is read once, reduced, and written.  A warp holds
-// 512 adjacent columns, up to 16 warps a row; rows of at most 256 columns share a warp.  A CTA keeps its share of the
-// weights in registers, walks rows a grid apart, and asks for its next row before it reduces the present one.  Wider
-// rows are read again from cache instead, by one CTA a row.
+// Up to 8192 columns (shifted rows: 8185 in 16 bits, 8189 in fp32) a row lives in registers, 16 values a thread: it is
+// read once, reduced, and written.  A warp holds 512 adjacent columns, up to 16 warps a row; rows of at most 256 columns
+// share a warp.  A CTA keeps its share of the weights in registers, walks rows a grid apart, and asks for its next row
+// before it reduces the present one.  Wider rows are read again from cache instead, value by value by one CTA a row.
 //
 // Memory is read and written in whole 16-byte units whatever D is.  A row starts k values into such a unit; a thread's
 // vectors lie on units, so vector v holds columns VEC v - k and up, and the two vectors that hang over the row's ends
@@ -11,8 +11,10 @@
 //
 // Bound by HBM: 65536 rows of 4096 columns in 16 bits with a residual 335 us (6.4 TB/s), e4m3 in groups of 128 with an
 // fp32 residual, 16384 x 2048, 57 us (6.5), the backward of 32768 x 2048 84 us (6.4), 65536 rows of 1001 columns 85 us
-// (6.2), their backward 103 us (5.1).  Groups of 128 of shifted rows are bound by instructions: 146 us at 65536 x 1001,
-// where 65536 x 1000 takes 72 us.  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower
+// (6.2), their backward 101 us (5.2).  Groups of 128 of shifted rows are bound by instructions: 146 us at 65536 x 1001,
+// where 65536 x 1000 takes 72 us.  The wide rows' kernels are bound by instructions and latency: 4096 rows of 16384 columns
+// in 16 bits, forward 207 us, e4m3 228, in groups of 128 (one after the other) 622, backward (its sums of dw in global
+// memory) 622, where a copy takes 69 to 79.  The forward takes three CTAs of 256 threads an SM; four, at 64 registers, ran slower
 // (86 -> 93 us at 65536 x 1024).
 #include <algorithm>
 #include <atomic>
@@ -26,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;        // threads of a CTA (more where a row needs them)
 constexpr int kHeld = 16;            // values of a row in a thread
-constexpr int kMaxHeld = 8192;       // columns of a row that 16 warps hold (fewer by kHeld where rows are shifted)
+constexpr int kMaxHeld = 8192;       // columns of a row that 16 warps hold, with what hangs over where rows are shifted
 constexpr float kE4m3Max = 448.f, kScaleMin = 1e-30f;
 
 // Maximum that keeps a NaN of either side.
@@ -131,7 +133,7 @@ __device__ __forceinline__ void put_end(E *p, Q lo, Q hi, int c, int D)
 // ends.  Of 32-bit values they are loaded one by one.  Of 16-bit values, two a register, that would make every load wait
 // to be put together; they are loaded like the others (their other values are the neighbouring rows') and masked when
 // they are used, and what would reach over the tensor's end is loaded only then.  Masks kept in registers and ends
-// stored in pieces of one, two and four took 65536 x 1001 from 93 to 85 us, its backward from 138 to 105, against a
+// stored in pieces of one, two and four took 65536 x 1001 from 93 to 85 us, its backward from 138 to 101, against a
 // test for each value.
 template <typename T, int VEC, bool SHIFTED>
 struct Part {
@@ -448,7 +450,8 @@ __device__ __forceinline__ void put_e4m3(uint8_t *p, const Place &at, int c, con
 
 enum Quant { kPlain, kByRow, kByGroup };
 
-// Registers: as many as hold the row and the next one without spilling.  Groups of unshifted 16-bit rows go faster with
+// Registers: as many as hold the row and the next one (12 bytes spill of e4m3 rows by row, shifted, of 16 bits with an fp32
+// residual).  Groups of unshifted 16-bit rows go faster with
 // three CTAs of 256 threads, at 80, than with two, at 96 (81 -> 72 us at 65536 x 1000, though 78 -> 81 at 29127 x 2304);
 // those of shifted rows do not (146 -> 152 us at 65536 x 1001).
 template <typename Tx, typename Tr, Quant Q, bool SHIFTED>
@@ -579,6 +582,7 @@ bool by_shared(const NormArgs &a, const Split &sp)
     return sectors && sp.lanes >= (sizeof(Tx) == sizeof(Tr) ? 128 : 256) && a.rows > (int64_t)a.ctas * sp.rows;
 }
 
+// 128 registers a thread for up to 512 threads (24 bytes spill of fp16 rows by registers).
 template <typename Tx, typename Tr, bool SHIFTED, bool SHARED>
 __global__ void __launch_bounds__(512) norm_bwd_rows(NormArgs a, Split sp)
 {

@@ -10,10 +10,10 @@
 //
 // Every input is read once and every output written once.  The order of all sums is fixed by the shape (and the SMs).
 //
-// HBM bounds it where there is enough to do: 65536 rows of 4096 channels, 16 bits, 250-265 us (6.1-6.4 TB/s; a copy
-// runs at 6.8), the backward of 65536 x 2048 217 us (6.2).  A tile of 128 rows by 64 channels costs a CTA 0.9 us alone
-// and 2 us beside another on its SM (16.6 instructions an element, 25 in the backward), an exchange between CTAs 0.45;
-// few channels of long sequences are bound by that chain (65536 x 512: 73 us), short ones by starting it.
+// HBM bounds it where there is enough to do: 65536 rows of 4096 channels, 16 bits, 248-257 us (6.3-6.5 TB/s; a copy
+// runs at 6.8), the backward of 65536 x 2048 205 us (6.5).  A tile of 128 rows by 64 channels costs a CTA 0.9 us alone
+// and 2 us beside another on its SM (16.3 instructions an element, 24.6 in the backward), an exchange between CTAs 0.45;
+// few channels of long sequences are bound by that chain (65536 x 512: 72 us), short ones by starting it.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kCols = 64;       // channels of a CTA: two per lane
-constexpr int kMaxCluster = 12;   // 65536 rows of 512 channels: 4 CTAs 174 us, 8: 96, 12: 73, but 14: 129 and 16: 115
+constexpr int kMaxCluster = 12;   // 65536 rows of 512 channels: 4 CTAs 174 us, 8: 96, 12: 72, but 14: 129 and 16: 115
 constexpr int kSlots = 2;       // tiles whose maps are in shared memory at a time
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -220,7 +220,8 @@ __device__ __forceinline__ float2 decay2(float2 g) { return exp2_fast2(log2_deca
 // their gates, and at most the largest fp32 value.  Gates may rise and fall by more than an exponential's range and
 // still leave the states in theirs; then A may be no fp32 value (or, as a product of decays, come back from 0 or infinity
 // as something else), but its root is one wherever a normal h leaves A h in range, and a (a h) is right in one rounding
-// more.  An h of zero stays zero, whatever a is.
+// more.  An h of zero stays zero, whatever a is.  Against products of decays: the same time where HBM bounds it, 71.6 ->
+// 72.3 us for 65536 x 512, and fp32 outputs nearer to fp64 (3.0e-7 -> 2.3e-7 relative), as a sum rounds less than a product.
 struct Map {
     float2 a, H;
     __device__ __forceinline__ Map() : a{1.f, 1.f}, H{0.f, 0.f} {}

@@ -412,8 +412,9 @@ int gla_norm_fwd(const void *x, const void *res, const float *w, void *y, void *
  *
  *     scale = max(max |y| / 448, 1e-30) over each group of columns,   q = e4m3(y / scale)  (to nearest, ties to even)
  *
- *   q           [rows, D] device, written.  y is not rounded in between; the quotient is formed as y times the fp32
- *               reciprocal of the scale
+ *   q           [rows, D] device, written.  y is not rounded in between; the scale is max |y| times the fp32 value of
+ *               1 / 448, and the quotient y times the scale's fp32 reciprocal (one unit in the last place): each within
+ *               2^-22 of the exact one, so that a y next to a tie may take the code on its other side
  *   scales      [rows, ceil(D / group)] fp32 device, written (the last group may be partial)
  *   group       0 (one scale per row) or 128
  * The rest as for gla_norm_fwd.  A NaN makes its row's values and scales NaN.
