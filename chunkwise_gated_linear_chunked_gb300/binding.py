@@ -29,7 +29,9 @@ EXPORTS = ("gla_fwd", "gla_fwd_workspace_size", "gla_get_status", "gla_strerror"
            "gla_bwd_workspace_size", "gla_ttt_linear_fwd", "gla_ttt_workspace_size", "gla_wy_fwd",
            "gla_wy_workspace_size", "gla_fwd_host", "gla_fwd_host_workspace_size", "gla_scan_fwd", "gla_scan_bwd",
            "gla_scan_step", "gla_scan_workspace_size", "gla_step", "gla_norm_fwd", "gla_norm_quant_fwd",
-           "gla_norm_bwd", "gla_norm_bwd_workspace_size", "gla_scan_shared_workspace")
+           "gla_norm_bwd", "gla_norm_bwd_workspace_size", "gla_scan_shared_workspace", "gla_delta_fwd",
+           "gla_delta_fwd_workspace_size", "gla_delta_bwd", "gla_delta_bwd_workspace_size", "gla_delta_step",
+           "gla_group_norm_fwd", "gla_group_norm_bwd", "gla_group_norm_workspace_size")
 
 if not os.path.exists(LIB):
     raise ImportError(f"libgla.so not built ({LIB}); call chunkwise_gated_linear_chunked_gb300.build.build()")
@@ -91,6 +93,22 @@ _lib.gla_norm_bwd.argtypes = [_p] * 8 + [_i64, _i, _i, _p, _sz, _p]
 _lib.gla_norm_bwd.restype = _i
 _lib.gla_norm_bwd_workspace_size.argtypes = [_i64, _i]
 _lib.gla_norm_bwd_workspace_size.restype = _sz
+_lib.gla_delta_fwd.argtypes = [_p] * 6 + [_f] + [_p] * 3 + [_i] * 8 + [_p, _p, _sz, _p]
+_lib.gla_delta_fwd.restype = _i
+_lib.gla_delta_fwd_workspace_size.argtypes = [_i] * 9
+_lib.gla_delta_fwd_workspace_size.restype = _sz
+_lib.gla_delta_bwd.argtypes = [_p] * 6 + [_f] + [_p] * 9 + [_i] * 8 + [_p, _p, _sz, _p]
+_lib.gla_delta_bwd.restype = _i
+_lib.gla_delta_bwd_workspace_size.argtypes = [_i] * 9
+_lib.gla_delta_bwd_workspace_size.restype = _sz
+_lib.gla_delta_step.argtypes = [_p] * 6 + [_f] + [_p] * 3 + [_i] * 7 + [_p, _p]
+_lib.gla_delta_step.restype = _i
+_lib.gla_group_norm_fwd.argtypes = [_p] * 6 + [_i64, _i64, _i, _i, _f, _i, _i, _p, _sz, _p]
+_lib.gla_group_norm_fwd.restype = _i
+_lib.gla_group_norm_bwd.argtypes = [_p] * 9 + [_i64, _i64, _i, _i, _i, _i, _p, _sz, _p]
+_lib.gla_group_norm_bwd.restype = _i
+_lib.gla_group_norm_workspace_size.argtypes = [_i64, _i64, _i, _i, _i, _i]
+_lib.gla_group_norm_workspace_size.restype = _sz
 
 
 class _NoCalls:
@@ -410,7 +428,7 @@ def _status_workspace(workspace, device: int):
 
 def layer_status(device=None, stream=None) -> int:
     """What the kernels of ``scan_fwd``, ``scan_bwd``, ``scan_step`` and ``gla_step`` calls without a workspace of their
-    own have reported on a device (default: the current one) since the last look: GLA_OK, or the code of the first error,
+    own, and of ``delta_fwd``, ``delta_bwd`` and ``delta_step`` calls without a ``status`` of their own, have reported on a device (default: the current one) since the last look: GLA_OK, or the code of the first error,
     which this call clears.  Waits for ``stream`` (default: the current one); what runs on other streams may report
     later.  One word serves all streams; a call's own ``workspace`` (256 zeroed bytes) and ``get_status`` tell its errors
     apart."""
@@ -784,6 +802,235 @@ def _norm_bwd_checked(s, rstd, dy, weight, ds, want_dw, workspace):
     if rc != GLA_OK:
         raise GlaError(rc, "gla_norm_bwd")
     return dx, dres, dw
+
+
+# ---------------------------------------------------------------------------------------------------------
+# Gated delta rule, and group norm with an activation
+# ---------------------------------------------------------------------------------------------------------
+
+# (input, output) types of the delta rule -> dtype code
+DELTA_CODE = {(torch.float32, torch.float32): GLA_F32, (torch.bfloat16, torch.float32): GLA_BF16,
+              (torch.bfloat16, torch.bfloat16): GLA_BF16_OBF16, (torch.float16, torch.float32): GLA_F16,
+              (torch.float16, torch.float16): GLA_F16_OF16}
+_ACTIVATION = {None: 0, "silu": 1}
+
+
+def _scratch(what, workspace, nbytes, device):
+    """(tensor, address, bytes) of a call's scratch: the caller's, or memory of the call's own."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: workspace must be a contiguous tensor on cuda:{device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _delta_shape(what, q, v, rank):
+    """(leading sizes, H, HV, K, V) of q [..., H, K] and v [..., HV, V]."""
+    if not isinstance(v, torch.Tensor) or q.dim() != rank or v.dim() != rank or q.shape[:-2] != v.shape[:-2]:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: expected q, k [{'B, ' * (rank == 3) or 'B, T, '}H, K] and v [..., HV, V] "
+                                            f"with the same leading sizes")
+    (H, K), (HV, V) = q.shape[-2:], v.shape[-2:]
+    if H < 1 or HV < 1 or HV % H:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {HV} value heads do not share {H} key heads evenly")
+    return q.shape[:-2], H, HV, K, V
+
+
+def _delta_inputs(what, q, k, v, g, beta, lead, HV, device):
+    _check(what, "q", q, q.dtype, q.shape, device)
+    _check(what, "k", k, q.dtype, q.shape, device)
+    _check(what, "v", v, q.dtype, v.shape, device)
+    _check(what, "g", g, torch.float32, (*lead, HV), device)
+    _check(what, "beta", beta, torch.float32, (*lead, HV), device)
+
+
+def _sequences(what, B, cu_seqlens, device):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
+            cu_seqlens.get_device() != device or not cu_seqlens.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: cu_seqlens must be a contiguous int32 vector on cuda:{device}")
+    return cu_seqlens.numel() - 1
+
+
+def delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, output_final_state=True, cu_seqlens=None, out_dtype=None,
+              status=None, workspace=None, stream=None):
+    """Gated delta rule on the GPU: S~ = exp(g_t) S, S = S~ + k_t^T beta_t (v_t - k_t S~), o_t = scale q_t S.
+
+    q, k: [B, T, H, K]; v: [B, T, HV, V] (cuda, contiguous, all fp32, bf16 or fp16; HV a multiple of H, each key head
+    serving HV / H value heads in a row; K, V up to 256); g, beta: fp32 [B, T, HV].  Keys are taken as they are: normalise
+    them before (``norm_fwd`` with a weight of K^-0.5 gives unit length).  scale: K^-0.5 by default.  initial_state: fp32
+    [N, HV, K, V] or None.  cu_seqlens: int32 [N+1] cuda offsets (B == 1); rows outside all sequences keep what the
+    allocator left in them.  out_dtype: q's type (default) or fp32.  Returns (o [B, T, HV, V], final state fp32
+    [N, HV, K, V] or None).  Bad offsets are reported on the device, see ``layer_status`` (or the call's own ``status``,
+    256 zeroed bytes).
+    """
+    return _delta_fwd_checked(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype, status,
+                              workspace, stream=stream)
+
+
+@_on_stream
+def _delta_fwd_checked(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype, status, workspace):
+    what, device = "gla_delta_fwd", q.get_device()
+    lead, H, HV, K, V = _delta_shape(what, q, v, 4)
+    code = DELTA_CODE.get((q.dtype, out_dtype or q.dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what} dtypes q {q.dtype} -> {out_dtype}")
+    _delta_inputs(what, q, k, v, g, beta, lead, HV, device)
+    (B, T), N = lead, _sequences(what, lead[0], cu_seqlens, device)
+    if initial_state is not None:
+        _check(what, "initial_state", initial_state, torch.float32, (N, HV, K, V), device)
+    o = torch.empty(v.shape, dtype=out_dtype or q.dtype, device=device)
+    ht = torch.empty(N, HV, K, V, dtype=torch.float32, device=device) if output_final_state else None
+    need = _lib.gla_delta_fwd_workspace_size(N, B, T, H, HV, K, V, code, cu_seqlens is not None)
+    workspace, at, nbytes = _scratch(what, workspace, need, device)
+    rc = _lib.gla_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), o.data_ptr(),
+                            K ** -0.5 if scale is None else scale, _at(initial_state), _at(ht), _at(cu_seqlens), N, B, T,
+                            H, HV, K, V, code, _status_workspace(status, device)[0], at, nbytes, _raw_stream(device))
+    if rc != GLA_OK:
+        raise GlaError(rc, what)
+    return o, ht
+
+
+def delta_bwd(q, k, v, g, beta, do, scale=None, initial_state=None, dht=None, cu_seqlens=None, want_dh0=True, status=None,
+              workspace=None, stream=None):
+    """Gradients of ``delta_fwd`` for L = sum(o * do) + sum(ht * dht); the states are computed again.
+
+    The inputs as for delta_fwd; do: [B, T, HV, V] of q's type; dht: fp32 [N, HV, K, V] or None.  Returns (dq, dk, dv in
+    q's type, dg, dbeta fp32 [B, T, HV], dh0 fp32 [N, HV, K, V] or None).
+    """
+    return _delta_bwd_checked(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0, status, workspace,
+                              stream=stream)
+
+
+@_on_stream
+def _delta_bwd_checked(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0, status, workspace):
+    what, device = "gla_delta_bwd", q.get_device()
+    lead, H, HV, K, V = _delta_shape(what, q, v, 4)
+    code = _NORM_CODE.get(q.dtype)
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what} dtype {q.dtype}")
+    _delta_inputs(what, q, k, v, g, beta, lead, HV, device)
+    _check(what, "do", do, q.dtype, v.shape, device)
+    (B, T), N = lead, _sequences(what, lead[0], cu_seqlens, device)
+    for name, t in (("initial_state", initial_state), ("dht", dht)):
+        if t is not None:
+            _check(what, name, t, torch.float32, (N, HV, K, V), device)
+    dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
+    dh0 = torch.empty(N, HV, K, V, dtype=torch.float32, device=device) if want_dh0 else None
+    need = _lib.gla_delta_bwd_workspace_size(N, B, T, H, HV, K, V, code, cu_seqlens is not None)
+    workspace, at, nbytes = _scratch(what, workspace, need, device)
+    rc = _lib.gla_delta_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), do.data_ptr(),
+                            K ** -0.5 if scale is None else scale, _at(initial_state), _at(dht), dq.data_ptr(),
+                            dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _at(dh0), _at(cu_seqlens), N, B,
+                            T, H, HV, K, V, code, _status_workspace(status, device)[0], at, nbytes, _raw_stream(device))
+    if rc != GLA_OK:
+        raise GlaError(rc, what)
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def delta_step(q, k, v, g, beta, state, scale=None, slots=None, state_out=None, out_dtype=None, status=None, stream=None):
+    """One token of ``delta_fwd``'s recurrence for each of B sequences, with the states in a pool.
+
+    q, k: [B, H, K]; v: [B, HV, V] (types as for delta_fwd); g, beta: fp32 [B, HV]; state: fp32 [S, HV, K, V] pool,
+    updated in place (or written to state_out, of which only the addressed rows are written); slots as for scan_step.
+    out_dtype: q's type (default) or fp32.  Returns o [B, HV, V].
+    """
+    return _delta_step_checked(q, k, v, g, beta, state, scale, slots, state_out, out_dtype, status, stream=stream)
+
+
+@_on_stream
+def _delta_step_checked(q, k, v, g, beta, state, scale, slots, state_out, out_dtype, status):
+    what, device = "gla_delta_step", q.get_device()
+    lead, H, HV, K, V = _delta_shape(what, q, v, 3)
+    code = DELTA_CODE.get((q.dtype, out_dtype or q.dtype))
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what} dtypes q {q.dtype} -> {out_dtype}")
+    _delta_inputs(what, q, k, v, g, beta, lead, HV, device)
+    B, = lead
+    S, state_out = _pool(what, state, state_out, slots, B, (HV, K, V), device)
+    o = torch.empty(v.shape, dtype=out_dtype or q.dtype, device=device)
+    rc = _lib.gla_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), o.data_ptr(),
+                             K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B,
+                             S, H, HV, K, V, code, _status_workspace(status, device)[0], _raw_stream(device))
+    if rc != GLA_OK:
+        raise GlaError(rc, what)
+    return o
+
+
+def _group_norm_args(what, x, groups, weight, bias, activation):
+    """(N, S, C, dtype code, activation code) of a group norm of x [N, ..., C]."""
+    code = _NORM_CODE.get(x.dtype)
+    if code is None:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what} dtype {x.dtype}")
+    if activation not in _ACTIVATION:
+        raise GlaError(GLA_ERR_UNSUPPORTED, f"{what}: activation {activation!r}")
+    if x.dim() < 2 or not x.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: x must be a contiguous [N, ..., C] tensor")
+    N, C = x.shape[0], x.shape[-1]
+    S = math.prod(x.shape[1:-1])
+    if groups < 1 or C < 1 or C % groups or S < 1:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: {groups} groups of {C} channels at {S} positions")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(what, name, t, torch.float32, (C,), x.get_device())
+    return N, S, C, code, _ACTIVATION[activation]
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, activation=None, eps=1e-5, workspace=None, stream=None):
+    """Group norm with an activation, channels last: y = act((x - mean) rstd weight + bias), mean and rstd over all
+    positions and the channels of a group.
+
+    x: contiguous [N, ..., C] fp32 / bf16 / fp16; a two-dimensional x [rows, C] has one position a row, as the heads of a
+    mixing layer's output have (groups: the heads).  weight, bias: fp32 [C] or None; activation: None or "silu".
+    Returns (y in x's type, mean, rstd fp32 [N, groups]).
+    """
+    return _group_norm_fwd_checked(x, groups, weight, bias, activation, eps, workspace, stream=stream)
+
+
+@_on_stream
+def _group_norm_fwd_checked(x, groups, weight, bias, activation, eps, workspace):
+    what, device = "gla_group_norm_fwd", x.get_device()
+    N, S, C, code, act = _group_norm_args(what, x, groups, weight, bias, activation)
+    y = torch.empty_like(x)
+    mean, rstd = (torch.empty(N, groups, dtype=torch.float32, device=device) for _ in range(2))
+    workspace, at, nbytes = _scratch(what, workspace, _lib.gla_group_norm_workspace_size(N, S, C, groups, code, 0), device)
+    rc = _lib.gla_group_norm_fwd(x.data_ptr(), _at(weight), _at(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), N, S,
+                                 C, groups, eps, act, code, at, nbytes, _raw_stream(device))
+    if rc != GLA_OK:
+        raise GlaError(rc, what)
+    return y, mean, rstd
+
+
+def group_norm_bwd(x, mean, rstd, dy, weight=None, bias=None, activation=None, want_dw=True, workspace=None, stream=None):
+    """Gradients of ``group_norm_fwd`` from its input and statistics, for the gradient dy of y.
+
+    Returns (dx in x's type, dw fp32 [C] or None without a weight, db fp32 [C] or None without a bias);
+    ``want_dw=False`` skips both.
+    """
+    return _group_norm_bwd_checked(x, mean, rstd, dy, weight, bias, activation, want_dw, workspace, stream=stream)
+
+
+@_on_stream
+def _group_norm_bwd_checked(x, mean, rstd, dy, weight, bias, activation, want_dw, workspace):
+    what, device = "gla_group_norm_bwd", x.get_device()
+    if mean.dim() != 2:
+        raise GlaError(GLA_ERR_INVALID_ARG, f"{what}: mean must be [N, groups]")
+    groups = mean.shape[1]
+    N, S, C, code, act = _group_norm_args(what, x, groups, weight, bias, activation)
+    _check(what, "mean", mean, torch.float32, (N, groups), device)
+    _check(what, "rstd", rstd, torch.float32, (N, groups), device)
+    _check(what, "dy", dy, x.dtype, x.shape, device)
+    dx = torch.empty_like(x)
+    dw, db = (torch.empty(C, dtype=torch.float32, device=device) if want_dw and t is not None else None for t in (weight, bias))
+    workspace, at, nbytes = _scratch(what, workspace, _lib.gla_group_norm_workspace_size(N, S, C, groups, code, 1), device)
+    rc = _lib.gla_group_norm_bwd(x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _at(weight), _at(bias), dy.data_ptr(),
+                                 dx.data_ptr(), _at(dw), _at(db), N, S, C, groups, act, code, at, nbytes,
+                                 _raw_stream(device))
+    if rc != GLA_OK:
+        raise GlaError(rc, what)
+    return dx, dw, db
 
 
 def get_status(workspace, stream=None) -> int:

@@ -45,7 +45,10 @@ enum KernelId {
     K_BWD_SUMS = 8, K_BWD_SCAN = 9, K_BWD_GRADS = 10, K_BWD_DG = 11, K_TTT = 12, K_WY = 13,
     K_WY_TC = 14, K_BWD_SUMS_TC = 15, K_BWD_GRADS_TC = 16, K_TTT_TC = 17,
     K_SCAN_FWD = 18, K_SCAN_BWD = 19, K_SCAN_STEP = 20, K_GLA_STEP = 21, K_NORM_FWD = 22, K_NORM_QUANT = 23,
-    K_NORM_BWD = 24, K_NORM_DW = 25, K_SCAN_FWD_ROWS = 26, K_SCAN_BWD_ROWS = 27
+    K_NORM_BWD = 24, K_NORM_DW = 25, K_SCAN_FWD_ROWS = 26, K_SCAN_BWD_ROWS = 27,
+    K_DELTA_COLS = 28, K_DELTA_COLS_BACK = 29, K_DELTA_ROWS = 30, K_DELTA_ROWS_BACK = 31, K_DELTA_JOIN = 32, K_DELTA_GATES = 33,
+    K_DELTA_STEP = 34, K_DELTA_PREP = 35, K_DELTA_CHAIN = 36, K_DELTA_CHAIN_BACK = 37, K_DELTA_GRADS = 38, K_GN_TOKENS = 39,
+    K_GN_SUMS = 40, K_GN_APPLY = 41, K_GN_TOKENS_BACK = 42, K_GN_GRAD_SUMS = 43, K_GN_GRAD = 44, K_GN_DW = 45
 };
 
 // Launch one kernel through `fn`, bracketed by the profiling events when they are armed.

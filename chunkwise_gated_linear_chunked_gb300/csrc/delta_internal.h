@@ -1,0 +1,116 @@
+// Internal declarations of the gated delta rule: entry points in delta_api.cu, the token-by-token kernels for any type
+// and head size in delta_scan.cu, the chunked tensor-core kernels in delta_mma.cu and delta_grads.cu, one token in
+// delta_step.cu.
+#pragma once
+
+#include "gla_internal.h"
+#include "layer_internal.h"
+
+namespace gla {
+
+// Forward and backward (passed by value).  Rows are tokens of all sequences; key head of value head hv: hv / (HV / H).
+struct DeltaArgs {
+    const void *q, *k, *v, *dout;      // [rows, H, K], [rows, H, K], [rows, HV, V], [rows, HV, V]
+    const float *g, *beta;             // [rows, HV]
+    const float *h0, *dht;             // [N, HV, K, V] or nullptr
+    const int32_t *cu;                 // device offsets or nullptr
+    void *o, *dq, *dk, *dv;
+    float *ht, *dg, *dbeta, *dh0;
+    float scale;
+    int N, B, T, H, HV, K, V;
+    int64_t rows;                      // B * T
+    int slots;                         // (sequence, chunk of 64 rows) pairs, an upper bound in packs
+    int *status;
+    // workspace of the backward's token-by-token kernels, fp32
+    float *upd, *dx;                   // [rows, HV, V]: update rows of the state, and their gradients over beta
+    float *dqh, *eh, *fh;              // [rows, HV, K]: gradients of q, and of k by way of k S and of k^T n
+    float *dG;                         // [rows, HV]: gradient of the running sum of gates
+    float *hd;                         // [N, HV, K]: rows of <ht, dht>
+    // workspace of the chunked kernels
+    char *chunk;
+};
+
+// One token (passed by value).
+struct DeltaStepArgs {
+    const void *q, *k, *v;             // [B, H, K], [B, H, K], [B, HV, V]
+    const float *g, *beta, *h0;
+    void *o;
+    float *ht;
+    const int32_t *slots;
+    float scale;
+    int B, S, H, HV, K, V;
+    int *status;
+};
+
+constexpr int kDeltaChunk = 64;        // rows of a chunk
+
+// Rows of sequence n, [bos, bos + len).  False for offsets outside [0, T] or decreasing.
+__device__ __forceinline__ bool delta_sequence(const DeltaArgs &a, int n, int &bos, int &len)
+{
+    if (!a.cu) {
+        bos = n * a.T;
+        len = a.T;
+        return true;
+    }
+    bos = a.cu[n];
+    const int eos = a.cu[n + 1];
+    len = eos - bos;
+    return bos >= 0 && len >= 0 && eos <= a.T;
+}
+
+// Slots of a pack's sequence n start at cu[n] / 64 + n: at least as many as it has chunks before the next one's first.
+__device__ __forceinline__ int delta_first_slot(const DeltaArgs &a, int n)
+{
+    return a.cu ? a.cu[n] / kDeltaChunk + n : n * ((a.T + kDeltaChunk - 1) / kDeltaChunk);
+}
+
+// The chunk of a slot: its sequence, its number in it, its first row and its rows.  False for a slot without rows.
+__device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int &n, int &c, int &row, int &rows)
+{
+    if (!a.cu) {
+        const int per = (a.T + kDeltaChunk - 1) / kDeltaChunk;
+        n = slot / per;
+    } else {
+        int lo = 0, hi = a.N - 1;   // the last sequence that starts at or before the slot
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (delta_first_slot(a, mid) <= slot)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        n = lo;
+    }
+    int bos, len;
+    if (!delta_sequence(a, n, bos, len))
+        return false;
+    c = slot - delta_first_slot(a, n);
+    if (c < 0 || (int64_t)c * kDeltaChunk >= len)
+        return false;
+    row = bos + c * kDeltaChunk;
+    rows = min(kDeltaChunk, len - c * kDeltaChunk);
+    return true;
+}
+
+cudaError_t launch_delta_cols(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);
+cudaError_t launch_delta_rows(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);
+cudaError_t launch_delta_join(const DeltaArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_delta_gates(const DeltaArgs &a, cudaStream_t s);
+cudaError_t launch_delta_step(const DeltaStepArgs &a, int dtype, cudaStream_t s);
+
+// Calls f with null pointers of the (input, output) types of a dtype code.
+template <typename F>
+cudaError_t delta_types(int dtype, F f)
+{
+    typedef __nv_bfloat16 bf;
+    switch (dtype) {
+    case GLA_F32: return f((float *)0, (float *)0);
+    case GLA_BF16: return f((bf *)0, (float *)0);
+    case GLA_BF16_OBF16: return f((bf *)0, (bf *)0);
+    case GLA_F16: return f((__half *)0, (float *)0);
+    case GLA_F16_OF16: return f((__half *)0, (__half *)0);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace gla

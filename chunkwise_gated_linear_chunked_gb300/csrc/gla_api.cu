@@ -380,6 +380,24 @@ extern "C" const char *gla_kernel_name(int kernel_id)
     case K_NORM_DW: return "norm_dw";
     case K_SCAN_FWD_ROWS: return "scan_fwd_rows";
     case K_SCAN_BWD_ROWS: return "scan_bwd_rows";
+    case K_DELTA_COLS: return "delta_cols";
+    case K_DELTA_COLS_BACK: return "delta_cols_bwd";
+    case K_DELTA_ROWS: return "delta_rows";
+    case K_DELTA_ROWS_BACK: return "delta_rows_bwd";
+    case K_DELTA_JOIN: return "delta_join";
+    case K_DELTA_GATES: return "delta_gates";
+    case K_DELTA_STEP: return "delta_step";
+    case K_DELTA_PREP: return "delta_prep";
+    case K_DELTA_CHAIN: return "delta_chain";
+    case K_DELTA_CHAIN_BACK: return "delta_chain_bwd";
+    case K_DELTA_GRADS: return "delta_grads";
+    case K_GN_TOKENS: return "group_norm_tokens";
+    case K_GN_SUMS: return "group_norm_sums";
+    case K_GN_APPLY: return "group_norm_apply";
+    case K_GN_TOKENS_BACK: return "group_norm_tokens_bwd";
+    case K_GN_GRAD_SUMS: return "group_norm_bwd_sums";
+    case K_GN_GRAD: return "group_norm_bwd";
+    case K_GN_DW: return "group_norm_dw";
     default: return "unknown";
     }
 }

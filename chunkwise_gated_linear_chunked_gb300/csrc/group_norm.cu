@@ -1,0 +1,656 @@
+// Group norm with an activation, channels last.  For sample n and group j of W = C / G channels, over all its positions:
+//
+//     mean, var over S x W values,   rstd = 1 / sqrt(var + eps),   xh = (x - mean) rstd,   z = xh w + b,   y = act(z)
+//     dz = dy act'(z),   a = w dz,   dx = rstd (a - mean(a) - xh mean(a xh)),   dw = sum dz xh,   db = sum dz
+//
+// Bound by HBM (two instructions an element a byte or so).  Two ways:
+//
+// One position a sample (tokens) and at most 4096 channels a group: a group is a run of memory that up to 256 lanes hold
+// in registers, so that it is read once; variances are sums of squares about the mean.  A lane keeps its channels from
+// sample to sample, with their weights and its share of dw and db in registers.
+//
+// Otherwise (maps): samples are cut into slices of positions.  A CTA walks a slice with a vector of channels a thread and
+// sums per channel, about the thread's first value (a value of the group itself, so the sum of squares loses at most the
+// thread's count of units to the cancellation), joins the threads' means and squares by group, and a second kernel joins
+// the slices and writes y (dx); it reads x again, from L2 where the tensor fits.  Every join has a fixed order, so results
+// do not depend on timing.
+#include <algorithm>
+#include <numeric>
+#include <type_traits>
+
+#include "api_common.h"
+#include "group_norm.h"
+#include "layer_internal.h"
+#include "tc_ptx.cuh"
+
+namespace gla {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int VEC>
+struct alignas(VEC * sizeof(T)) Vec {
+    T v[VEC];
+};
+
+// sigmoid(z); its error is that of ex2 and rcp, about 3 units in the last place.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(-z * kLog2e)));
+    return r;
+}
+
+__device__ __forceinline__ float activated(float z, bool silu) { return silu ? z * sigmoid(z) : z; }
+
+// The gradient before the activation.
+__device__ __forceinline__ float before_act(float dy, float z, bool silu)
+{
+    if (!silu)
+        return dy;
+    const float s = sigmoid(z);
+    return dy * s * fmaf(z, 1.f - s, 1.f);
+}
+
+// Count, mean and sum of squares about the mean of some values.
+struct Moments {
+    float n, mean, m2;
+};
+__device__ __forceinline__ Moments joined(Moments a, Moments b)
+{
+    if (a.n == 0.f || b.n == 0.f)
+        return a.n == 0.f ? b : a;
+    const float n = a.n + b.n, d = b.mean - a.mean, f = b.n / n;
+    return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * (a.n * f)};
+}
+__device__ __forceinline__ Moments shuffled(Moments a, int m)
+{
+    return {__shfl_xor_sync(~0u, a.n, m), __shfl_xor_sync(~0u, a.mean, m), __shfl_xor_sync(~0u, a.m2, m)};
+}
+__device__ __forceinline__ Moments over_warp(Moments a)
+{
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {   // the lower lane's first on both sides, so that they agree
+        const Moments b = shuffled(a, m);
+        a = threadIdx.x & m ? joined(b, a) : joined(a, b);
+    }
+    return a;
+}
+
+// Sum of two values over the lanes of a group: L lanes of a warp, or L / 32 warps by way of shared memory.
+__device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
+{
+    const int in = L < 32 ? L : 32;
+    for (int m = in / 2; m; m /= 2) {
+        v.x += __shfl_xor_sync(~0u, v.x, m);
+        v.y += __shfl_xor_sync(~0u, v.y, m);
+    }
+    if (L > 32) {
+        const int warp = threadIdx.x / 32, first = warp & ~(L / 32 - 1);
+        __syncthreads();
+        if (threadIdx.x % 32 == 0)
+            part[warp] = v;
+        __syncthreads();
+        v = part[first];
+        for (int i = 1; i < L / 32; ++i) {
+            v.x += part[first + i].x;
+            v.y += part[first + i].y;
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Tokens: one position a sample.  Unit u is group u % G of sample u / G; a CTA holds kThreads / L units, and the grid's
+// units are a multiple of G, so that a lane's next unit has the same channels.
+// ---------------------------------------------------------------------------------------------------------
+template <typename T, int VEC, int NV, bool BACK>
+__global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L)
+{
+    __shared__ float2 part[kThreads / 32];
+    tc::grid_dep_wait();
+    const int W = a.W, lane = threadIdx.x % L, per = kThreads / L;
+    const int64_t units = a.N * a.G, stride = (int64_t)gridDim.x * per;
+    const int64_t u0 = (int64_t)blockIdx.x * per + threadIdx.x / L;
+    const int c0 = (int)(u0 % a.G) * W;
+    const bool silu = a.silu;
+    const float inv = 1.f / W;
+    typedef Vec<T, VEC> V;
+    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    bool on[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + L * i) * VEC;
+        on[i] = c < W;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            w[i][e] = a.w && on[i] ? a.w[c0 + c + e] : 1.f;
+            b[i][e] = a.b && on[i] ? a.b[c0 + c + e] : 0.f;
+            dw[i][e] = db[i][e] = 0.f;
+        }
+    }
+    auto ask = [&](const void *p, int64_t u, V (&r)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (on[i] && u < units)
+                r[i] = *reinterpret_cast<const V *>(static_cast<const T *>(p) + u * W + (lane + L * i) * VEC);
+    };
+    V next[NV] = {}, next_dy[NV] = {};
+    ask(a.x, u0, next);
+    if constexpr (BACK)
+        ask(a.dy, u0, next_dy);
+    // all of a CTA's units take the same turns, as they may share its barriers
+    for (int64_t base = (int64_t)blockIdx.x * per; base < units; base += stride) {
+        const int64_t u = base + threadIdx.x / L;
+        const bool live = u < units;
+        V x[NV], dy[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = next[i];
+            if constexpr (BACK)
+                dy[i] = next_dy[i];
+        }
+        ask(a.x, u + stride, next);
+        if constexpr (BACK)
+            ask(a.dy, u + stride, next_dy);
+        if constexpr (!BACK) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    sum += on[i] ? widen(x[i].v[e]) : 0.f;
+            const float mean = group_sum(make_float2(sum, 0.f), L, part).x * inv;
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float d = on[i] ? widen(x[i].v[e]) - mean : 0.f;
+                    sq = fmaf(d, d, sq);
+                }
+            const float rstd = rsqrtf(fmaf(group_sum(make_float2(sq, 0.f), L, part).x, inv, a.eps));
+            if (!live)
+                continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!on[i])
+                    continue;
+                V y;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    y.v[e] = narrow<T>(activated(fmaf((widen(x[i].v[e]) - mean) * rstd, w[i][e], b[i][e]), silu));
+                *reinterpret_cast<V *>(static_cast<T *>(a.y) + u * W + (lane + L * i) * VEC) = y;
+            }
+            if (lane == 0) {
+                a.mean[u] = mean;
+                a.rstd[u] = rstd;
+            }
+        } else {
+            const float mean = live ? a.mean_in[u] : 0.f, rstd = live ? a.rstd_in[u] : 0.f;
+            float xh[NV][VEC], g[NV][VEC];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (!on[i] || !live)
+                        continue;
+                    const float n = (widen(x[i].v[e]) - mean) * rstd;
+                    const float dz = before_act(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]), silu);
+                    db[i][e] += dz;
+                    dw[i][e] = fmaf(dz, n, dw[i][e]);
+                    xh[i][e] = n;
+                    g[i][e] = dz * w[i][e];
+                    sum = make_float2(sum.x + g[i][e], fmaf(g[i][e], n, sum.y));
+                }
+            sum = group_sum(sum, L, part);
+            if (!live)
+                continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!on[i])
+                    continue;
+                V dx;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    dx.v[e] = narrow<T>(rstd * (g[i][e] - inv * fmaf(xh[i][e], sum.y, sum.x)));
+                *reinterpret_cast<V *>(static_cast<T *>(a.dx) + u * W + (lane + L * i) * VEC) = dx;
+            }
+        }
+    }
+    if constexpr (BACK) {
+        if (!a.part_dw)
+            return;
+        float *pw = a.part_dw + (size_t)u0 * W, *pb = a.part_db + (size_t)u0 * W;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (on[i]) {
+                    pw[(lane + L * i) * VEC + e] = dw[i][e];
+                    pb[(lane + L * i) * VEC + e] = db[i][e];
+                }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Maps.  CTA (sample, slice of positions, chunk of channels): TX threads on adjacent vectors, TY rows at a time.
+// ---------------------------------------------------------------------------------------------------------
+struct Slice {
+    int64_t n, row0, rows;     // sample, first position and positions
+    int slice, chunk, c0, cc;  // channels [c0, c0 + cc)
+};
+__device__ __forceinline__ Slice slice_of(const GroupNormArgs &a, const GroupNormSplit &s)
+{
+    Slice r;
+    r.chunk = blockIdx.x % s.chunks;
+    const int64_t i = blockIdx.x / s.chunks;
+    r.slice = (int)(i % s.slices);
+    r.n = i / s.slices;
+    r.row0 = r.slice * s.rows;
+    r.rows = min(s.rows, a.S - r.row0);
+    r.c0 = r.chunk * s.chunk;
+    r.cc = min(s.chunk, a.C - r.c0);
+    return r;
+}
+
+// Sums over the TY rows that a CTA takes at a time: what each thread holds for its channels goes to `to`, [TY][chunk].
+template <int VEC>
+__device__ __forceinline__ void lay_out(float2 *to, const float2 (&v)[VEC], int tx, int ty, int chunk)
+{
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        to[ty * chunk + tx * VEC + e] = v[e];
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, GroupNormSplit sp)
+{
+    __shared__ float2 held[kThreads * VEC];
+    tc::grid_dep_wait();
+    const Slice s = slice_of(a, sp);
+    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
+    const bool on = ty < sp.ty && tx * VEC < s.cc;
+    typedef Vec<T, VEC> V;
+    const T *x = static_cast<const T *>(a.x) + (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
+    float first[VEC], s1[VEC] = {}, s2[VEC] = {};
+    if (on && ty < s.rows) {
+        const V v = *reinterpret_cast<const V *>(x + (int64_t)ty * a.C);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            first[e] = widen(v.v[e]);
+#pragma unroll 4
+        for (int64_t r = ty + sp.ty; r < s.rows; r += sp.ty) {
+            const V v = *reinterpret_cast<const V *>(x + r * a.C);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float d = widen(v.v[e]) - first[e];
+                s1[e] += d;
+                s2[e] = fmaf(d, d, s2[e]);
+            }
+        }
+    }
+    auto rows_of = [&](int y) { return y < s.rows ? (float)((s.rows - y + sp.ty - 1) / sp.ty) : 0.f; };
+    if (on) {
+        float2 m[VEC];
+        const float many = rows_of(ty);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            m[e] = many > 0.f ? make_float2(first[e] + s1[e] / many, fmaxf(s2[e] - s1[e] * (s1[e] / many), 0.f)) : make_float2(0.f, 0.f);
+        // a NaN among the values is not lost in the maximum
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (s2[e] != s2[e] || s1[e] != s1[e])
+                m[e].y = s2[e] + s1[e];
+        lay_out<VEC>(held, m, tx, ty, sp.chunk);
+    }
+    __syncthreads();
+    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
+    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+        const int lo = max(g * a.W, s.c0) - s.c0, hi = min((g + 1) * a.W, s.c0 + s.cc) - s.c0;
+        Moments m = {0.f, 0.f, 0.f};
+        const int many = (hi - lo) * sp.ty;
+        for (int i = lane; i < many; i += 32) {
+            const int y = i / (hi - lo), c = lo + i - y * (hi - lo);
+            const float2 h = held[y * sp.chunk + c];
+            m = joined(m, {rows_of(y), h.x, h.y});
+        }
+        m = over_warp(m);
+        if (lane == 0)
+            a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(m.n, m.mean, m.m2, 0.f);
+    }
+}
+
+// The statistics of the groups of a CTA's chunk, joined over the slices, by warps in turn; to shared memory.
+__device__ __forceinline__ void join_slices(const GroupNormArgs &a, const GroupNormSplit &sp, const Slice &s, float2 *stat)
+{
+    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
+    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+        const int k0 = g * a.W / sp.chunk, k1 = ((g + 1) * a.W - 1) / sp.chunk, chunks = k1 - k0 + 1;   // chunks with its channels
+        Moments m = {0.f, 0.f, 0.f};
+        for (int i = lane; i < sp.slices * chunks; i += 32) {
+            const int sl = i / chunks, k = k0 + i - sl * chunks;
+            const float4 p = a.part[(s.n * sp.slices + sl) * sp.entries + g + k];
+            m = joined(m, {p.x, p.y, p.z});
+        }
+        m = over_warp(m);
+        const float rstd = rsqrtf(m.m2 / m.n + a.eps);
+        if (lane == 0) {
+            stat[g - g0] = make_float2(m.mean, rstd);
+            if (s.slice == 0 && k0 == s.chunk) {   // one CTA writes them
+                a.mean[s.n * a.G + g] = m.mean;
+                a.rstd[s.n * a.G + g] = rstd;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) maps_apply_kernel(GroupNormArgs a, GroupNormSplit sp)
+{
+    extern __shared__ float2 stat[];
+    tc::grid_dep_wait();
+    const Slice s = slice_of(a, sp);
+    join_slices(a, sp, s, stat);
+    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx, g0 = s.c0 / a.W;
+    if (ty >= sp.ty || tx * VEC >= s.cc)
+        return;
+    const bool silu = a.silu;
+    float mean[VEC], f[VEC], b[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int c = s.c0 + tx * VEC + e;
+        const float2 st = stat[c / a.W - g0];
+        mean[e] = st.x;
+        f[e] = a.w ? st.y * a.w[c] : st.y;
+        b[e] = a.b ? a.b[c] : 0.f;
+    }
+    typedef Vec<T, VEC> V;
+    const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
+    const T *x = static_cast<const T *>(a.x) + at;
+    T *y = static_cast<T *>(a.y) + at;
+#pragma unroll 4
+    for (int64_t r = ty; r < s.rows; r += sp.ty) {
+        const V v = *reinterpret_cast<const V *>(x + r * a.C);
+        V o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            o.v[e] = narrow<T>(activated(fmaf(widen(v.v[e]) - mean[e], f[e], b[e]), silu));
+        *reinterpret_cast<V *>(y + r * a.C) = o;
+    }
+}
+
+// Backward, first pass: dz and dz xh summed per channel over a slice, and w times them by group.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs a, GroupNormSplit sp)
+{
+    __shared__ float2 held[kThreads * VEC];
+    tc::grid_dep_wait();
+    const Slice s = slice_of(a, sp);
+    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
+    const bool silu = a.silu;
+    if (ty < sp.ty && tx * VEC < s.cc) {
+        float mean[VEC], rstd[VEC], w[VEC], b[VEC];
+        float2 sum[VEC] = {};   // dz, dz xh
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = s.c0 + tx * VEC + e;
+            const int64_t g = s.n * a.G + c / a.W;
+            mean[e] = a.mean_in[g];
+            rstd[e] = a.rstd_in[g];
+            w[e] = a.w ? a.w[c] : 1.f;
+            b[e] = a.b ? a.b[c] : 0.f;
+        }
+        typedef Vec<T, VEC> V;
+        const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
+        const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
+#pragma unroll 4
+        for (int64_t r = ty; r < s.rows; r += sp.ty) {
+            const V v = *reinterpret_cast<const V *>(x + r * a.C), d = *reinterpret_cast<const V *>(dy + r * a.C);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float n = (widen(v.v[e]) - mean[e]) * rstd[e];
+                const float dz = before_act(widen(d.v[e]), fmaf(n, w[e], b[e]), silu);
+                sum[e] = make_float2(sum[e].x + dz, fmaf(dz, n, sum[e].y));
+            }
+        }
+        lay_out<VEC>(held, sum, tx, ty, sp.chunk);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < s.cc; c += kThreads) {
+        float2 t = held[c];
+        for (int y = 1; y < sp.ty; ++y) {
+            const float2 h = held[y * sp.chunk + c];
+            t = make_float2(t.x + h.x, t.y + h.y);
+        }
+        if (a.part_dw) {
+            const int64_t at = (s.n * sp.slices + s.slice) * a.C + s.c0 + c;
+            a.part_db[at] = t.x;
+            a.part_dw[at] = t.y;
+        }
+        const float w = a.w ? a.w[s.c0 + c] : 1.f;
+        held[c] = make_float2(w * t.x, w * t.y);
+    }
+    __syncthreads();
+    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
+    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+        const int lo = max(g * a.W, s.c0) - s.c0, hi = min((g + 1) * a.W, s.c0 + s.cc) - s.c0;
+        float2 t = make_float2(0.f, 0.f);
+        for (int c = lo + lane; c < hi; c += 32)
+            t = make_float2(t.x + held[c].x, t.y + held[c].y);
+        t = group_sum(t, 32, nullptr);
+        if (lane == 0)
+            a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(t.x, t.y, 0.f, 0.f);
+    }
+}
+
+// Backward, second pass: dx.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, GroupNormSplit sp)
+{
+    extern __shared__ float2 stat[];
+    tc::grid_dep_wait();
+    const Slice s = slice_of(a, sp);
+    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
+    const float inv = 1.f / ((float)a.W * (float)a.S);
+    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+        const int k0 = g * a.W / sp.chunk, chunks = ((g + 1) * a.W - 1) / sp.chunk - k0 + 1;
+        float2 t = make_float2(0.f, 0.f);
+        for (int i = lane; i < sp.slices * chunks; i += 32) {
+            const int sl = i / chunks, k = k0 + i - sl * chunks;
+            const float4 p = a.part[(s.n * sp.slices + sl) * sp.entries + g + k];
+            t = make_float2(t.x + p.x, t.y + p.y);
+        }
+        t = group_sum(t, 32, nullptr);
+        if (lane == 0)
+            stat[g - g0] = make_float2(t.x * inv, t.y * inv);
+    }
+    __syncthreads();
+    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
+    if (ty >= sp.ty || tx * VEC >= s.cc)
+        return;
+    const bool silu = a.silu;
+    float mean[VEC], rstd[VEC], w[VEC], b[VEC];
+    float2 st[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int c = s.c0 + tx * VEC + e;
+        const int64_t g = s.n * a.G + c / a.W;
+        st[e] = stat[c / a.W - g0];
+        mean[e] = a.mean_in[g];
+        rstd[e] = a.rstd_in[g];
+        w[e] = a.w ? a.w[c] : 1.f;
+        b[e] = a.b ? a.b[c] : 0.f;
+    }
+    typedef Vec<T, VEC> V;
+    const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
+    const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
+    T *dx = static_cast<T *>(a.dx) + at;
+#pragma unroll 2
+    for (int64_t r = ty; r < s.rows; r += sp.ty) {
+        const V v = *reinterpret_cast<const V *>(x + r * a.C), d = *reinterpret_cast<const V *>(dy + r * a.C);
+        V o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float n = (widen(v.v[e]) - mean[e]) * rstd[e];
+            const float dz = before_act(widen(d.v[e]), fmaf(n, w[e], b[e]), silu);
+            o.v[e] = narrow<T>(rstd[e] * (fmaf(w[e], dz, -st[e].x) - n * st[e].y));
+        }
+        *reinterpret_cast<V *>(dx + r * a.C) = o;
+    }
+}
+
+// dw and db from their partial sums: `many` rows of C.
+__global__ void __launch_bounds__(kThreads) group_norm_dw_kernel(GroupNormArgs a, int64_t many)
+{
+    __shared__ float2 held[8][32];
+    tc::grid_dep_wait();
+    const int lane = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float2 t = make_float2(0.f, 0.f);
+    if (c < a.C)
+#pragma unroll 4
+        for (int64_t r = y; r < many; r += 8)
+            t = make_float2(t.x + a.part_dw[r * a.C + c], t.y + a.part_db[r * a.C + c]);
+    held[y][lane] = t;
+    __syncthreads();
+    if (y == 0 && c < a.C) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            t = make_float2(t.x + held[i][lane].x, t.y + held[i][lane].y);
+        if (a.dw) a.dw[c] = t.x;
+        if (a.db) a.db[c] = t.y;
+    }
+}
+
+// Vector width: whole 16-byte units where the groups of tokens (the rows of maps) are made of them.
+int vec_of(const GroupNormArgs &a, int dtype, bool tokens)
+{
+    const int vec = dtype == GLA_F32 ? 4 : 8;
+    return (tokens ? a.W : a.C) % vec ? 1 : vec;
+}
+
+// Lanes of a group and vectors of a lane of the tokens' kernel: as few vectors as 32 lanes allow, then more lanes.
+void lanes_of(int W, int vec, int &L, int &nv)
+{
+    const int vectors = (W + vec - 1) / vec, most = 16 / vec;
+    L = 1;
+    while (L < 32 && L < vectors)
+        L *= 2;
+    nv = 1;
+    while (nv < most && L * nv < vectors)
+        nv *= 2;
+    while (L * nv < vectors)
+        L *= 2;
+}
+
+}  // namespace
+
+bool group_norm_tokens(int64_t S, int W) { return S == 1 && W <= 4096; }
+
+int64_t group_norm_token_ctas(const GroupNormArgs &a, int dtype, bool back)
+{
+    int L, nv;
+    lanes_of(a.W, vec_of(a, dtype, true), L, nv);
+    const int64_t per = kThreads / L, q = a.G / std::gcd((int64_t)a.G, per), need = (a.N * a.G + per - 1) / per;
+    const int64_t cap = (int64_t)sm_count() * (back ? 3 : 6);
+    return std::max<int64_t>(1, std::min((need + q - 1) / q, std::max<int64_t>(cap / q, 1))) * q;
+}
+
+int64_t group_norm_token_parts(const GroupNormArgs &a, int dtype)   // rows of C of partial sums of dw
+{
+    int L, nv;
+    lanes_of(a.W, vec_of(a, dtype, true), L, nv);
+    return group_norm_token_ctas(a, dtype, true) * (kThreads / L) / a.G;
+}
+
+// Enough slices that the CTAs fill the GPU four times (two CTAs an SM at least stay busy to the end), as long as each has
+// four turns of rows.
+GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
+{
+    const int vec = vec_of(a, dtype, false), vectors = a.C / vec;
+    GroupNormSplit s;
+    s.chunk = std::min(vectors, kThreads) * vec;
+    s.chunks = (a.C + s.chunk - 1) / s.chunk;
+    s.tx = s.chunk / vec;
+    s.ty = kThreads / s.tx;
+    s.entries = a.G + s.chunks - 1;
+    const int64_t want = std::max<int64_t>(1, (4 * (int64_t)sm_count()) / std::max<int64_t>(1, a.N * s.chunks));
+    const int64_t most = std::max<int64_t>(1, a.S / (4 * s.ty));
+    const int64_t slices = std::min(want, most);
+    s.rows = (a.S + slices - 1) / slices;
+    s.slices = (int)((a.S + s.rows - 1) / s.rows);
+    return s;
+}
+
+namespace {
+
+template <typename F>
+cudaError_t by_norm_type(int dtype, int vec, F f)
+{
+    auto go = [&](auto t) {
+        typedef std::remove_pointer_t<decltype(t)> T;
+        return vec == 1 ? f(t, std::integral_constant<int, 1>()) : f(t, std::integral_constant<int, 16 / sizeof(T)>());
+    };
+    switch (dtype) {
+    case GLA_F32: return go((float *)0);
+    case GLA_BF16: return go((__nv_bfloat16 *)0);
+    case GLA_F16: return go((__half *)0);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+size_t stat_bytes(const GroupNormArgs &a, const GroupNormSplit &sp)
+{
+    return sizeof(float2) * std::min<int64_t>(a.G, (sp.chunk - 2) / a.W + 2 + 1);
+}
+
+}  // namespace
+
+cudaError_t launch_group_norm_tokens(const GroupNormArgs &a, int dtype, bool back, cudaStream_t s)
+{
+    const int vec = vec_of(a, dtype, true);
+    int L, nv;
+    lanes_of(a.W, vec, L, nv);
+    const unsigned grid = (unsigned)group_norm_token_ctas(a, dtype, back);
+    return by_norm_type(dtype, vec, [&](auto t, auto v) {
+        typedef std::remove_pointer_t<decltype(t)> T;
+        constexpr int VEC = decltype(v)::value;
+        auto go = [&](auto count) {
+            constexpr int NV = decltype(count)::value;
+            return back ? launch_early(tokens_kernel<T, VEC, NV, true>, grid, kThreads, s, a, L)
+                        : launch_early(tokens_kernel<T, VEC, NV, false>, grid, kThreads, s, a, L);
+        };
+        if (nv == 1) return go(std::integral_constant<int, 1>());
+        if (nv == 2) return go(std::integral_constant<int, 2>());
+        if constexpr (VEC <= 4)
+            if (nv == 4) return go(std::integral_constant<int, 4>());
+        if constexpr (VEC == 1) {
+            if (nv == 8) return go(std::integral_constant<int, 8>());
+            return go(std::integral_constant<int, 16>());
+        }
+        return cudaErrorInvalidValue;
+    });
+}
+
+cudaError_t launch_group_norm_maps(const GroupNormArgs &a, const GroupNormSplit &sp, int dtype, bool back, int pass, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(a.N * sp.slices * sp.chunks);
+    return by_norm_type(dtype, vec_of(a, dtype, false), [&](auto t, auto v) {
+        typedef std::remove_pointer_t<decltype(t)> T;
+        constexpr int VEC = decltype(v)::value;
+        if (pass == 0)
+            return back ? launch_early(maps_grad_sums_kernel<T, VEC>, grid, kThreads, s, a, sp)
+                        : launch_early(maps_sums_kernel<T, VEC>, grid, kThreads, s, a, sp);
+        return back ? launch_early_shared(maps_grad_kernel<T, VEC>, grid, kThreads, stat_bytes(a, sp), s, a, sp)
+                    : launch_early_shared(maps_apply_kernel<T, VEC>, grid, kThreads, stat_bytes(a, sp), s, a, sp);
+    });
+}
+
+cudaError_t launch_group_norm_dw(const GroupNormArgs &a, int64_t many, cudaStream_t s)
+{
+    return launch_early(group_norm_dw_kernel, (unsigned)((a.C + 31) / 32), kThreads, s, a, many);
+}
+
+}  // namespace gla

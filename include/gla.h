@@ -441,6 +441,112 @@ int gla_norm_bwd(const void *s, const float *rstd, const float *w, const void *d
 /* Bytes of device workspace gla_norm_bwd needs on the CURRENT device (0 for a D it would reject). */
 size_t gla_norm_bwd_workspace_size(int64_t rows, int D);
 
+/* ---------------------------------------------------------------------------------------------------------
+ * Gated delta rule (forward, backward, one token) and group norm with an activation.  The delta rule is the method
+ * whose WY step gla_wy_fwd computes (page "wy_fast.py"); its recurrence and the group norm that follows the heads (page
+ * "fla/ops/ttt/fused_chunk.py": norm_residual) have no kernel on the pages.  The conventions of the layer operators hold.
+ * `status` is a status word's memory: gla_scan_workspace_size() bytes on the device, 256-byte aligned and zeroed before
+ * first use, or gla_scan_shared_workspace(); read with gla_get_status().  `workspace` is scratch of one call at a time,
+ * 256-byte aligned; it needs no zeroing and nothing in it outlives the call.
+ * ------------------------------------------------------------------------------------------------------ */
+
+/*
+ * gla_delta_fwd — gated delta rule.  Per sequence n and value head hv, whose key head is h = hv / (HV / H),
+ *
+ *     S~ = exp(g_t) S_{t-1},   n_t = beta_t (v_t - k_t S~),   S_t = S~ + k_t^T n_t,   o_t = scale q_t S_t
+ *
+ *   q, k        [rows, H, K] device, input type;  v [rows, HV, V];  HV a multiple of H
+ *   g, beta     [rows, HV] fp32 whatever the input type: log-decay (usually <= 0; -inf clears the state) and write strength.
+ *               The state stays bounded for beta in [0, 2] and keys of length at most 1; neither is checked
+ *   o           [rows, HV, V] device, written
+ *   h0, ht      [N, HV, K, V] fp32 device or NULL; ht may equal h0.  A sequence of length zero has ht = h0 (or 0)
+ *   cu_seqlens  int32 [N + 1] device offsets (B == 1; T the packed rows) or NULL (N == B).  They must not decrease and
+ *               lie in [0, T]; rows outside all sequences are left as they were.  A pack with offsets that break this is
+ *               reported in the status word as GLA_ERR_INVALID_ARG, and its outputs are void
+ *   1 <= K, V <= 256;  scale finite and > 0;  B * T < 2^31 - 2^16
+ *   dtype       types of (q, k, v; o): GLA_F32 (f32, f32), GLA_BF16 (bf16, f32), GLA_BF16_OBF16 (bf16, bf16),
+ *               GLA_F16 (f16, f32), GLA_F16_OF16 (f16, f16)
+ *   workspace   gla_delta_fwd_workspace_size() bytes (may be NULL where that is 0)
+ *
+ * 16-bit inputs with K = 64 or 128 and V a multiple of 16 run in chunks of 64 tokens on the tensor cores, with every
+ * operand that is not an input in two 16-bit terms of bf16 (about 2^-16 of its size); everything else runs token by token
+ * in fp32.  States and sums are fp32.  The decays of a chunk are formed from differences of the running sum of its gates.
+ */
+int gla_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta, void *o, float scale,
+                  const float *h0, float *ht, const int32_t *cu_seqlens, int N, int B, int T, int H, int HV, int K, int V,
+                  int dtype, void *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gla_delta_fwd needs (0 also for arguments it would reject). */
+size_t gla_delta_fwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen);
+
+/*
+ * gla_delta_bwd — gradients of gla_delta_fwd for L = sum(o * dout) + sum(ht * dht); the forward's states are recomputed.
+ *
+ *   q .. cu_seqlens as for the forward;  dout [rows, HV, V] of the input type;  dht [N, HV, K, V] fp32 or NULL (zeros)
+ *   dq, dk [rows, H, K], dv [rows, HV, V] of the input type, written;  dg, dbeta [rows, HV] fp32, written
+ *   dh0         [N, HV, K, V] fp32 or NULL to skip it
+ *   dtype       GLA_F32, GLA_BF16 or GLA_F16: the type of q, k, v, dout, dq, dk, dv
+ * The gradients of a key head are summed over its value heads in a fixed order (no atomics).  Outputs must not overlap any
+ * input, the workspace or one another.
+ */
+int gla_delta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta, const void *dout,
+                  float scale, const float *h0, const float *dht, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                  float *dh0, const int32_t *cu_seqlens, int N, int B, int T, int H, int HV, int K, int V, int dtype,
+                  void *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gla_delta_bwd needs (0 for arguments it would reject). */
+size_t gla_delta_bwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen);
+
+/*
+ * gla_delta_step — one token of the gated delta rule for each of B sequences, with the states in a pool:
+ *
+ *     s = slots ? slots[b] : b,   S~ = exp(g_b) h0[s],   n = beta_b (v_b - k_b S~),   ht[s] = S~ + k_b^T n,   o_b = scale q_b ht[s]
+ *
+ *   q, k        [B, H, K],  v [B, HV, V] device, contiguous;  g, beta [B, HV] fp32;  o [B, HV, V] device, written
+ *   h0, ht      [S, HV, K, V] fp32 state pools; ht may equal h0 (update in place).  Only the addressed rows are written
+ *   slots       as for gla_scan_step (an idle sequence's o is zeros)
+ *   K, V, scale, dtype, status as for gla_delta_fwd
+ */
+int gla_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta, void *o, float scale,
+                   const float *h0, float *ht, const int32_t *slots, int B, int S, int H, int HV, int K, int V, int dtype,
+                   void *status, void *stream);
+
+/* Activations of the group norm. */
+#define GLA_ACT_NONE 0
+#define GLA_ACT_SILU 1
+
+/*
+ * gla_group_norm_fwd — group norm with an activation, channels last.  For sample n and group j, over the S positions and
+ * the C / G channels j C / G up to (j + 1) C / G:
+ *
+ *     mean, var,   rstd = 1 / sqrt(var + eps),   z = (x - mean) rstd w + b,   y = act(z),   silu(z) = z / (1 + exp(-z))
+ *
+ *   x, y        [N, S, C] device, fp32 / bf16 / fp16 by dtype (GLA_F32, GLA_BF16, GLA_F16); S = 1 for the heads of tokens
+ *   w, b        [C] fp32 or NULL (ones; zeros);   mean, rstd [N, G] fp32, written (the backward needs them)
+ *   C a multiple of G;  N >= 0, S >= 1;  eps finite and >= 0;  act GLA_ACT_NONE or GLA_ACT_SILU
+ *   workspace   gla_group_norm_workspace_size() bytes (may be NULL where that is 0)
+ * A NaN or an infinity makes its group NaN.  y must not overlap x.
+ */
+int gla_group_norm_fwd(const void *x, const float *w, const float *b, void *y, float *mean, float *rstd, int64_t N,
+                       int64_t S, int C, int G, float eps, int act, int dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * gla_group_norm_bwd — gradients of gla_group_norm_fwd: with xh = (x - mean) rstd, dz = dy act'(xh w + b), a = dz w,
+ *
+ *     dx = rstd (a - mean(a) - xh mean(a xh)),   dw = sum of dz xh,   db = sum of dz   (over samples and positions)
+ *
+ *   x, mean, rstd as the forward read and wrote them;  dy, dx [N, S, C] of x's type;  dw, db [C] fp32 or NULL to skip one
+ * Sums are added in a fixed order.  Outputs must not overlap any input, the workspace or one another.
+ */
+int gla_group_norm_bwd(const void *x, const float *mean, const float *rstd, const float *w, const float *b,
+                       const void *dy, void *dx, float *dw, float *db, int64_t N, int64_t S, int C, int G, int act,
+                       int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gla_group_norm_fwd (or, with backward, gla_group_norm_bwd) needs on the CURRENT device (0 also
+ * for arguments it would reject). */
+size_t gla_group_norm_workspace_size(int64_t N, int64_t S, int C, int G, int dtype, int backward);
+
 #ifdef __cplusplus
 }
 #endif
