@@ -71,7 +71,13 @@ using namespace gla;
 
 extern "C" size_t gla_delta_fwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen)
 {
-    return 0;
+    size_t x, o;
+    if (!delta_sizes(dtype, false, x, o) || check_shape(N, B, T, H, HV, K, V, varlen != 0) || !delta_chunked(dtype, K, V))
+        return 0;
+    DeltaArgs a;
+    std::memset(&a, 0, sizeof a);
+    plan(a, N, B, T, H, HV, K, V, varlen != 0);
+    return (size_t)a.slots * HV * delta_cell_bytes(false);
 }
 
 extern "C" size_t gla_delta_bwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen)
@@ -124,8 +130,16 @@ extern "C" int gla_delta_fwd(const void *q, const void *k, const void *v, const 
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.h0 = h0; a.ht = ht; a.cu = cu_seqlens; a.scale = scale;
     a.status = static_cast<int *>(status);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return profiled(K_DELTA_COLS, s, [&] { return launch_delta_cols(a, dtype, false, s); }) == cudaSuccess ? GLA_OK
-                                                                                                          : GLA_ERR_CUDA;
+    if (!delta_chunked(dtype, K, V))
+        return profiled(K_DELTA_COLS, s, [&] { return launch_delta_cols(a, dtype, false, s); }) == cudaSuccess
+                   ? GLA_OK : GLA_ERR_CUDA;
+    a.chunk = static_cast<char *>(workspace);
+    const bool half = dtype == GLA_F16 || dtype == GLA_F16_OF16;
+    if (a.slots && profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, false, s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, sm_count(), s); }) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    return GLA_OK;
 }
 
 extern "C" int gla_delta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

@@ -1,0 +1,104 @@
+// Pieces shared by the chunked kernels of the gated delta rule: the layout of a chunk's cell in the workspace, and warp
+// matrix instructions (m16n8k16 of 16-bit operands, fp32 sums) with their fragments.
+//
+// Fragments of a warp's product: lane l holds of a 16 x 8 result c[0..1] at row l / 4, columns 2 (l % 4) and + 1, and
+// c[2..3] eight rows further.  Two adjacent results are, rounded to 16 bits, the left operand (16 x 16) of a next product,
+// which is what lets the chain of a chunk's products stay in registers.
+#pragma once
+
+#include <type_traits>
+
+#include "delta_internal.h"
+#include "tc_ptx.cuh"
+
+namespace gla {
+
+// One (chunk, value head): per row (beta, e^G, e^(G_end - G), scale e^G), G the running sum of gates in the chunk, and the
+// lower triangles of two 64 x 64 matrices in fragments of right operands, 16 bytes a lane: two words of rounded values and
+// two of the remainders.  Result tile j (rows 8 j up) takes steps i (columns 16 i up) with 16 i <= 8 j + 7: 20 in all.
+constexpr int kTriangle = 20, kFragments = kTriangle * 32;
+struct DeltaCell {
+    float4 row[kDeltaChunk];
+    uint4 inverse[kFragments];   // T^ = (I + L diag(beta))^-1, L_ij = e^(G_i - G_j) k_i.k_j below the diagonal
+    uint4 score[kFragments];     // P_ij = scale e^(G_i - G_j) q_i.k_j up to the diagonal
+};
+struct DeltaCellBack : DeltaCell {   // and transposed: rows and columns of the tiles' numbers run from the other end
+    uint4 inverse_t[kFragments];     // T' = (I + L' diag(beta))^-1
+    uint4 score_t[kFragments];       // P'
+};
+__host__ __device__ constexpr int triangle_at(int j, int i) { return (j / 2) * (j / 2 + 1) + (j % 2) * (j / 2 + 1) + i; }
+__host__ __device__ constexpr int triangle_at_t(int j, int i) { return triangle_at(7 - j, 3 - i); }
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same_v<T, __half>)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four 8 x 8 matrices of 16-bit values from shared memory, lane l giving the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+// Two values as 16-bit ones and their remainders: bf16 keeps 2^-18 of the value, fp16 2^-22 (down to 2^-25 in all).
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = narrow2<T>(make_float2(x, y));
+    const float2 h = widen2<T>(hi);
+    lo = narrow2<T>(make_float2(x - h.x, y - h.y));
+}
+
+// A left operand's 16 columns from two adjacent results.
+template <typename T>
+__device__ __forceinline__ void split_pair(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4], uint32_t (&lo)[4])
+{
+    split2<T>(c0[0], c0[1], hi[0], lo[0]);
+    split2<T>(c0[2], c0[3], hi[1], lo[1]);
+    split2<T>(c1[0], c1[1], hi[2], lo[2]);
+    split2<T>(c1[2], c1[3], hi[3], lo[3]);
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// 64 rows of WIDTH 16-bit values, `pitch` apart in memory, to shared rows of WIDTH + 8 values (an odd number of 16-byte
+// units, so that eight rows' units lie in different banks); rows from `rows` on, and columns from `cols` on, are zeros.
+template <int WIDTH, int THREADS, typename T>
+__device__ __forceinline__ void copy_rows(uint32_t to, const T *from, size_t pitch, int rows, int cols)
+{
+    constexpr int kUnits = WIDTH / 8;
+    static_assert(64 * kUnits % THREADS == 0 || 64 * kUnits < THREADS, "whole turns");
+#pragma unroll
+    for (int i = 0; i < (64 * kUnits + THREADS - 1) / THREADS; ++i) {
+        const int e = i * THREADS + threadIdx.x, r = e / kUnits, u = e % kUnits;
+        if (64 * kUnits < THREADS && e >= 64 * kUnits)
+            break;
+        const bool on = r < rows && u * 8 < cols;
+        copy16(to + (r * (kUnits + 1) + u) * 16, from + (on ? r * pitch + u * 8 : 0), on);
+    }
+}
+
+template <int I>
+using Int = std::integral_constant<int, I>;
+
+}  // namespace gla
