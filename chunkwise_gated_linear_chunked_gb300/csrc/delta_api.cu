@@ -137,7 +137,7 @@ extern "C" int gla_delta_fwd(const void *q, const void *k, const void *v, const 
     const bool half = dtype == GLA_F16 || dtype == GLA_F16_OF16;
     if (a.slots && profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, false, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;
-    if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, sm_count(), s); }) != cudaSuccess)
+    if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;
     return GLA_OK;
 }

@@ -96,7 +96,7 @@ __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int &n
 inline bool delta_chunked(int dtype, int K, int V) { return dtype != GLA_F32 && (K == 64 || K == 128) && V % 16 == 0; }
 size_t delta_cell_bytes(bool backward);
 cudaError_t launch_delta_prep(const DeltaArgs &a, bool half, bool backward, cudaStream_t s);
-cudaError_t launch_delta_chain(const DeltaArgs &a, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_delta_chain(const DeltaArgs &a, int dtype, cudaStream_t s);
 
 cudaError_t launch_delta_cols(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);
 cudaError_t launch_delta_rows(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);

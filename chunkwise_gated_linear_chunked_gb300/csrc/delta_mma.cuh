@@ -90,7 +90,7 @@ __device__ __forceinline__ void copy_rows(uint32_t to, const T *from, size_t pit
     static_assert(64 * kUnits % THREADS == 0 || 64 * kUnits < THREADS, "whole turns");
 #pragma unroll
     for (int i = 0; i < (64 * kUnits + THREADS - 1) / THREADS; ++i) {
-        const int e = i * THREADS + threadIdx.x, r = e / kUnits, u = e % kUnits;
+        const int e = i * THREADS + threadIdx.x % THREADS, r = e / kUnits, u = e % kUnits;
         if (64 * kUnits < THREADS && e >= 64 * kUnits)
             break;
         const bool on = r < rows && u * 8 < cols;

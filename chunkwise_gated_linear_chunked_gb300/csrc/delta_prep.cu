@@ -3,10 +3,12 @@
 // head): k k^T and q k^T once for the value heads that share the key head.
 //
 // With L_ij = e^(G_i - G_j) k_i.k_j (j < i) and N the rows that update the state, N = beta Y and Y = R - L N for
-// R = V - e^G K S, so Y = (I + L diag(beta))^-1 R.  The inverse is I + W diag(beta), and the one that the gradients take,
-// (I + diag(beta) L)^-1, is I + diag(beta) W, with W_ij = -(L_ij + sum over j < m < i of L_im beta_m W_mj): found by
-// substitution, a lane a column, in two blocks of 32 side by side, then the block below them by two products.  A sum of
-// powers of L would need none of it and is not taken: for keys that look alike its terms grow like binomials.
+// R = V - e^G K S, so Y = (I + L diag(beta))^-1 R.  The inverse is T^ = I + W diag(beta), and the one that the gradients
+// take, (I + diag(beta) L)^-1, is T = I + diag(beta) W, with one W below the diagonal.  Warp w holds rows 16 w up.  Its block
+// on the diagonal is found by substitution in fp32, a lane a column (W_ij = -(L_ij + sum over j < m < i of L_im beta_m
+// W_mj)); what lies left of it by warp products, W_wp = -sum over p <= m < w of (T^_ww L_wm) T_mp, rows of blocks one after
+// the other.  A sum of powers of L would need no substitution and is not taken: for keys that look alike its terms grow
+// like binomials.  Products of two rounded matrices take three terms, so that blocks are within 2^-16 of their size.
 //
 // Differences of G decide the decays, and G may run far from zero, so it is summed in 64 bits and kept in two floats.
 // Gates count as at least -1000 (a decay of 0), which keeps differences of two cleared rows finite.
@@ -16,34 +18,78 @@ namespace gla {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kPitch = 68;   // floats of a row of L and W
 
-template <int KD>
+template <bool BACK>
 struct PrepShared {
-    uint16_t k[64][KD + 8], q[64][KD + 8];
-    float l[64][kPitch], w[64][kPitch], b[32][36];
+    uint16_t t_hi[64][72], t_lo[64][72];   // L, then T (16 bits and remainders), by blocks up to the diagonal
+    uint16_t d_hi[4][16][24], d_lo[4][16][24];   // T^ on the diagonal
+    float l[4][16][20];                    // L on the diagonal
     float g_hi[64], g_lo[64], beta[64];
+    uint16_t p_hi[BACK ? 64 : 1][72], p_lo[BACK ? 64 : 1][72];
+};
+template <int KD, bool BACK>
+union PrepMemory {
+    struct {
+        uint16_t k[64][KD + 8], q[64][KD + 8];
+    } rows;   // until the products are formed
+    PrepShared<BACK> s;
 };
 
-__device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j)
+// c += (a_hi + a_lo) (b_hi + b_lo) but for the remainders' product; two tiles, b as ldsm_t of the two planes gives it.
+template <typename T>
+__device__ __forceinline__ void mma3(float (&c)[2][4], const uint32_t (&a_hi)[4], const uint32_t (&a_lo)[4], const uint32_t (&b_hi)[4],
+                                     const uint32_t (&b_lo)[4])
 {
-    return exp2_fast((hi_i - hi_j) + (lo_i - lo_j));   // G is held times log2 e
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        mma<T>(c[y], a_hi, b_hi[2 * y], b_hi[2 * y + 1]);
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        mma<T>(c[y], a_lo, b_hi[2 * y], b_hi[2 * y + 1]);
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        mma<T>(c[y], a_hi, b_lo[2 * y], b_lo[2 * y + 1]);
+}
+
+// Words of a 16 x 16 block (two tiles of a result) to two planes of 16-bit values.
+template <int PITCH>
+__device__ __forceinline__ void put_block(uint16_t (*hi)[PITCH], uint16_t (*lo)[PITCH], int row, int col, const uint32_t (&h)[4], const uint32_t (&l)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {   // (rows, rows + 8) of the first tile, then of the second
+        *reinterpret_cast<uint32_t *>(&hi[row + (e & 1) * 8][col + (e >> 1) * 8]) = h[e];
+        *reinterpret_cast<uint32_t *>(&lo[row + (e & 1) * 8][col + (e >> 1) * 8]) = l[e];
+    }
 }
 
 template <typename T, int KD, bool BACK>
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaArgs a)
+__global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(DeltaArgs a)
 {
     typedef std::conditional_t<BACK, DeltaCellBack, DeltaCell> Cell;
     extern __shared__ __align__(16) char raw[];
-    PrepShared<KD> &sh = *reinterpret_cast<PrepShared<KD> *>(raw);
+    PrepMemory<KD, BACK> &mem = *reinterpret_cast<PrepMemory<KD, BACK> *>(raw);
+    PrepShared<BACK> &sh = mem.s;
     const int slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     int n, c, first, rows;
     if (!delta_chunk(a, slot, n, c, first, rows))
         return;
+    const int per = a.HV / a.H;
     const size_t key = ((size_t)first * a.H + h) * KD, pitch = (size_t)a.H * KD;
-    copy_rows<KD, kThreads>(tc::smem_u32(sh.k), static_cast<const T *>(a.k) + key, pitch, rows, KD);
-    copy_rows<KD, kThreads>(tc::smem_u32(sh.q), static_cast<const T *>(a.q) + key, pitch, rows, KD);
+    copy_rows<KD, kThreads>(tc::smem_u32(mem.rows.k), static_cast<const T *>(a.k) + key, pitch, rows, KD);
+    copy_rows<KD, kThreads>(tc::smem_u32(mem.rows.q), static_cast<const T *>(a.q) + key, pitch, rows, KD);
     copies_end();
+    float gate[2], strength[2];   // of two rows a lane of the first warp, one head ahead
+    auto ask = [&](int v) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            const bool on = warp == 0 && v < per && t < rows;
+            const size_t at = (size_t)(first + t) * a.HV + h * per + v;
+            gate[e] = on ? a.g[at] : 0.f;
+            strength[e] = on ? a.beta[at] : 0.f;
+        }
+    };
+    ask(0);
     copies_wait<0>();
     __syncthreads();
 
@@ -51,8 +97,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaArgs a)
     float kk[8][4] = {}, qk[8][4] = {};
     {
         const uint32_t row = (16 * warp + lane % 16) * (KD + 8) * 2 + (lane / 16) * 16;
-        const uint32_t ka = tc::smem_u32(sh.k) + row, qa = tc::smem_u32(sh.q) + row;
-        const uint32_t kb = tc::smem_u32(sh.k) + ((lane & 7) + (lane / 16) * 8) * (KD + 8) * 2 + ((lane / 8) & 1) * 16;
+        const uint32_t ka = tc::smem_u32(mem.rows.k) + row, qa = tc::smem_u32(mem.rows.q) + row;
+        const uint32_t kb = tc::smem_u32(mem.rows.k) + ((lane & 7) + (lane / 16) * 8) * (KD + 8) * 2 + ((lane / 8) & 1) * 16;
 #pragma unroll
         for (int s = 0; s < KD / 16; ++s) {
             uint32_t fk[4], fq[4];
@@ -72,22 +118,17 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaArgs a)
         }
     }
 
-    const int per = a.HV / a.H;
+    // a block of 16-bit values [rows][columns] as a right operand: rows are its steps (ldsm_t), or its columns (ldsm)
+    const int step_row = (lane & 7) + ((lane / 8) & 1) * 8, step_col = (lane / 16) * 8;
+    const int t0 = 16 * warp + lane / 4, two = 2 * (lane % 4);
     for (int v = 0; v < per; ++v) {
-        const int hv = h * per + v;
-        Cell &cell = reinterpret_cast<Cell *>(a.chunk)[(size_t)slot * a.HV + hv];
-        __syncthreads();   // the last head's sums are read
-        if (warp == 0) {   // two rows a lane
+        Cell &cell = reinterpret_cast<Cell *>(a.chunk)[(size_t)slot * a.HV + h * per + v];
+        __syncthreads();   // the rows' products (the last head's blocks) are read
+        if (warp == 0) {
             double g[2];
-            float bt[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const size_t at = (size_t)(first + t) * a.HV + hv;
-                const float gate = t < rows ? a.g[at] : 0.f;
-                bt[e] = t < rows ? a.beta[at] : 0.f;
-                g[e] = (gate < -1000.f ? -1000.0 : (double)gate) * 1.4426950408889634;
-            }
+            for (int e = 0; e < 2; ++e)
+                g[e] = (gate[e] < -1000.f ? -1000.0 : (double)gate[e]) * 1.4426950408889634;
             g[1] += g[0];
             double sum = g[1];
 #pragma unroll
@@ -103,138 +144,153 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaArgs a)
                 const double G = before + g[e];
                 sh.g_hi[t] = (float)G;
                 sh.g_lo[t] = (float)(G - (double)(float)G);
-                sh.beta[t] = bt[e];
+                sh.beta[t] = strength[e];
                 const float start = exp2_fast((float)G);
-                cell.row[t] = make_float4(bt[e], start, exp2_fast((float)(end - G)), a.scale * start);
+                cell.row[t] = make_float4(strength[e], start, exp2_fast((float)(end - G)), a.scale * start);
             }
         }
+        ask(v + 1);
         __syncthreads();
-        // L to shared memory, P to the cell: a result's rows are a right operand's columns, so P goes as it lies
+        // decays of this lane's rows t0 and t0 + 8 times k k^T and q k^T: P goes to the cell as it lies (a result's rows
+        // are a right operand's columns), L to shared memory
+        const float hi0 = sh.g_hi[t0], lo0 = sh.g_lo[t0], hi1 = sh.g_hi[t0 + 8], lo1 = sh.g_lo[t0 + 8];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = 16 * warp + lane / 4 + 8 * half;
-            const float hi = sh.g_hi[i], lo = sh.g_lo[i];
+        for (int p = 0; p < 4; ++p) {
+            if (p > warp)
+                break;
+            float l[2][4], s[2][4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                uint32_t word[4];
-                float pv[4];
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int tile = 0; tile < 2; ++tile)
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 16 * p + 8 * y + two + e;
+                    const float hj = sh.g_hi[j], lj = sh.g_lo[j];
+                    const float d0 = j <= t0 ? exp2_fast((hi0 - hj) + (lo0 - lj)) : 0.f;
+                    const float d1 = j <= t0 + 8 ? exp2_fast((hi1 - hj) + (lo1 - lj)) : 0.f;
+                    s[y][e] = j <= t0 ? a.scale * (d0 * qk[2 * p + y][e]) : 0.f;
+                    s[y][2 + e] = j <= t0 + 8 ? a.scale * (d1 * qk[2 * p + y][2 + e]) : 0.f;
+                    l[y][e] = j < t0 ? d0 * kk[2 * p + y][e] : 0.f;
+                    l[y][2 + e] = j < t0 + 8 ? d1 * kk[2 * p + y][2 + e] : 0.f;
+                }
+            uint32_t hi[4], lo[4];
+            split_pair<T>(s[0], s[1], hi, lo);   // rows t0 and t0 + 8 of the first tile, then of the second
+            cell.score[triangle_at(2 * warp, p) * 32 + lane] = make_uint4(hi[0], hi[2], lo[0], lo[2]);
+            cell.score[triangle_at(2 * warp + 1, p) * 32 + lane] = make_uint4(hi[1], hi[3], lo[1], lo[3]);
+            if constexpr (BACK)
+                put_block<72>(sh.p_hi, sh.p_lo, t0, 16 * p + two, hi, lo);
+            if (p < warp) {
+                split_pair<T>(l[0], l[1], hi, lo);
+                put_block<72>(sh.t_hi, sh.t_lo, t0, 16 * p + two, hi, lo);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 16 * p + 8 * tile + 2 * (lane % 4) + e;
-                        const float d = j <= i ? decay_between(hi, lo, sh.g_hi[j], sh.g_lo[j]) : 0.f;
-                        sh.l[i][j] = j < i ? d * kk[2 * p + tile][2 * half + e] : 0.f;
-                        pv[2 * tile + e] = j <= i ? a.scale * d * qk[2 * p + tile][2 * half + e] : 0.f;
-                        if constexpr (BACK)
-                            sh.w[i][j] = pv[2 * tile + e];   // for its transpose, before W lies there
-                    }
-                if (p > warp)
-                    continue;
-                split2<T>(pv[0], pv[1], word[0], word[2]);
-                split2<T>(pv[2], pv[3], word[1], word[3]);
-                cell.score[triangle_at(2 * warp + half, p) * 32 + lane] = make_uint4(word[0], word[1], word[2], word[3]);
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sh.l[warp][lane / 4 + (e >> 1) * 8][8 * y + two + (e & 1)] = l[y][e];
             }
         }
-        __syncthreads();
-        // fragments of a transposed matrix: tile j, step i, entry (column 8 j + lane / 4, row 16 i + 2 (lane % 4) ..)
-        auto store_t = [&](uint4 *to, auto value) {
-            for (int f = warp; f < kTriangle; f += kThreads / 32) {
-                int j = 7, i = 3;
-                while (triangle_at_t(j, i) != f)   // tiles from the last, steps from the last
-                    if (--i < j / 2)
-                        --j, i = 3;
-                const int t = 8 * j + lane / 4, r = 16 * i + 2 * (lane % 4);
-                uint32_t word[4];
-                split2<T>(value(r, t), value(r + 1, t), word[0], word[2]);
-                split2<T>(value(r + 8, t), value(r + 9, t), word[1], word[3]);
-                to[f * 32 + lane] = make_uint4(word[0], word[1], word[2], word[3]);
-            }
-        };
-        if constexpr (BACK) {
-            store_t(static_cast<DeltaCellBack &>(cell).score_t, [&](int r, int t) { return sh.w[r][t]; });
-            __syncthreads();
-        }
-        // W: the blocks on the diagonal, a warp each, a lane a column
-        if (warp < 2) {
-            const int o = 32 * warp;
-            float w[32];   // beta W of the rows so far, 1 on the diagonal
+        __syncwarp();
+        {   // the block on the diagonal; both halves of the warp find it, one stores T^, the other T
+            const int x = lane % 16;
+            const float bx = sh.beta[16 * warp + x];
+            float w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int m = 0; m < i; m += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sh.l[o + i][o + m]);
-                    s0 = fmaf(x.x, w[m], s0);
-                    if (m + 1 < i) s1 = fmaf(x.y, w[m + 1], s1);
-                    if (m + 2 < i) s0 = fmaf(x.z, w[m + 2], s0);
-                    if (m + 3 < i) s1 = fmaf(x.w, w[m + 3], s1);
+                    const float4 l = *reinterpret_cast<const float4 *>(&sh.l[warp][i][m]);
+                    s0 = fmaf(l.x, w[m], s0);
+                    if (m + 1 < i) s1 = fmaf(l.y, w[m + 1], s1);
+                    if (m + 2 < i) s0 = fmaf(l.z, w[m + 2], s0);
+                    if (m + 3 < i) s1 = fmaf(l.w, w[m + 3], s1);
                 }
                 const float value = -(s0 + s1);
-                sh.w[o + i][o + lane] = i > lane ? value : 0.f;
-                w[i] = i == lane ? 1.f : i > lane ? sh.beta[o + i] * value : 0.f;
+                w[i] = i == x ? 1.f : i > x ? sh.beta[16 * warp + i] * value : 0.f;
+                const float out = lane < 16 && i > x ? bx * value : w[i];
+                uint32_t hi, lo;
+                split2<T>(out, 0.f, hi, lo);
+                if (lane < 16)
+                    sh.d_hi[warp][i][x] = (uint16_t)hi, sh.d_lo[warp][i][x] = (uint16_t)lo;
+                else
+                    sh.t_hi[16 * warp + i][16 * warp + x] = (uint16_t)hi, sh.t_lo[16 * warp + i][16 * warp + x] = (uint16_t)lo;
             }
         }
-        __syncthreads();
-        // below them: B = L21 (beta W + I)11, W21 = -(W diag(beta) + I)22 B; four adjacent columns of two rows a thread
+        __syncwarp();
+        uint32_t m_hi[3][4], m_lo[3][4];   // -T^ L of this row of blocks
         {
-            const int r = tid / 8 * 2, x = tid % 8 * 4;
-            float acc[2][4] = {};
-#pragma unroll 4
-            for (int m = 0; m < 32; ++m) {
-                const float4 w = *reinterpret_cast<const float4 *>(&sh.w[m][x]);
-                const float f = sh.beta[m];
-                const float u[4] = {m == x ? 1.f : f * w.x, m == x + 1 ? 1.f : f * w.y, m == x + 2 ? 1.f : f * w.z,
-                                    m == x + 3 ? 1.f : f * w.w};
+            uint32_t d_hi[4], d_lo[4], f_hi[4], f_lo[4];
+            ldsm(d_hi, tc::smem_u32(&sh.d_hi[warp][lane % 16][(lane / 16) * 8]));
+            ldsm(d_lo, tc::smem_u32(&sh.d_lo[warp][lane % 16][(lane / 16) * 8]));
+            // as a right operand its rows are the columns: words 0, 2 hold rows up to 8, words 1, 3 the others
+            cell.inverse[triangle_at(2 * warp, warp) * 32 + lane] = make_uint4(d_hi[0], d_hi[2], d_lo[0], d_lo[2]);
+            cell.inverse[triangle_at(2 * warp + 1, warp) * 32 + lane] = make_uint4(d_hi[1], d_hi[3], d_lo[1], d_lo[3]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float l = sh.l[32 + r + e][m];
+            for (int p = 0; p < 3; ++p) {
+                if (p >= warp)
+                    break;
+                float f[2][4] = {};
+                ldsm_t(f_hi, tc::smem_u32(&sh.t_hi[16 * warp + step_row][16 * p + step_col]));
+                ldsm_t(f_lo, tc::smem_u32(&sh.t_lo[16 * warp + step_row][16 * p + step_col]));
+                mma3<T>(f, d_hi, d_lo, f_hi, f_lo);
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        acc[e][d] = fmaf(l, u[d], acc[e][d]);
-                }
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[y][e] = -f[y][e];
+                split_pair<T>(f[0], f[1], m_hi[p], m_lo[p]);
             }
+        }
+        const float b0 = sh.beta[t0], b1 = sh.beta[t0 + 8];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float4 *>(&sh.b[r + e][x]) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+        for (int w = 1; w < 4; ++w) {
+            __syncthreads();   // the rows of blocks before this one are there
+            if (warp != w)
+                continue;
+#pragma unroll
+            for (int p = 0; p < w; ++p) {
+                float f[2][4] = {};
+#pragma unroll
+                for (int m = p; m < w; ++m) {
+                    uint32_t f_hi[4], f_lo[4];
+                    ldsm_t(f_hi, tc::smem_u32(&sh.t_hi[16 * m + step_row][16 * p + step_col]));
+                    ldsm_t(f_lo, tc::smem_u32(&sh.t_lo[16 * m + step_row][16 * p + step_col]));
+                    mma3<T>(f, m_hi[m], m_lo[m], f_hi, f_lo);
+                }
+                uint32_t hi[4], lo[4];
+                float t[2][4], i[2][4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        t[y][e] = (e < 2 ? b0 : b1) * f[y][e];
+                        i[y][e] = sh.beta[16 * p + 8 * y + two + (e & 1)] * f[y][e];
+                    }
+                split_pair<T>(t[0], t[1], hi, lo);
+                put_block<72>(sh.t_hi, sh.t_lo, t0, 16 * p + two, hi, lo);
+                split_pair<T>(i[0], i[1], hi, lo);
+                cell.inverse[triangle_at(2 * w, p) * 32 + lane] = make_uint4(hi[0], hi[2], lo[0], lo[2]);
+                cell.inverse[triangle_at(2 * w + 1, p) * 32 + lane] = make_uint4(hi[1], hi[3], lo[1], lo[3]);
+            }
+        }
+        if constexpr (BACK) {   // T' and P': blocks (step i, column tiles 2 p and 2 p + 1), i >= p
             __syncthreads();
+            DeltaCellBack &back = static_cast<DeltaCellBack &>(cell);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float4 b = *reinterpret_cast<const float4 *>(&sh.b[r + e][x]);
-                acc[e][0] = b.x, acc[e][1] = b.y, acc[e][2] = b.z, acc[e][3] = b.w;
+            for (int i = 0; i < 4; ++i) {
+                if (i < warp)
+                    continue;
+                uint32_t hi[4], lo[4];
+                ldsm_t(hi, tc::smem_u32(&sh.t_hi[16 * i + step_row][16 * warp + step_col]));
+                ldsm_t(lo, tc::smem_u32(&sh.t_lo[16 * i + step_row][16 * warp + step_col]));
+                back.inverse_t[triangle_at_t(2 * warp, i) * 32 + lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                back.inverse_t[triangle_at_t(2 * warp + 1, i) * 32 + lane] = make_uint4(hi[2], hi[3], lo[2], lo[3]);
+                ldsm_t(hi, tc::smem_u32(&sh.p_hi[16 * i + step_row][16 * warp + step_col]));
+                ldsm_t(lo, tc::smem_u32(&sh.p_lo[16 * i + step_row][16 * warp + step_col]));
+                back.score_t[triangle_at_t(2 * warp, i) * 32 + lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                back.score_t[triangle_at_t(2 * warp + 1, i) * 32 + lane] = make_uint4(hi[2], hi[3], lo[2], lo[3]);
             }
-#pragma unroll 4
-            for (int m = 0; m < 32; ++m) {
-                const float4 b = *reinterpret_cast<const float4 *>(&sh.b[m][x]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = sh.w[32 + r + e][32 + m] * sh.beta[32 + m];   // 0 from the diagonal on
-                    acc[e][0] = fmaf(f, b.x, acc[e][0]);
-                    acc[e][1] = fmaf(f, b.y, acc[e][1]);
-                    acc[e][2] = fmaf(f, b.z, acc[e][2]);
-                    acc[e][3] = fmaf(f, b.w, acc[e][3]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float4 *>(&sh.w[32 + r + e][x]) = make_float4(-acc[e][0], -acc[e][1], -acc[e][2], -acc[e][3]);
         }
-        __syncthreads();
-        for (int f = warp; f < kTriangle; f += kThreads / 32) {
-            int j = 0, i = 0;
-            while (triangle_at(j, i) != f)
-                if (++i > j / 2)
-                    ++j, i = 0;
-            const int t = 8 * j + lane / 4, s = 16 * i + 2 * (lane % 4);
-            auto value = [&](int u) { return u == t ? 1.f : u < t ? sh.w[t][u] * sh.beta[u] : 0.f; };
-            uint32_t word[4];
-            split2<T>(value(s), value(s + 1), word[0], word[2]);
-            split2<T>(value(s + 8), value(s + 9), word[1], word[3]);
-            cell.inverse[f * 32 + lane] = make_uint4(word[0], word[1], word[2], word[3]);
-        }
-        if constexpr (BACK)
-            store_t(static_cast<DeltaCellBack &>(cell).inverse_t,
-                    [&](int r, int t) { return r == t ? 1.f : r > t ? sh.beta[r] * sh.w[r][t] : 0.f; });
     }
 }
 
@@ -254,7 +310,8 @@ cudaError_t launch_delta_prep(const DeltaArgs &a, bool half, bool backward, cuda
     auto by_back = [&](auto t, auto kd) {
         typedef std::remove_pointer_t<decltype(t)> T;
         constexpr int KD = decltype(kd)::value;
-        return backward ? go(delta_prep_kernel<T, KD, true>, sizeof(PrepShared<KD>)) : go(delta_prep_kernel<T, KD, false>, sizeof(PrepShared<KD>));
+        return backward ? go(delta_prep_kernel<T, KD, true>, sizeof(PrepMemory<KD, true>))
+                        : go(delta_prep_kernel<T, KD, false>, sizeof(PrepMemory<KD, false>));
     };
     auto by_type = [&](auto kd) { return half ? by_back((__half *)0, kd) : by_back((__nv_bfloat16 *)0, kd); };
     return a.K == 128 ? by_type(Int<128>()) : by_type(Int<64>());
