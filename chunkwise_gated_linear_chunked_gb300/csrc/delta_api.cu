@@ -49,10 +49,28 @@ void place(E *&p, char *base, size_t &at, size_t count)
     at += align_up(count * sizeof(E));
 }
 
-// The backward's workspace where it runs token by token.
-size_t place_bwd(DeltaArgs &a, char *base)
+// The backward's workspace.
+size_t place_bwd(DeltaArgs &a, int dtype, char *base)
 {
     size_t at = 0;
+    if (delta_chunked(dtype, a.K, a.V)) {
+        const size_t cells = (size_t)a.slots * a.HV, columns = a.V / 16;
+        constexpr int kRows = kDeltaChunk * kDeltaKept;
+        const size_t kept = (size_t)(a.cu ? a.T / kRows + a.N : a.B * ((a.T + kRows - 1) / kRows)) * a.HV * columns;
+        DeltaTrace &t = a.trace;
+        t.s_size = (size_t)a.V * a.K / 2;
+        t.n_size = (size_t)a.V * kDeltaChunk / 2;
+        place(a.chunk, base, at, cells * delta_cell_bytes(true));
+        place(t.s, base, at, cells * t.s_size);
+        place(t.ds, base, at, cells * t.s_size);
+        place(t.n, base, at, cells * t.n_size);
+        place(t.x, base, at, cells * t.n_size);
+        place(t.y, base, at, cells * columns * 256);
+        place(t.dots, base, at, cells * columns * 3 * kDeltaChunk);
+        place(t.kept, base, at, kept * (a.K / 8) * 32);
+        place(t.across, base, at, kept);
+        return at;
+    }
     const size_t heads = (size_t)a.rows * a.HV;
     place(a.upd, base, at, heads * a.V);
     place(a.dx, base, at, heads * a.V);
@@ -88,7 +106,9 @@ extern "C" size_t gla_delta_bwd_workspace_size(int N, int B, int T, int H, int H
     DeltaArgs a;
     std::memset(&a, 0, sizeof a);
     plan(a, N, B, T, H, HV, K, V, varlen != 0);
-    return place_bwd(a, nullptr);
+    static const int32_t offsets = 0;
+    a.cu = varlen ? &offsets : nullptr;   // only whether there are any
+    return place_bwd(a, dtype, nullptr);
 }
 
 extern "C" int gla_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta, void *o,
@@ -137,7 +157,7 @@ extern "C" int gla_delta_fwd(const void *q, const void *k, const void *v, const 
     const bool half = dtype == GLA_F16 || dtype == GLA_F16_OF16;
     if (a.slots && profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, false, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;
-    if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, s); }) != cudaSuccess)
+    if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, false, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;
     return GLA_OK;
 }
@@ -183,10 +203,22 @@ extern "C" int gla_delta_bwd(const void *q, const void *k, const void *v, const 
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.dout = dout; a.h0 = h0; a.dht = dht; a.cu = cu_seqlens;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0; a.scale = scale;
     a.status = static_cast<int *>(status);
-    place_bwd(a, static_cast<char *>(workspace));
+    place_bwd(a, dtype, static_cast<char *>(workspace));
     if (!dht)
         a.hd = nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (delta_chunked(dtype, K, V)) {
+        const bool half = dtype == GLA_F16;
+        if (a.slots && (profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, true, s); }) != cudaSuccess ||
+                        profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, true, s); }) != cudaSuccess))
+            return GLA_ERR_CUDA;
+        if (profiled(K_DELTA_CHAIN_BACK, s, [&] { return launch_delta_chain_back(a, half, s); }) != cudaSuccess)
+            return GLA_ERR_CUDA;
+        if (rows && (profiled(K_DELTA_GRADS, s, [&] { return launch_delta_grads(a, half, sm_count(), s); }) != cudaSuccess ||
+                     profiled(K_DELTA_GATES, s, [&] { return launch_delta_chunk_gates(a, s); }) != cudaSuccess))
+            return GLA_ERR_CUDA;
+        return GLA_OK;
+    }
     if (profiled(K_DELTA_COLS, s, [&] { return launch_delta_cols(a, dtype, false, s); }) != cudaSuccess ||
         profiled(K_DELTA_COLS_BACK, s, [&] { return launch_delta_cols(a, dtype, true, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;

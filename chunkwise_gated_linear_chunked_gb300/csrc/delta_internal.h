@@ -8,6 +8,17 @@
 
 namespace gla {
 
+// What the chunked forward leaves for the gradients, and the reverse pass for them; a cell is a (slot, value head).
+struct DeltaTrace {
+    uint32_t *s, *ds, *n, *x;          // cells of s_size (s, ds) or n_size (n, x) words: S' at the chunk's start and its
+                                       // gradient at the end, N' and the gradient of N, in blocks of 8 x 8 rounded values
+    float4 *y;                         // [cell][V / 16][8][32] Y as a warp's results have it
+    float *dots;                       // [cell][V / 16][3][64] o.dO, x.Y and dv.v over 16 columns
+    float4 *kept;                      // [kept group][HV][V / 16][K / 8][32] states at the ends of groups of chunks
+    float *across;                     // [kept group][HV][V / 16] their products with their gradients
+    size_t s_size, n_size;
+};
+
 // Forward and backward (passed by value).  Rows are tokens of all sequences; key head of value head hv: hv / (HV / H).
 struct DeltaArgs {
     const void *q, *k, *v, *dout;      // [rows, H, K], [rows, H, K], [rows, HV, V], [rows, HV, V]
@@ -27,7 +38,8 @@ struct DeltaArgs {
     float *dG;                         // [rows, HV]: gradient of the running sum of gates
     float *hd;                         // [N, HV, K]: rows of <ht, dht>
     // workspace of the chunked kernels
-    char *chunk;
+    char *chunk;                       // cells (DeltaCell, or DeltaCellBack)
+    DeltaTrace trace;
 };
 
 // One token (passed by value).
@@ -43,6 +55,7 @@ struct DeltaStepArgs {
 };
 
 constexpr int kDeltaChunk = 64;        // rows of a chunk
+constexpr int kDeltaKept = 8;          // chunks between two states that are kept in fp32
 
 // Rows of sequence n, [bos, bos + len).  False for offsets outside [0, T] or decreasing.
 __device__ __forceinline__ bool delta_sequence(const DeltaArgs &a, int n, int &bos, int &len)
@@ -62,6 +75,17 @@ __device__ __forceinline__ bool delta_sequence(const DeltaArgs &a, int n, int &b
 __device__ __forceinline__ int delta_first_slot(const DeltaArgs &a, int n)
 {
     return a.cu ? a.cu[n] / kDeltaChunk + n : n * ((a.T + kDeltaChunk - 1) / kDeltaChunk);
+}
+
+// Groups of kDeltaKept chunks, numbered likewise; the place of a group's state at the end of chunk c.
+__device__ __forceinline__ int delta_first_group(const DeltaArgs &a, int n)
+{
+    constexpr int kRows = kDeltaChunk * kDeltaKept;
+    return a.cu ? a.cu[n] / kRows + n : n * ((a.T + kRows - 1) / kRows);
+}
+__device__ __forceinline__ size_t delta_kept_at(const DeltaArgs &a, int n, int c, int hv, int g16)
+{
+    return ((size_t)(delta_first_group(a, n) + c / kDeltaKept) * a.HV + hv) * (a.V / 16) + g16;
 }
 
 // The chunk of a slot: its sequence, its number in it, its first row and its rows.  False for a slot without rows.
@@ -96,7 +120,10 @@ __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int &n
 inline bool delta_chunked(int dtype, int K, int V) { return dtype != GLA_F32 && (K == 64 || K == 128) && V % 16 == 0; }
 size_t delta_cell_bytes(bool backward);
 cudaError_t launch_delta_prep(const DeltaArgs &a, bool half, bool backward, cudaStream_t s);
-cudaError_t launch_delta_chain(const DeltaArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_delta_chain(const DeltaArgs &a, int dtype, bool save, cudaStream_t s);
+cudaError_t launch_delta_chain_back(const DeltaArgs &a, bool half, cudaStream_t s);
+cudaError_t launch_delta_grads(const DeltaArgs &a, bool half, int sms, cudaStream_t s);
+cudaError_t launch_delta_chunk_gates(const DeltaArgs &a, cudaStream_t s);
 
 cudaError_t launch_delta_cols(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);
 cudaError_t launch_delta_rows(const DeltaArgs &a, int dtype, bool backward, cudaStream_t s);

@@ -25,6 +25,7 @@ struct DeltaCell {
 struct DeltaCellBack : DeltaCell {   // and transposed: rows and columns of the tiles' numbers run from the other end
     uint4 inverse_t[kFragments];     // T' = (I + L' diag(beta))^-1
     uint4 score_t[kFragments];       // P'
+    float2 gate[kDeltaChunk];        // G times log2 e in two floats
 };
 __host__ __device__ constexpr int triangle_at(int j, int i) { return (j / 2) * (j / 2 + 1) + (j % 2) * (j / 2 + 1) + i; }
 __host__ __device__ constexpr int triangle_at_t(int j, int i) { return triangle_at(7 - j, 3 - i); }
@@ -42,16 +43,17 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four 8 x 8 matrices of 16-bit values from shared memory, lane l giving the address of row l % 8 of matrix l / 8.
+// Four 8 x 8 matrices of 16-bit values from shared memory, lane l giving the address of row l % 8 of matrix l / 8.  In
+// order with barriers (volatile), but other loads and stores may pass it: what it reads is written before a barrier.
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 
 // Two values as 16-bit ones and their remainders: bf16 keeps 2^-18 of the value, fp16 2^-22 (down to 2^-25 in all).

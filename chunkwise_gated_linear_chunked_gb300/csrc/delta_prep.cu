@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
                 sh.beta[t] = strength[e];
                 const float start = exp2_fast((float)G);
                 cell.row[t] = make_float4(strength[e], start, exp2_fast((float)(end - G)), a.scale * start);
+                if constexpr (BACK)
+                    cell.gate[t] = make_float2(sh.g_hi[t], sh.g_lo[t]);
             }
         }
         ask(v + 1);

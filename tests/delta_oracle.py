@@ -6,10 +6,13 @@ a column of the state, so that errors made at different tokens add up at most.
 
   * token by token in fp32 (u = 2^-24): a token's dot products over K (or V) values are within (K + 16) u of the column's
     length, the roundings of different tokens are independent: (D + 16) u sqrt(T) with D the longer of K and V.
-  * in chunks of 64 on the tensor cores: an operand in two bf16 terms is within 2^-18 of its value, a product of two such
-    drops 2^-18 more (3 2^-18 in all).  k S (1), its product with the inverse (3), the state's update (1) and the output's
-    product (3) make 2^-15 a chunk; chunks add up: 2^-15 (1 + chunks).  The backward reads forward's rows and states and
-    walks the same chain once more, so that its products hold twice that.
+  * in chunks of 64 on the tensor cores: an operand in two bf16 terms is within 2^-16 of its value at worst and 2^-18 in
+    the mean square (a rounding's error is spread over its half step, and a value over the steps of its binade: 2^-9 each),
+    and a sum of 64 and more such errors of random sign is as large as their mean square has it.  A product of two such
+    operands drops as much again (3 2^-18 in all).  k S (1), its product with the inverse (3), the state's update (1) and
+    the output's product (3) make 2^-15 a chunk; chunks add up: 2^-15 (1 + chunks).  The backward reads forward's rows and
+    states and walks the same chain once more, so that its products hold twice that.
+    dq and dk come from operands in one 16-bit term each: ``grad_sizes``.
 
 Both are relative to the largest value of the head (over its tokens, or of its state).  Sums over two such values
 (gradients of gates and strengths) are relative to the product of the lengths.
@@ -60,8 +63,9 @@ def delta_fwd(q, k, v, g, beta, scale, h0=None, cu=None, keep=False):
     return (o, ht, states) if keep else (o, ht)
 
 
-def delta_bwd(q, k, v, g, beta, do, scale, h0=None, dht=None, cu=None):
-    """-> dq, dk, dv, dg, dbeta, dh0 (zeros in rows outside all sequences)."""
+def delta_bwd(q, k, v, g, beta, do, scale, h0=None, dht=None, cu=None, keep=None):
+    """-> dq, dk, dv, dg, dbeta, dh0 (zeros in rows outside all sequences).  ``keep``: a dict that gets each row's gradient of
+    its update row, and of the state behind it."""
     B, T, H, K = q.shape
     HV, V = v.shape[2:]
     _, _, states = delta_fwd(q, k, v, g, beta, scale, h0, cu, keep=True)
@@ -73,10 +77,13 @@ def delta_bwd(q, k, v, g, beta, do, scale, h0=None, dht=None, cu=None):
         dS = np.zeros((HV, K, V)) if dht is None else dht[n].copy()
         for r in range(hi - 1, lo - 1, -1):
             old, row, S = states[r]
+            behind = dS
             dq[r] = scale * np.einsum("hkv,hv->hk", S, fo[r])
             dS = dS + scale * _outer(fq[r], fo[r])
             x = np.einsum("hk,hkv->hv", fk[r], dS)
             back = fb[r][:, None] * x
+            if keep is not None:
+                keep[r] = (old, row, x, behind)
             dv[r] = back
             db[r] = (x * (fv[r] - np.einsum("hk,hkv->hv", fk[r], old))).sum(-1)
             dk[r] = np.einsum("hkv,hv->hk", dS, row) - np.einsum("hkv,hv->hk", old, back)
@@ -86,6 +93,38 @@ def delta_bwd(q, k, v, g, beta, do, scale, h0=None, dht=None, cu=None):
         dh0[n] = dS
     shared = lambda t: t.reshape(B, T, H, HV // H, K).sum(3)   # noqa: E731
     return shared(dq), shared(dk), dv.reshape(v.shape), dg.reshape(g.shape), db.reshape(g.shape), dh0
+
+
+def grad_sizes(q, k, g, beta, do, scale, B, T, cu, keep):
+    """What the terms of the chunked dq and dk add up to in magnitude, [B, T, H, K] each, from what ``delta_bwd`` kept.
+
+    In a chunk, with G the running sum of gates and D_ij = exp(G_i - G_j),
+        dq_i = scale exp(G_i) S do_i + sum over j <= i of p_ij k_j,                     p_ij = scale D_ij do_i.N_j
+        dk_i = -beta_i exp(G_i) S x_i + exp(G_end - G_i) dS' N_i + sum over j of (p_ji q_j + (b_ij + b_ji) k_j),
+                                                                                          b_ij = -beta_i D_ij x_i.N_j (j < i)
+    Where S, dS', N, x, and then p and b are rounded to 16 bits, a term is off by at most three roundings: two of its
+    factors, and p's (b's) own."""
+    H, HV = q.shape[2], beta.shape[2]
+    fq, fk, fg, fb, fo = _flat(*(np.repeat(np.abs(t), HV // H, 2) for t in (q, k)), g, beta, np.abs(do))
+    aq, ak = np.zeros_like(fq), np.zeros_like(fk)
+    for lo, hi in sequences(B, T, cu):
+        for c in range(lo, hi, 64):
+            rows = slice(c, min(c + 64, hi))
+            G = np.cumsum(np.maximum(fg[rows], -1000), 0).T                                   # [HV, n]
+            D = np.exp(np.minimum(G[:, :, None] - G[:, None, :], 0 if (fg <= 0).all() else np.inf)) * np.tril(np.ones((G.shape[1],) * 2))
+            first, last = keep[rows.start], keep[rows.stop - 1]
+            S = np.abs(first[0])                                                              # the state after the first row's gate
+            dS, n = np.abs(last[3]), np.stack([np.abs(keep[r][1]) for r in range(c, rows.stop)], 1)
+            x, d = np.stack([np.abs(keep[r][2]) for r in range(c, rows.stop)], 1), fo[rows].transpose(1, 0, 2)
+            kk, qq, b = fk[rows].transpose(1, 0, 2), fq[rows].transpose(1, 0, 2), fb[rows].T[..., None]
+            start, end = np.exp(G - G[:, :1])[..., None], np.exp(G[:, -1:] - G)[..., None]
+            P = scale * D * (d @ n.transpose(0, 2, 1))
+            A = b * D * (x @ n.transpose(0, 2, 1)) * np.tril(np.ones(D.shape[1:]), -1)
+            aq[rows] = (scale * start * (d @ S.transpose(0, 2, 1)) + P @ kk).transpose(1, 0, 2)
+            ak[rows] = (b * start * (x @ S.transpose(0, 2, 1)) + end * (n @ dS.transpose(0, 2, 1)) + P.transpose(0, 2, 1) @ qq +
+                        (A + A.transpose(0, 2, 1)) @ kk).transpose(1, 0, 2)
+    shared = lambda t: t.reshape(B, T, H, HV // H, -1).sum(3)   # noqa: E731
+    return shared(aq), shared(ak)
 
 
 def largest(ref, axes):

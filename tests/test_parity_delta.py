@@ -85,7 +85,8 @@ def check_bwd(B, s, x, scale=None):
     got = B.delta_bwd(*(dev(s[n]) for n in names), dev(x["do"]), scale=scale, initial_state=dev(x["h0"]), dht=dev(x["dht"]),
                       cu_seqlens=dev(x["cu"]))
     assert B.layer_status() == B.GLA_OK
-    ref = do.delta_bwd(*(f64(s[n]) for n in names), f64(x["do"]), scale or K ** -0.5, f64(x["h0"]), f64(x["dht"]), x["cu"])
+    keep, scale = {}, scale or K ** -0.5
+    ref = do.delta_bwd(*(f64(s[n]) for n in names), f64(x["do"]), scale, f64(x["h0"]), f64(x["dht"]), x["cu"], keep)
     dq, dk, dv, dg, db, dh0 = ref
     rel = do.bound("chunk" if chunked(q.dtype, K, V) else "scan", K, V, T, backward=True)
     inside = slice(0, T if x["cu"] is None else int(x["cu"][-1]))
@@ -94,10 +95,14 @@ def check_bwd(B, s, x, scale=None):
     size_k = np.maximum(do.largest(dk, (0, 1, 3)), do.largest(dq, (0, 1, 3))) * per + \
         do.largest(dv.reshape(*dv.shape[:2], q.shape[2], -1), (0, 1, 3))
     size_v = do.largest(dv, (0, 1, 3)) + np.repeat(size_k, per, 2)
+    size_dq = size_dk = size_k
+    if chunked(q.dtype, K, V):   # operands of one 16-bit term: three roundings a term
+        aq, ak = do.grad_sizes(f64(q), f64(s["k"]), f64(s["g"]), f64(s["beta"]), f64(x["do"]), scale, *q.shape[:2], x["cu"], keep)
+        size_dq, size_dk = (size_k + 3 * lo.UNIT[KIND[q.dtype]] / rel * a[:, inside] for a in (aq, ak))
     # sums over a chunk of products of two rows: eight times (64 terms of random sign) the lengths' product
     long = lambda t: np.linalg.norm(t, axis=-1).max(initial=0.0)   # noqa: E731
     size_g = 8 * (long(dq) + long(dk) + long(dv) * (long(f64(v)[:, inside]) + 1)) + np.abs(f64(x["dht"]) if x["dht"] is not None else 0).max(initial=0.0)
-    for name, y, r, size in (("dq", got[0], dq, size_k), ("dk", got[1], dk, size_k), ("dv", got[2], dv, size_v),
+    for name, y, r, size in (("dq", got[0], dq, size_dq), ("dk", got[1], dk, size_dk), ("dv", got[2], dv, size_v),
                              ("dg", got[3], dg, size_g), ("dbeta", got[4], db, size_g), ("dh0", got[5], dh0, do.largest(dh0, (2, 3)))):
         close(y[:, inside] if name != "dh0" else y, r[:, inside] if name != "dh0" else r, size, rel, name)
     return got
