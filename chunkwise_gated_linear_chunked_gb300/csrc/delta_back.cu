@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             s[j][0] += p.x, s[j][1] += p.y, s[j][2] += p.z, s[j][3] += p.w;
         }
     };
+    constexpr bool kChecked = std::is_same_v<T, __half>;
+    bool bad = false;
     auto help = [&](typename Shared::Stage &st, int c) {
         const float4 *row = st.cell.row;
         const size_t cell = (size_t)(w.slot + c) * a.HV + w.hv;
@@ -173,6 +175,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 const int j = 2 * i + e, t = 8 * j + two;
                 const float4 x = sh.n[group][j][lane];
                 const float b0 = row[t].x, b1 = row[t + 1].x;
+                if constexpr (kChecked)
+                    bad |= lost(x.x) || lost(x.y) || lost(x.z) || lost(x.w);
                 const float2 v0 = widen2<T>(v[2 * e]), v1 = widen2<T>(v[2 * e + 1]);
                 xw[2 * e] = narrow2<T>(make_float2(x.x, x.y));
                 xw[2 * e + 1] = narrow2<T>(make_float2(x.z, x.w));
@@ -244,10 +248,13 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             }
             chain(st, s);
         });
+        report_lost<T>(a, s, false);
         if (a.dh0)
             state_io<KD>(s, a.dh0, nullptr, state, a.V, col, on, true);
     } else {
         walk([&](auto &st, int c) { help(st, c); });
+        if (kChecked && bad)
+            report(a.status, GLA_ERR_RANGE);
     }
 }
 

@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     };
     const DeltaTrace trace = SAVE ? a.trace : DeltaTrace();
     const int g16 = (w.v0 >> 4) + group;   // this group of 16 columns among the head's
+    constexpr bool kChecked = std::is_same_v<T, __half>;
+    bool bad = false;
     auto put_out = [&](typename Shared::Stage &st, int c) {
         const float4 *row = st.cell.row;
         const size_t cell = (size_t)(w.slot + c) * a.HV + w.hv;
@@ -150,6 +152,12 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             split_pair<T>(n[0], n[1], hi[i], lo[i]);
         }
         triangle<T, false>(o, hi, lo, st.cell.score, lane);
+        if constexpr (kChecked)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)   // rows behind the end have q and N of zero
+                    bad |= lost(o[j][e]);
         if constexpr (SAVE) {
             if (on)
                 put_blocks<4>(trace.n + cell * trace.n_size, hi, 2 * g16, 8, lane);
@@ -216,10 +224,13 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                     to[j * 32] = as_float4(s[j]);
             }
         });
+        report_lost<T>(a, s, false);
         if (!SAVE && a.ht)
             state_io<KD>(s, a.ht, nullptr, state, a.V, col, on, true);
     } else {
         walk([&](auto &st, int c) { put_out(st, c); });
+        if (kChecked && bad)
+            report(a.status, GLA_ERR_RANGE);
     }
 }
 

@@ -159,6 +159,23 @@ __device__ __forceinline__ void sum_over_columns(float (&v)[N], int lane)
     }
 }
 
+// Whether a value is not finite.  With fp16 operands (GLA_F16) such a result is reported: a value on the way may have left
+// their range, where bf16 has fp32's.
+__device__ __forceinline__ bool lost(float v) { return !(fabsf(v) <= 3.402823466e38f); }
+template <typename T, int N>
+__device__ __forceinline__ void report_lost(const DeltaArgs &a, const float (&s)[N][4], bool already)
+{
+    if constexpr (std::is_same_v<T, __half>) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                already |= lost(s[j][e]);
+        if (already)
+            report(a.status, GLA_ERR_RANGE);
+    }
+}
+
 // What a CTA walks.
 struct ChainWalk {
     int n, hv, hk, bos, len, chunks, slot, v0;

@@ -311,6 +311,20 @@ def test_bad_slots_are_reported(B):
     assert B.layer_status() == B.GLA_ERR_INVALID_ARG and (o == 0).all() and (pool == 1).all()
 
 
+def test_fp16_range_is_reported(B):
+    """A state that leaves fp16's range on the chunked path; token by token, and in bf16, it does not matter."""
+    for dtype, K, want in ((TH, 64, "GLA_ERR_RANGE"), (TH, 96, "GLA_OK"), (TB, 64, "GLA_OK")):
+        s, x = make(dtype, Bn=1, T=100, K=K, V=64, seed=15)
+        args = [dev(s[n]) for n in ("q", "k", "v", "g", "beta")]
+        o, ht = B.delta_fwd(*args, initial_state=1e5 * torch.ones(1, 1, K, 64, device="cuda"), out_dtype=T32)
+        assert B.layer_status() == getattr(B, want)
+        assert torch.isfinite(o).all() == (want == "GLA_OK")
+        B.delta_bwd(*args, dev(x["do"]), dht=1e5 * torch.ones(1, 1, K, 64, device="cuda"))
+        assert B.layer_status() == getattr(B, want)
+        B.delta_bwd(*args, dev(x["do"]))
+        assert B.layer_status() == B.GLA_OK
+
+
 def test_nothing_to_do(B):
     z = lambda *s: torch.zeros(*s, device="cuda")   # noqa: E731
     o, ht = B.delta_fwd(z(0, 5, 2, 64), z(0, 5, 2, 64), z(0, 5, 2, 64), z(0, 5, 2), z(0, 5, 2))
