@@ -866,6 +866,10 @@ def delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, output_final_sta
     [N, HV, K, V] or None).  Bad offsets are reported on the device, see ``layer_status`` (or the call's own ``status``,
     256 zeroed bytes).
     """
+    if status is None and workspace is None and stream is None:
+        got = _calls.delta_fwd(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype)
+        if got is not None:
+            return got
     return _delta_fwd_checked(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype, status,
                               workspace, stream=stream)
 
@@ -900,6 +904,10 @@ def delta_bwd(q, k, v, g, beta, do, scale=None, initial_state=None, dht=None, cu
     The inputs as for delta_fwd; do: [B, T, HV, V] of q's type; dht: fp32 [N, HV, K, V] or None.  Returns (dq, dk, dv in
     q's type, dg, dbeta fp32 [B, T, HV], dh0 fp32 [N, HV, K, V] or None).
     """
+    if status is None and workspace is None and stream is None:
+        got = _calls.delta_bwd(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0)
+        if got is not None:
+            return got
     return _delta_bwd_checked(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0, status, workspace,
                               stream=stream)
 
@@ -937,6 +945,10 @@ def delta_step(q, k, v, g, beta, state, scale=None, slots=None, state_out=None, 
     updated in place (or written to state_out, of which only the addressed rows are written); slots as for scan_step.
     out_dtype: q's type (default) or fp32.  Returns o [B, HV, V].
     """
+    if status is None and stream is None:
+        got = _calls.delta_step(q, k, v, g, beta, state, scale, slots, state_out, out_dtype)
+        if got is not None:
+            return got
     return _delta_step_checked(q, k, v, g, beta, state, scale, slots, state_out, out_dtype, status, stream=stream)
 
 
@@ -986,6 +998,10 @@ def group_norm_fwd(x, groups, weight=None, bias=None, activation=None, eps=1e-5,
     mixing layer's output have (groups: the heads).  weight, bias: fp32 [C] or None; activation: None or "silu".
     Returns (y in x's type, mean, rstd fp32 [N, groups]).
     """
+    if workspace is None and stream is None:
+        got = _calls.group_norm_fwd(x, groups, weight, bias, activation, eps)
+        if got is not None:
+            return got
     return _group_norm_fwd_checked(x, groups, weight, bias, activation, eps, workspace, stream=stream)
 
 
@@ -1009,6 +1025,10 @@ def group_norm_bwd(x, mean, rstd, dy, weight=None, bias=None, activation=None, w
     Returns (dx in x's type, dw fp32 [C] or None without a weight, db fp32 [C] or None without a bias);
     ``want_dw=False`` skips both.
     """
+    if workspace is None and stream is None:
+        got = _calls.group_norm_bwd(x, mean, rstd, dy, weight, bias, activation, want_dw)
+        if got is not None:
+            return got
     return _group_norm_bwd_checked(x, mean, rstd, dy, weight, bias, activation, want_dw, workspace, stream=stream)
 
 

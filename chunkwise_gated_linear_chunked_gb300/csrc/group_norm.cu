@@ -52,29 +52,34 @@ __device__ __forceinline__ float before_act(float dy, float z, bool silu)
     return dy * s * fmaf(z, 1.f - s, 1.f);
 }
 
-// Count, mean and sum of squares about the mean of some values.
-struct Moments {
-    float n, mean, m2;
-};
-__device__ __forceinline__ Moments joined(Moments a, Moments b)
-{
-    if (a.n == 0.f || b.n == 0.f)
-        return a.n == 0.f ? b : a;
-    const float n = a.n + b.n, d = b.mean - a.mean, f = b.n / n;
-    return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * (a.n * f)};
-}
-__device__ __forceinline__ Moments shuffled(Moments a, int m)
-{
-    return {__shfl_xor_sync(~0u, a.n, m), __shfl_xor_sync(~0u, a.mean, m), __shfl_xor_sync(~0u, a.m2, m)};
-}
-__device__ __forceinline__ Moments over_warp(Moments a)
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
-    for (int m = 1; m < 32; m *= 2) {   // the lower lane's first on both sides, so that they agree
-        const Moments b = shuffled(a, m);
-        a = threadIdx.x & m ? joined(b, a) : joined(a, b);
+    for (int m = 16; m; m /= 2)
+        v += __shfl_xor_sync(~0u, v, m);
+    return v;
+}
+
+// Joins means and sums of squares about them, `many` parts by a warp: the mean first, then what the parts' means spread
+// about it (part(i): count, mean, squares).  -> count, mean, squares.
+template <typename F>
+__device__ __forceinline__ float3 join_parts(int many, F part)
+{
+    const int lane = threadIdx.x % 32;
+    float n = 0.f, sum = 0.f, sq = 0.f;
+    for (int i = lane; i < many; i += 32) {
+        const float3 p = part(i);
+        n += p.x;
+        sum = fmaf(p.x, p.y, sum);
     }
-    return a;
+    n = warp_sum(n);
+    const float mean = warp_sum(sum) / n;
+    for (int i = lane; i < many; i += 32) {
+        const float3 p = part(i);
+        const float d = p.y - mean;
+        sq += p.x > 0.f ? fmaf(p.x * d, d, p.z) : 0.f;
+    }
+    return make_float3(n, mean, warp_sum(sq));
 }
 
 // Sum of two values over the lanes of a group: L lanes of a warp, or L / 32 warps by way of shared memory.
@@ -104,8 +109,102 @@ __device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
 // Tokens: one position a sample.  Unit u is group u % G of sample u / G; a CTA holds kThreads / L units, and the grid's
 // units are a multiple of G, so that a lane's next unit has the same channels.
 // ---------------------------------------------------------------------------------------------------------
-template <typename T, int VEC, int NV, bool BACK>
+// UNITS: of a lane's group at a time, so that enough loads are under way.
+template <typename T, int VEC, int NV, int UNITS>
 __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L)
+{
+    __shared__ float2 part[kThreads / 32];
+    tc::grid_dep_wait();
+    const int W = a.W, lane = threadIdx.x % L, per = kThreads / L;
+    const int64_t units = a.N * a.G, stride = (int64_t)gridDim.x * per;
+    const int64_t u0 = (int64_t)blockIdx.x * per + threadIdx.x / L;
+    const int c0 = (int)(u0 % a.G) * W;
+    const bool silu = a.silu;
+    const float inv = 1.f / W;
+    typedef Vec<T, VEC> V;
+    float w[NV][VEC], b[NV][VEC];
+    bool on[NV];
+    V x[UNITS][NV] = {};
+    auto ask = [&](int64_t u) {
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (on[i] && u + k * stride < units)
+                    x[k][i] = *reinterpret_cast<const V *>(static_cast<const T *>(a.x) + (u + k * stride) * W + (lane + L * i) * VEC);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        on[i] = (lane + L * i) * VEC < W;
+    ask(u0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = c0 + (lane + L * i) * VEC + e;
+            w[i][e] = a.w && on[i] ? a.w[c] : 1.f;
+            b[i][e] = a.b && on[i] ? a.b[c] : 0.f;
+        }
+    // all of a CTA's units take the same turns, as they may share its barriers
+    for (int64_t base = (int64_t)blockIdx.x * per; base < units; base += UNITS * stride) {
+        const int64_t u = base + threadIdx.x / L;
+        float f[UNITS][NV][VEC], mean[UNITS], rstd[UNITS];
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    f[k][i][e] = on[i] ? widen(x[k][i].v[e]) : 0.f;
+                    sum += f[k][i][e];
+                }
+            mean[k] = sum;
+        }
+        ask(u + UNITS * stride);
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+            mean[k] = group_sum(make_float2(mean[k], 0.f), L, part).x * inv;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    f[k][i][e] = on[i] ? f[k][i][e] - mean[k] : 0.f;
+                    sq = fmaf(f[k][i][e], f[k][i][e], sq);
+                }
+            rstd[k] = sq;
+        }
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+            rstd[k] = rsqrtf(fmaf(group_sum(make_float2(rstd[k], 0.f), L, part).x, inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const int64_t at = u + k * stride;
+            if (at >= units)
+                continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!on[i])
+                    continue;
+                V y;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    y.v[e] = narrow<T>(activated(fmaf(f[k][i][e] * rstd[k], w[i][e], b[i][e]), silu));
+                *reinterpret_cast<V *>(static_cast<T *>(a.y) + at * W + (lane + L * i) * VEC) = y;
+            }
+            if (lane == 0) {
+                a.mean[at] = mean[k];
+                a.rstd[at] = rstd[k];
+            }
+        }
+    }
+}
+
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, int L)
 {
     __shared__ float2 part[kThreads / 32];
     tc::grid_dep_wait();
@@ -137,8 +236,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
     };
     V next[NV] = {}, next_dy[NV] = {};
     ask(a.x, u0, next);
-    if constexpr (BACK)
-        ask(a.dy, u0, next_dy);
+    ask(a.dy, u0, next_dy);
     // all of a CTA's units take the same turns, as they may share its barriers
     for (int64_t base = (int64_t)blockIdx.x * per; base < units; base += stride) {
         const int64_t u = base + threadIdx.x / L;
@@ -147,91 +245,52 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             x[i] = next[i];
-            if constexpr (BACK)
-                dy[i] = next_dy[i];
+            dy[i] = next_dy[i];
         }
         ask(a.x, u + stride, next);
-        if constexpr (BACK)
-            ask(a.dy, u + stride, next_dy);
-        if constexpr (!BACK) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    sum += on[i] ? widen(x[i].v[e]) : 0.f;
-            const float mean = group_sum(make_float2(sum, 0.f), L, part).x * inv;
-            float sq = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = on[i] ? widen(x[i].v[e]) - mean : 0.f;
-                    sq = fmaf(d, d, sq);
-                }
-            const float rstd = rsqrtf(fmaf(group_sum(make_float2(sq, 0.f), L, part).x, inv, a.eps));
-            if (!live)
-                continue;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!on[i])
-                    continue;
-                V y;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    y.v[e] = narrow<T>(activated(fmaf((widen(x[i].v[e]) - mean) * rstd, w[i][e], b[i][e]), silu));
-                *reinterpret_cast<V *>(static_cast<T *>(a.y) + u * W + (lane + L * i) * VEC) = y;
-            }
-            if (lane == 0) {
-                a.mean[u] = mean;
-                a.rstd[u] = rstd;
-            }
-        } else {
-            const float mean = live ? a.mean_in[u] : 0.f, rstd = live ? a.rstd_in[u] : 0.f;
-            float xh[NV][VEC], g[NV][VEC];
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    if (!on[i] || !live)
-                        continue;
-                    const float n = (widen(x[i].v[e]) - mean) * rstd;
-                    const float dz = before_act(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]), silu);
-                    db[i][e] += dz;
-                    dw[i][e] = fmaf(dz, n, dw[i][e]);
-                    xh[i][e] = n;
-                    g[i][e] = dz * w[i][e];
-                    sum = make_float2(sum.x + g[i][e], fmaf(g[i][e], n, sum.y));
-                }
-            sum = group_sum(sum, L, part);
-            if (!live)
-                continue;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!on[i])
-                    continue;
-                V dx;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    dx.v[e] = narrow<T>(rstd * (g[i][e] - inv * fmaf(xh[i][e], sum.y, sum.x)));
-                *reinterpret_cast<V *>(static_cast<T *>(a.dx) + u * W + (lane + L * i) * VEC) = dx;
-            }
-        }
-    }
-    if constexpr (BACK) {
-        if (!a.part_dw)
-            return;
-        float *pw = a.part_dw + (size_t)u0 * W, *pb = a.part_db + (size_t)u0 * W;
+        ask(a.dy, u + stride, next_dy);
+        const float mean = live ? a.mean_in[u] : 0.f, rstd = live ? a.rstd_in[u] : 0.f;
+        float xh[NV][VEC], g[NV][VEC];
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (!on[i] || !live)
+                    continue;
+                const float n = (widen(x[i].v[e]) - mean) * rstd;
+                const float dz = before_act(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]), silu);
+                db[i][e] += dz;
+                dw[i][e] = fmaf(dz, n, dw[i][e]);
+                xh[i][e] = n;
+                g[i][e] = dz * w[i][e];
+                sum = make_float2(sum.x + g[i][e], fmaf(g[i][e], n, sum.y));
+            }
+        sum = group_sum(sum, L, part);
+        if (!live)
+            continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!on[i])
+                continue;
+            V dx;
+#pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (on[i]) {
-                    pw[(lane + L * i) * VEC + e] = dw[i][e];
-                    pb[(lane + L * i) * VEC + e] = db[i][e];
-                }
+                dx.v[e] = narrow<T>(rstd * (g[i][e] - inv * fmaf(xh[i][e], sum.y, sum.x)));
+            *reinterpret_cast<V *>(static_cast<T *>(a.dx) + u * W + (lane + L * i) * VEC) = dx;
+        }
     }
+    if (!a.part_dw)
+        return;
+    float *pw = a.part_dw + (size_t)u0 * W, *pb = a.part_db + (size_t)u0 * W;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (on[i]) {
+                pw[(lane + L * i) * VEC + e] = dw[i][e];
+                pb[(lane + L * i) * VEC + e] = db[i][e];
+            }
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -308,17 +367,14 @@ __global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, Gr
     __syncthreads();
     const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
     for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
-        const int lo = max(g * a.W, s.c0) - s.c0, hi = min((g + 1) * a.W, s.c0 + s.cc) - s.c0;
-        Moments m = {0.f, 0.f, 0.f};
-        const int many = (hi - lo) * sp.ty;
-        for (int i = lane; i < many; i += 32) {
-            const int y = i / (hi - lo), c = lo + i - y * (hi - lo);
-            const float2 h = held[y * sp.chunk + c];
-            m = joined(m, {rows_of(y), h.x, h.y});
-        }
-        m = over_warp(m);
+        const int lo = max(g * a.W, s.c0) - s.c0, width = min((g + 1) * a.W, s.c0 + s.cc) - s.c0 - lo;
+        const float3 m = join_parts(width * sp.ty, [&](int i) {
+            const int y = i / width;
+            const float2 h = held[y * sp.chunk + lo + i - y * width];
+            return make_float3(rows_of(y), h.x, h.y);
+        });
         if (lane == 0)
-            a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(m.n, m.mean, m.m2, 0.f);
+            a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(m.x, m.y, m.z, 0.f);
     }
 }
 
@@ -328,18 +384,16 @@ __device__ __forceinline__ void join_slices(const GroupNormArgs &a, const GroupN
     const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
     for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
         const int k0 = g * a.W / sp.chunk, k1 = ((g + 1) * a.W - 1) / sp.chunk, chunks = k1 - k0 + 1;   // chunks with its channels
-        Moments m = {0.f, 0.f, 0.f};
-        for (int i = lane; i < sp.slices * chunks; i += 32) {
+        const float3 m = join_parts(sp.slices * chunks, [&](int i) {
             const int sl = i / chunks, k = k0 + i - sl * chunks;
             const float4 p = a.part[(s.n * sp.slices + sl) * sp.entries + g + k];
-            m = joined(m, {p.x, p.y, p.z});
-        }
-        m = over_warp(m);
-        const float rstd = rsqrtf(m.m2 / m.n + a.eps);
+            return make_float3(p.x, p.y, p.z);
+        });
+        const float rstd = rsqrtf(m.z / m.x + a.eps);
         if (lane == 0) {
-            stat[g - g0] = make_float2(m.mean, rstd);
+            stat[g - g0] = make_float2(m.y, rstd);
             if (s.slice == 0 && k0 == s.chunk) {   // one CTA writes them
-                a.mean[s.n * a.G + g] = m.mean;
+                a.mean[s.n * a.G + g] = m.y;
                 a.rstd[s.n * a.G + g] = rstd;
             }
         }
@@ -502,25 +556,25 @@ __global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, Gr
     }
 }
 
-// dw and db from their partial sums: `many` rows of C.
-__global__ void __launch_bounds__(kThreads) group_norm_dw_kernel(GroupNormArgs a, int64_t many)
+// dw and db from their partial sums: `many` rows of C, 32 columns a CTA.
+__global__ void __launch_bounds__(1024) group_norm_dw_kernel(GroupNormArgs a, int64_t many)
 {
-    __shared__ float2 held[8][32];
+    __shared__ float2 held[32][33];
     tc::grid_dep_wait();
     const int lane = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float2 t = make_float2(0.f, 0.f);
     if (c < a.C)
-#pragma unroll 4
-        for (int64_t r = y; r < many; r += 8)
+#pragma unroll 8
+        for (int64_t r = y; r < many; r += 32)
             t = make_float2(t.x + a.part_dw[r * a.C + c], t.y + a.part_db[r * a.C + c]);
     held[y][lane] = t;
     __syncthreads();
-    if (y == 0 && c < a.C) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            t = make_float2(t.x + held[i][lane].x, t.y + held[i][lane].y);
-        if (a.dw) a.dw[c] = t.x;
-        if (a.db) a.db[c] = t.y;
+    t = held[lane][y];   // a warp joins a column
+    t = make_float2(warp_sum(t.x), warp_sum(t.y));
+    const int at = blockIdx.x * 32 + y;
+    if (lane == 0 && at < a.C) {
+        if (a.dw) a.dw[at] = t.x;
+        if (a.db) a.db[at] = t.y;
     }
 }
 
@@ -566,7 +620,7 @@ int64_t group_norm_token_parts(const GroupNormArgs &a, int dtype)   // rows of C
 }
 
 // Enough slices that the CTAs fill the GPU four times (two CTAs an SM at least stay busy to the end), as long as each has
-// four turns of rows.
+// 16 turns of rows, or as many as there are SMs with four turns.
 GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
 {
     const int vec = vec_of(a, dtype, false), vectors = a.C / vec;
@@ -577,8 +631,9 @@ GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
     s.ty = kThreads / s.tx;
     s.entries = a.G + s.chunks - 1;
     const int64_t want = std::max<int64_t>(1, (4 * (int64_t)sm_count()) / std::max<int64_t>(1, a.N * s.chunks));
-    const int64_t most = std::max<int64_t>(1, a.S / (4 * s.ty));
-    const int64_t slices = std::min(want, most);
+    const int64_t most = std::max<int64_t>(1, a.S / (16 * s.ty));
+    const int64_t least = std::min<int64_t>(std::max<int64_t>(1, a.S / (4 * s.ty)), std::max<int64_t>(1, sm_count() / std::max<int64_t>(1, a.N * s.chunks)));
+    const int64_t slices = std::max(least, std::min(want, most));
     s.rows = (a.S + slices - 1) / slices;
     s.slices = (int)((a.S + s.rows - 1) / s.rows);
     return s;
@@ -619,8 +674,9 @@ cudaError_t launch_group_norm_tokens(const GroupNormArgs &a, int dtype, bool bac
         constexpr int VEC = decltype(v)::value;
         auto go = [&](auto count) {
             constexpr int NV = decltype(count)::value;
-            return back ? launch_early(tokens_kernel<T, VEC, NV, true>, grid, kThreads, s, a, L)
-                        : launch_early(tokens_kernel<T, VEC, NV, false>, grid, kThreads, s, a, L);
+            constexpr int kUnits = VEC * NV <= 4 ? 4 : VEC * NV <= 8 ? 2 : 1;
+            return back ? launch_early(tokens_grad_kernel<T, VEC, NV>, grid, kThreads, s, a, L)
+                        : launch_early(tokens_kernel<T, VEC, NV, kUnits>, grid, kThreads, s, a, L);
         };
         if (nv == 1) return go(std::integral_constant<int, 1>());
         if (nv == 2) return go(std::integral_constant<int, 2>());
@@ -650,7 +706,7 @@ cudaError_t launch_group_norm_maps(const GroupNormArgs &a, const GroupNormSplit 
 
 cudaError_t launch_group_norm_dw(const GroupNormArgs &a, int64_t many, cudaStream_t s)
 {
-    return launch_early(group_norm_dw_kernel, (unsigned)((a.C + 31) / 32), kThreads, s, a, many);
+    return launch_early(group_norm_dw_kernel, (unsigned)((a.C + 31) / 32), 1024, s, a, many);
 }
 
 }  // namespace gla

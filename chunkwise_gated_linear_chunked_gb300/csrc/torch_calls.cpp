@@ -398,10 +398,244 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- gated delta rule and group norm ----
+
+// The dtype code of (input, output) types of the delta rule, or -1.
+int delta_code(at::ScalarType x, at::ScalarType o)
+{
+    if (x == at::kFloat) return o == at::kFloat ? GLA_F32 : -1;
+    if (x == at::kBFloat16) return o == at::kFloat ? GLA_BF16 : o == x ? GLA_BF16_OBF16 : -1;
+    if (x == at::kHalf) return o == at::kFloat ? GLA_F16 : o == x ? GLA_F16_OF16 : -1;
+    return -1;
+}
+
+double scale_of(PyObject *o, int64_t K, Call &c)
+{
+    const double scale = o == Py_None ? 1.0 / std::sqrt((double)K) : PyFloat_Check(o) ? PyFloat_AS_DOUBLE(o) : -1;
+    c.need(scale > 0);
+    return scale;
+}
+
+// The operands of a delta rule call: q, k [..., H, K], v [..., HV, V], g and beta fp32 [..., HV], `rank` dimensions.
+struct Delta {
+    const at::Tensor *q, *k, *v, *g, *beta;
+    int64_t H = 0, HV = 0, K = 0, V = 0;
+};
+Delta delta(Call &c, PyObject *const *a, int rank)
+{
+    Delta d = {c.take(a[0]), c.take(a[1]), c.take(a[2]), c.take(a[3]), c.take(a[4])};
+    if (!c.ok)
+        return d;
+    c.need(d.q->dim() == rank && d.v->dim() == rank && d.v->scalar_type() == d.q->scalar_type() && status(c.device));
+    c.like(d.k, *d.q, d.q->scalar_type());
+    if (!c.ok)
+        return d;
+    d.H = d.q->size(-2), d.HV = d.v->size(-2), d.K = d.q->size(-1), d.V = d.v->size(-1);
+    c.need(d.q->sizes().slice(0, rank - 2) == d.v->sizes().slice(0, rank - 2) && d.H > 0 && d.HV % d.H == 0);
+    for (int64_t n : d.q->sizes())
+        c.need(n <= INT32_MAX);
+    c.need(d.HV <= INT32_MAX && d.V <= INT32_MAX);
+    c.shaped(d.g, d.v->sizes().slice(0, rank - 1), at::kFloat);
+    c.shaped(d.beta, d.v->sizes().slice(0, rank - 1), at::kFloat);
+    return d;
+}
+
+// Sequences of a delta rule call, dense or packed.
+int delta_sequences(Call &c, const Delta &d, const at::Tensor *cu)
+{
+    if (!c.ok || !cu)
+        return c.ok ? (int)d.q->size(0) : 0;
+    c.need(cu->scalar_type() == at::kInt && cu->dim() == 1 && cu->numel() >= 1 && cu->numel() <= INT32_MAX);
+    return c.ok ? (int)cu->numel() - 1 : 0;
+}
+
+// delta_fwd(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype)
+PyObject *delta_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Call c;
+    if (n != 10)
+        return none();
+    const Delta d = delta(c, a, 4);
+    const at::Tensor *h0 = c.take(a[6], true), *cu = c.take(a[8], true);
+    if (!c.ok)
+        return none();
+    const at::ScalarType type = dtype_or(a[9], d.q->scalar_type(), c);
+    const int code = delta_code(d.q->scalar_type(), type), N = delta_sequences(c, d, cu);
+    c.need(code >= 0);
+    const double scale = scale_of(a[5], d.K, c);
+    c.shaped(h0, {N, d.HV, d.K, d.V}, at::kFloat);
+    if (!c.ok)
+        return none();
+    const int B = (int)d.q->size(0), T = (int)d.q->size(1), H = (int)d.H, HV = (int)d.HV, K = (int)d.K, V = (int)d.V;
+    const size_t need = gla_delta_fwd_workspace_size(N, B, T, H, HV, K, V, code, cu != nullptr);
+    at::Tensor o = empty(d.v->sizes(), *d.q, type), ht, ws;
+    if (PyObject_IsTrue(a[7]))
+        ht = empty({N, d.HV, d.K, d.V}, *d.q, at::kFloat);
+    if (need)
+        ws = empty({(int64_t)need}, *d.q, at::kByte);
+    const int rc = gla_delta_fwd(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), floats(d.g), floats(d.beta), o.data_ptr(),
+                                 (float)scale, floats(h0), ht.defined() ? floats(&ht) : nullptr, ints(cu), N, B, T, H, HV, K, V,
+                                 code, status(c.device), need ? ws.data_ptr() : nullptr, need, c.stream());
+    return rc == GLA_OK ? tuple_of(std::move(o), std::move(ht)) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// delta_bwd(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0)
+PyObject *delta_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Call c;
+    if (n != 11)
+        return none();
+    const Delta d = delta(c, a, 4);
+    const at::Tensor *dout = c.take(a[5]), *h0 = c.take(a[7], true), *dht = c.take(a[8], true), *cu = c.take(a[9], true);
+    if (!c.ok)
+        return none();
+    const at::ScalarType type = d.q->scalar_type();
+    const int code = type == at::kFloat ? GLA_F32 : type == at::kBFloat16 ? GLA_BF16 : type == at::kHalf ? GLA_F16 : -1;
+    const int N = delta_sequences(c, d, cu);
+    c.need(code >= 0);
+    c.like(dout, *d.v, type);
+    const double scale = scale_of(a[6], d.K, c);
+    c.shaped(h0, {N, d.HV, d.K, d.V}, at::kFloat);
+    c.shaped(dht, {N, d.HV, d.K, d.V}, at::kFloat);
+    if (!c.ok)
+        return none();
+    const int B = (int)d.q->size(0), T = (int)d.q->size(1), H = (int)d.H, HV = (int)d.HV, K = (int)d.K, V = (int)d.V;
+    const size_t need = gla_delta_bwd_workspace_size(N, B, T, H, HV, K, V, code, cu != nullptr);
+    at::Tensor dq = empty(d.q->sizes(), *d.q, type), dk = empty(d.q->sizes(), *d.q, type), dv = empty(d.v->sizes(), *d.q, type);
+    at::Tensor dg = empty(d.g->sizes(), *d.q, at::kFloat), db = empty(d.g->sizes(), *d.q, at::kFloat), dh0, ws;
+    if (PyObject_IsTrue(a[10]))
+        dh0 = empty({N, d.HV, d.K, d.V}, *d.q, at::kFloat);
+    if (need)
+        ws = empty({(int64_t)need}, *d.q, at::kByte);
+    const int rc = gla_delta_bwd(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), floats(d.g), floats(d.beta), dout->data_ptr(),
+                                 (float)scale, floats(h0), floats(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), floats(&dg),
+                                 floats(&db), dh0.defined() ? floats(&dh0) : nullptr, ints(cu), N, B, T, H, HV, K, V, code,
+                                 status(c.device), need ? ws.data_ptr() : nullptr, need, c.stream());
+    return rc == GLA_OK ? tuple_of(std::move(dq), std::move(dk), std::move(dv), std::move(dg), std::move(db), std::move(dh0)) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// delta_step(q, k, v, g, beta, state, scale, slots, state_out, out_dtype)
+PyObject *delta_step(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Call c;
+    if (n != 10)
+        return none();
+    const Delta d = delta(c, a, 3);
+    const at::Tensor *state = c.take(a[5]), *slots = c.take(a[7], true), *out = c.take(a[8], true);
+    if (!c.ok)
+        return none();
+    const at::ScalarType type = dtype_or(a[9], d.q->scalar_type(), c);
+    const int code = delta_code(d.q->scalar_type(), type);
+    c.need(code >= 0);
+    const double scale = scale_of(a[6], d.K, c);
+    const int64_t B = d.q->size(0), S = c.ok ? pool(c, state, out, slots, B, {d.HV, d.K, d.V}) : -1;
+    if (!c.ok)
+        return none();
+    at::Tensor o = empty(d.v->sizes(), *d.q, type);
+    const int rc = gla_delta_step(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), floats(d.g), floats(d.beta), o.data_ptr(),
+                                  (float)scale, floats(state), floats(out ? out : state), ints(slots), (int)B, (int)S, (int)d.H,
+                                  (int)d.HV, (int)d.K, (int)d.V, code, status(c.device), c.stream());
+    return rc == GLA_OK ? wrap(std::move(o)) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// A group norm's operands.
+struct GroupNorm {
+    int code = -1, act = -1;
+    int64_t N = 0, S = 1, C = 0;
+};
+GroupNorm group_norm(Call &c, const at::Tensor *x, const at::Tensor *w, const at::Tensor *b, PyObject *act, int64_t groups)
+{
+    GroupNorm r;
+    r.code = norm_code(x->scalar_type(), x->scalar_type());
+    r.act = act == Py_None ? GLA_ACT_NONE : PyUnicode_Check(act) && PyUnicode_CompareWithASCIIString(act, "silu") == 0 ? GLA_ACT_SILU : -1;
+    c.need(r.code >= 0 && r.act >= 0 && x->dim() >= 2);
+    if (!c.ok)
+        return r;
+    r.N = x->size(0), r.C = x->size(-1);
+    for (int64_t i = 1; i + 1 < x->dim(); ++i)
+        r.S *= x->size(i);
+    c.need(groups >= 1 && r.C >= 1 && r.C <= INT32_MAX && r.C % groups == 0 && r.S >= 1);
+    c.shaped(w, {r.C}, at::kFloat);
+    c.shaped(b, {r.C}, at::kFloat);
+    return r;
+}
+
+// group_norm_fwd(x, groups, weight, bias, activation, eps)
+PyObject *group_norm_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Call c;
+    if (n != 6)
+        return none();
+    const at::Tensor *x = c.take(a[0]), *w = c.take(a[2], true), *b = c.take(a[3], true);
+    const long groups = PyLong_Check(a[1]) ? PyLong_AsLong(a[1]) : -1;
+    if (PyErr_Occurred())
+        PyErr_Clear();
+    const double eps = number(a[5], c);
+    if (!c.ok)
+        return none();
+    const GroupNorm m = group_norm(c, x, w, b, a[4], groups);
+    if (!c.ok)
+        return none();
+    const size_t need = gla_group_norm_workspace_size(m.N, m.S, (int)m.C, (int)groups, m.code, 0);
+    at::Tensor y = empty(x->sizes(), *x, x->scalar_type()), mean = empty({m.N, groups}, *x, at::kFloat),
+               rstd = empty({m.N, groups}, *x, at::kFloat), ws;
+    if (need)
+        ws = empty({(int64_t)need}, *x, at::kByte);
+    const int rc = gla_group_norm_fwd(x->data_ptr(), floats(w), floats(b), y.data_ptr(), floats(&mean), floats(&rstd), m.N, m.S,
+                                      (int)m.C, (int)groups, (float)eps, m.act, m.code, need ? ws.data_ptr() : nullptr, need,
+                                      c.stream());
+    return rc == GLA_OK ? tuple_of(std::move(y), std::move(mean), std::move(rstd)) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// group_norm_bwd(x, mean, rstd, dy, weight, bias, activation, want_dw)
+PyObject *group_norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Call c;
+    if (n != 8)
+        return none();
+    const at::Tensor *x = c.take(a[0]), *mean = c.take(a[1]), *rstd = c.take(a[2]), *dy = c.take(a[3]), *w = c.take(a[4], true),
+                     *b = c.take(a[5], true);
+    c.need(c.ok && mean->dim() == 2);
+    if (!c.ok)
+        return none();
+    const int64_t groups = mean->size(1);
+    const GroupNorm m = group_norm(c, x, w, b, a[6], groups);
+    c.like(dy, *x, x->scalar_type());
+    c.shaped(mean, {m.N, groups}, at::kFloat);
+    c.shaped(rstd, {m.N, groups}, at::kFloat);
+    if (!c.ok)
+        return none();
+    const size_t need = gla_group_norm_workspace_size(m.N, m.S, (int)m.C, (int)groups, m.code, 1);
+    at::Tensor dx = empty(x->sizes(), *x, x->scalar_type()), dw, db, ws;
+    const bool sums = PyObject_IsTrue(a[7]);
+    if (w && sums)
+        dw = empty({m.C}, *x, at::kFloat);
+    if (b && sums)
+        db = empty({m.C}, *x, at::kFloat);
+    if (need)
+        ws = empty({(int64_t)need}, *x, at::kByte);
+    const int rc = gla_group_norm_bwd(x->data_ptr(), floats(mean), floats(rstd), floats(w), floats(b), dy->data_ptr(), dx.data_ptr(),
+                                      dw.defined() ? floats(&dw) : nullptr, db.defined() ? floats(&db) : nullptr, m.N, m.S, (int)m.C,
+                                      (int)groups, m.act, m.code, need ? ws.data_ptr() : nullptr, need, c.stream());
+    return rc == GLA_OK ? tuple_of(std::move(dx), std::move(dw), std::move(db)) : none();
+    END_HANDLE_TH_ERRORS
+}
+
 #define CALL(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL("scan_fwd", scan_fwd), CALL("scan_bwd", scan_bwd), CALL("scan_step", scan_step),
                          CALL("gla_step", step), CALL("norm_fwd", norm_fwd), CALL("norm_quant_fwd", norm_quant_fwd),
-                         CALL("norm_bwd", norm_bwd), {nullptr, nullptr, 0, nullptr}};
+                         CALL("norm_bwd", norm_bwd), CALL("delta_fwd", delta_fwd), CALL("delta_bwd", delta_bwd),
+                         CALL("delta_step", delta_step), CALL("group_norm_fwd", group_norm_fwd),
+                         CALL("group_norm_bwd", group_norm_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
