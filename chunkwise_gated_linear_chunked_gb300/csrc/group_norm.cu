@@ -41,15 +41,87 @@ __device__ __forceinline__ float sigmoid(float z)
     return r;
 }
 
-__device__ __forceinline__ float activated(float z, bool silu) { return silu ? z * sigmoid(z) : z; }
+template <bool SILU>
+__device__ __forceinline__ float activated(float z)
+{
+    if constexpr (SILU)
+        return z * sigmoid(z);
+    return z;
+}
 
 // The gradient before the activation.
-__device__ __forceinline__ float before_act(float dy, float z, bool silu)
+template <bool SILU>
+__device__ __forceinline__ float before_act(float dy, float z)
 {
-    if (!silu)
+    if constexpr (!SILU)
         return dy;
     const float s = sigmoid(z);
     return dy * s * fmaf(z, 1.f - s, 1.f);
+}
+
+// A vector of values in fp32, as pairs (the last alone where VEC is odd, i.e. 1).
+template <typename T, int VEC>
+__device__ __forceinline__ void widened(const Vec<T, VEC> &v, float (&f)[VEC])
+{
+    if constexpr (VEC % 2 == 0 && sizeof(T) == 2) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v.v);
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const float2 p = widen2<T>(w[e]);
+            f[2 * e] = p.x, f[2 * e + 1] = p.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            f[e] = widen(v.v[e]);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> narrowed(const float (&f)[VEC])
+{
+    Vec<T, VEC> v;
+    if constexpr (VEC % 2 == 0 && sizeof(T) == 2) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(v.v);
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e)
+            w[e] = narrow2<T>(make_float2(f[2 * e], f[2 * e + 1]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            v.v[e] = narrow<T>(f[e]);
+    }
+    return v;
+}
+// d = a b + c by pairs.
+template <int VEC>
+__device__ __forceinline__ void fma_all(float (&d)[VEC], const float (&a)[VEC], const float (&b)[VEC], const float (&c)[VEC])
+{
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 r = fma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+            d[e] = r.x, d[e + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            d[e] = fmaf(a[e], b[e], c[e]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_to(float (&d)[VEC], const float (&a)[VEC])
+{
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 r = add2(make_float2(d[e], d[e + 1]), make_float2(a[e], a[e + 1]));
+            d[e] = r.x, d[e + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            d[e] += a[e];
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -60,26 +132,43 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Joins means and sums of squares about them, `many` parts by a warp: the mean first, then what the parts' means spread
-// about it (part(i): count, mean, squares).  -> count, mean, squares.
-template <typename F>
-__device__ __forceinline__ float3 join_parts(int many, F part)
+// Lanes that share a group's join where a CTA has so many groups: as many as let all groups join at once.
+__device__ __forceinline__ int team_of(int groups)
 {
-    const int lane = threadIdx.x % 32;
+    int t = 32;
+    while (t > 1 && t * groups > kThreads)
+        t /= 2;
+    return t;
+}
+__device__ __forceinline__ float team_sum(float v, int team)
+{
+    for (int m = team / 2; m; m /= 2)
+        v += __shfl_xor_sync(~0u, v, m);
+    return v;
+}
+
+// Joins means and sums of squares about them, `many` parts by a team of lanes: the mean first, then what the parts' means
+// spread about it (part(i): count, mean, squares).  -> count, mean, squares.  All lanes of a warp call it.
+template <typename F>
+__device__ __forceinline__ float3 join_parts(int many, int team, F part)
+{
+    const int lane = threadIdx.x % team;
     float n = 0.f, sum = 0.f, sq = 0.f;
-    for (int i = lane; i < many; i += 32) {
+#pragma unroll 4
+    for (int i = lane; i < many; i += team) {
         const float3 p = part(i);
         n += p.x;
         sum = fmaf(p.x, p.y, sum);
     }
-    n = warp_sum(n);
-    const float mean = warp_sum(sum) / n;
-    for (int i = lane; i < many; i += 32) {
+    n = team_sum(n, team);
+    const float mean = team_sum(sum, team) / n;
+#pragma unroll 4
+    for (int i = lane; i < many; i += team) {
         const float3 p = part(i);
         const float d = p.y - mean;
         sq += p.x > 0.f ? fmaf(p.x * d, d, p.z) : 0.f;
     }
-    return make_float3(n, mean, warp_sum(sq));
+    return make_float3(n, mean, team_sum(sq, team));
 }
 
 // Sum of two values over the lanes of a group: L lanes of a warp, or L / 32 warps by way of shared memory.
@@ -110,7 +199,7 @@ __device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
 // units are a multiple of G, so that a lane's next unit has the same channels.
 // ---------------------------------------------------------------------------------------------------------
 // UNITS: of a lane's group at a time, so that enough loads are under way.
-template <typename T, int VEC, int NV, int UNITS>
+template <typename T, int VEC, int NV, int UNITS, bool SILU>
 __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L)
 {
     __shared__ float2 part[kThreads / 32];
@@ -119,7 +208,6 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
     const int64_t units = a.N * a.G, stride = (int64_t)gridDim.x * per;
     const int64_t u0 = (int64_t)blockIdx.x * per + threadIdx.x / L;
     const int c0 = (int)(u0 % a.G) * W;
-    const bool silu = a.silu;
     const float inv = 1.f / W;
     typedef Vec<T, VEC> V;
     float w[NV][VEC], b[NV][VEC];
@@ -151,15 +239,16 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
         float f[UNITS][NV][VEC], mean[UNITS], rstd[UNITS];
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
-            float sum = 0.f;
+            float sum[VEC] = {};   // lanes without values hold zeros
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                widened(x[k][i], f[k][i]);
+                add_to(sum, f[k][i]);
+            }
+            mean[k] = 0.f;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    f[k][i][e] = on[i] ? widen(x[k][i].v[e]) : 0.f;
-                    sum += f[k][i][e];
-                }
-            mean[k] = sum;
+            for (int e = 0; e < VEC; ++e)
+                mean[k] += sum[e];
         }
         ask(u + UNITS * stride);
 #pragma unroll
@@ -167,15 +256,22 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
             mean[k] = group_sum(make_float2(mean[k], 0.f), L, part).x * inv;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
-            float sq = 0.f;
+            rstd[k] = 0.f;
+            float minus[VEC];
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int e = 0; e < VEC; ++e)
+                minus[e] = -mean[k];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    f[k][i][e] = on[i] ? f[k][i][e] - mean[k] : 0.f;
-                    sq = fmaf(f[k][i][e], f[k][i][e], sq);
-                }
-            rstd[k] = sq;
+            for (int i = 0; i < NV; ++i) {
+                float sq[VEC] = {};
+                add_to(f[k][i], minus);
+                fma_all(sq, f[k][i], f[k][i], sq);
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    sum += sq[e];
+                rstd[k] += on[i] ? sum : 0.f;
+            }
         }
 #pragma unroll
         for (int k = 0; k < UNITS; ++k)
@@ -185,15 +281,21 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
             const int64_t at = u + k * stride;
             if (at >= units)
                 continue;
+            float r[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                r[e] = rstd[k];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!on[i])
                     continue;
-                V y;
+                float y[VEC], zero[VEC] = {};
+                fma_all(y, f[k][i], r, zero);
+                fma_all(y, y, w[i], b[i]);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    y.v[e] = narrow<T>(activated(fmaf(f[k][i][e] * rstd[k], w[i][e], b[i][e]), silu));
-                *reinterpret_cast<V *>(static_cast<T *>(a.y) + at * W + (lane + L * i) * VEC) = y;
+                    y[e] = activated<SILU>(y[e]);
+                *reinterpret_cast<V *>(static_cast<T *>(a.y) + at * W + (lane + L * i) * VEC) = narrowed<T, VEC>(y);
             }
             if (lane == 0) {
                 a.mean[at] = mean[k];
@@ -203,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
     }
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool SILU>
 __global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, int L)
 {
     __shared__ float2 part[kThreads / 32];
@@ -212,7 +314,6 @@ __global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, 
     const int64_t units = a.N * a.G, stride = (int64_t)gridDim.x * per;
     const int64_t u0 = (int64_t)blockIdx.x * per + threadIdx.x / L;
     const int c0 = (int)(u0 % a.G) * W;
-    const bool silu = a.silu;
     const float inv = 1.f / W;
     typedef Vec<T, VEC> V;
     float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
@@ -259,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, 
                 if (!on[i] || !live)
                     continue;
                 const float n = (widen(x[i].v[e]) - mean) * rstd;
-                const float dz = before_act(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]), silu);
+                const float dz = before_act<SILU>(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]));
                 db[i][e] += dz;
                 dw[i][e] = fmaf(dz, n, dw[i][e]);
                 xh[i][e] = n;
@@ -314,15 +415,6 @@ __device__ __forceinline__ Slice slice_of(const GroupNormArgs &a, const GroupNor
     return r;
 }
 
-// Sums over the TY rows that a CTA takes at a time: what each thread holds for its channels goes to `to`, [TY][chunk].
-template <int VEC>
-__device__ __forceinline__ void lay_out(float2 *to, const float2 (&v)[VEC], int tx, int ty, int chunk)
-{
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-        to[ty * chunk + tx * VEC + e] = v[e];
-}
-
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
@@ -333,65 +425,80 @@ __global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, Gr
     const bool on = ty < sp.ty && tx * VEC < s.cc;
     typedef Vec<T, VEC> V;
     const T *x = static_cast<const T *>(a.x) + (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
-    float first[VEC], s1[VEC] = {}, s2[VEC] = {};
-    if (on && ty < s.rows) {
-        const V v = *reinterpret_cast<const V *>(x + (int64_t)ty * a.C);
+    auto rows_of = [&](int y) { return y < s.rows ? (float)((s.rows - y + sp.ty - 1) / sp.ty) : 0.f; };
+    const bool whole = a.W % VEC == 0;   // a vector's channels are of one group
+    if (on) {
+        const float many = rows_of(ty), inv = many > 0.f ? 1.f / many : 0.f;
+        float mean[VEC] = {}, m2[VEC] = {};
+        if (many > 0.f) {
+            float minus[VEC], s1[VEC] = {}, s2[VEC] = {};
+            widened(*reinterpret_cast<const V *>(x + (int64_t)ty * a.C), minus);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            first[e] = widen(v.v[e]);
+            for (int e = 0; e < VEC; ++e)
+                minus[e] = -minus[e];
 #pragma unroll 4
-        for (int64_t r = ty + sp.ty; r < s.rows; r += sp.ty) {
-            const V v = *reinterpret_cast<const V *>(x + r * a.C);
+            for (int64_t r = ty + sp.ty; r < s.rows; r += sp.ty) {
+                float d[VEC];
+                widened(*reinterpret_cast<const V *>(x + r * a.C), d);
+                add_to(d, minus);
+                add_to(s1, d);
+                fma_all(s2, d, d, s2);
+            }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float d = widen(v.v[e]) - first[e];
-                s1[e] += d;
-                s2[e] = fmaf(d, d, s2[e]);
+                mean[e] = fmaf(s1[e], inv, -minus[e]);
+                m2[e] = s2[e] - s1[e] * (s1[e] * inv);
+                m2[e] = m2[e] < 0.f ? 0.f : m2[e];   // a NaN stays
             }
         }
-    }
-    auto rows_of = [&](int y) { return y < s.rows ? (float)((s.rows - y + sp.ty - 1) / sp.ty) : 0.f; };
-    if (on) {
-        float2 m[VEC];
-        const float many = rows_of(ty);
+        if (whole) {   // of equal counts: the mean of the means, and what they spread
+            float sum = 0.f, sq = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            m[e] = many > 0.f ? make_float2(first[e] + s1[e] / many, fmaxf(s2[e] - s1[e] * (s1[e] / many), 0.f)) : make_float2(0.f, 0.f);
-        // a NaN among the values is not lost in the maximum
+            for (int e = 0; e < VEC; ++e)
+                sum += mean[e];
+            const float at = sum * (1.f / VEC);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (s2[e] != s2[e] || s1[e] != s1[e])
-                m[e].y = s2[e] + s1[e];
-        lay_out<VEC>(held, m, tx, ty, sp.chunk);
+            for (int e = 0; e < VEC; ++e)
+                sq += fmaf(many * (mean[e] - at), mean[e] - at, m2[e]);
+            held[ty * sp.tx + tx] = make_float2(at, sq);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                held[ty * sp.chunk + tx * VEC + e] = make_float2(mean[e], m2[e]);
+        }
     }
     __syncthreads();
-    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
-    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
-        const int lo = max(g * a.W, s.c0) - s.c0, width = min((g + 1) * a.W, s.c0 + s.cc) - s.c0 - lo;
-        const float3 m = join_parts(width * sp.ty, [&](int i) {
+    const int unit = whole ? VEC : 1, pitch = sp.chunk / unit;   // channels of an entry, entries of a row
+    const int g0 = s.c0 / a.W, groups = (s.c0 + s.cc - 1) / a.W - g0 + 1, team = team_of(groups);
+    for (int first = 0; first < groups; first += kThreads / team) {
+        const int k = first + threadIdx.x / team, g = g0 + min(k, groups - 1);
+        const int lo = max(g * a.W, s.c0) - s.c0, width = (min((g + 1) * a.W, s.c0 + s.cc) - s.c0 - lo) / unit;
+        const float3 m = join_parts(width * sp.ty, team, [&](int i) {
             const int y = i / width;
-            const float2 h = held[y * sp.chunk + lo + i - y * width];
-            return make_float3(rows_of(y), h.x, h.y);
+            const float2 h = held[y * pitch + lo / unit + i - y * width];
+            return make_float3(rows_of(y) * unit, h.x, h.y);
         });
-        if (lane == 0)
+        if (k < groups && threadIdx.x % team == 0)
             a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(m.x, m.y, m.z, 0.f);
     }
 }
 
-// The statistics of the groups of a CTA's chunk, joined over the slices, by warps in turn; to shared memory.
+// The statistics of the groups of a CTA's chunk, joined over the slices, to shared memory.
 __device__ __forceinline__ void join_slices(const GroupNormArgs &a, const GroupNormSplit &sp, const Slice &s, float2 *stat)
 {
-    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
-    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
-        const int k0 = g * a.W / sp.chunk, k1 = ((g + 1) * a.W - 1) / sp.chunk, chunks = k1 - k0 + 1;   // chunks with its channels
-        const float3 m = join_parts(sp.slices * chunks, [&](int i) {
-            const int sl = i / chunks, k = k0 + i - sl * chunks;
-            const float4 p = a.part[(s.n * sp.slices + sl) * sp.entries + g + k];
+    const int g0 = s.c0 / a.W, groups = (s.c0 + s.cc - 1) / a.W - g0 + 1, team = team_of(groups);
+    for (int first = 0; first < groups; first += kThreads / team) {
+        const int at = first + threadIdx.x / team, g = g0 + min(at, groups - 1);
+        const int k0 = g * a.W / sp.chunk, chunks = ((g + 1) * a.W - 1) / sp.chunk - k0 + 1;   // chunks with its channels
+        const float4 *from = a.part + s.n * sp.slices * sp.entries + g + k0;
+        const float3 m = join_parts(sp.slices * chunks, team, [&](int i) {
+            const int sl = chunks == 1 ? i : i / chunks;
+            const float4 p = from[sl * sp.entries + i - sl * chunks];
             return make_float3(p.x, p.y, p.z);
         });
         const float rstd = rsqrtf(m.z / m.x + a.eps);
-        if (lane == 0) {
-            stat[g - g0] = make_float2(m.y, rstd);
+        if (at < groups && threadIdx.x % team == 0) {
+            stat[at] = make_float2(m.y, rstd);
             if (s.slice == 0 && k0 == s.chunk) {   // one CTA writes them
                 a.mean[s.n * a.G + g] = m.y;
                 a.rstd[s.n * a.G + g] = rstd;
@@ -401,7 +508,7 @@ __device__ __forceinline__ void join_slices(const GroupNormArgs &a, const GroupN
     __syncthreads();
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads) maps_apply_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
     extern __shared__ float2 stat[];
@@ -411,13 +518,12 @@ __global__ void __launch_bounds__(kThreads) maps_apply_kernel(GroupNormArgs a, G
     const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx, g0 = s.c0 / a.W;
     if (ty >= sp.ty || tx * VEC >= s.cc)
         return;
-    const bool silu = a.silu;
-    float mean[VEC], f[VEC], b[VEC];
+    float minus[VEC], f[VEC], b[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         const int c = s.c0 + tx * VEC + e;
         const float2 st = stat[c / a.W - g0];
-        mean[e] = st.x;
+        minus[e] = -st.x;
         f[e] = a.w ? st.y * a.w[c] : st.y;
         b[e] = a.b ? a.b[c] : 0.f;
     }
@@ -427,32 +533,32 @@ __global__ void __launch_bounds__(kThreads) maps_apply_kernel(GroupNormArgs a, G
     T *y = static_cast<T *>(a.y) + at;
 #pragma unroll 4
     for (int64_t r = ty; r < s.rows; r += sp.ty) {
-        const V v = *reinterpret_cast<const V *>(x + r * a.C);
-        V o;
+        float v[VEC];
+        widened(*reinterpret_cast<const V *>(x + r * a.C), v);
+        add_to(v, minus);
+        fma_all(v, v, f, b);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            o.v[e] = narrow<T>(activated(fmaf(widen(v.v[e]) - mean[e], f[e], b[e]), silu));
-        *reinterpret_cast<V *>(y + r * a.C) = o;
+            v[e] = activated<SILU>(v[e]);
+        *reinterpret_cast<V *>(y + r * a.C) = narrowed<T, VEC>(v);
     }
 }
 
 // Backward, first pass: dz and dz xh summed per channel over a slice, and w times them by group.
-template <typename T, int VEC>
+template <typename T, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
     __shared__ float2 held[kThreads * VEC];
     tc::grid_dep_wait();
     const Slice s = slice_of(a, sp);
     const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
-    const bool silu = a.silu;
     if (ty < sp.ty && tx * VEC < s.cc) {
-        float mean[VEC], rstd[VEC], w[VEC], b[VEC];
-        float2 sum[VEC] = {};   // dz, dz xh
+        float minus[VEC], rstd[VEC], w[VEC], b[VEC], zero[VEC] = {}, sum_z[VEC] = {}, sum_zn[VEC] = {};
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int c = s.c0 + tx * VEC + e;
             const int64_t g = s.n * a.G + c / a.W;
-            mean[e] = a.mean_in[g];
+            minus[e] = -a.mean_in[g];
             rstd[e] = a.rstd_in[g];
             w[e] = a.w ? a.w[c] : 1.f;
             b[e] = a.b ? a.b[c] : 0.f;
@@ -462,15 +568,24 @@ __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs 
         const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
 #pragma unroll 4
         for (int64_t r = ty; r < s.rows; r += sp.ty) {
-            const V v = *reinterpret_cast<const V *>(x + r * a.C), d = *reinterpret_cast<const V *>(dy + r * a.C);
+            float n[VEC], dz[VEC];
+            widened(*reinterpret_cast<const V *>(x + r * a.C), n);
+            widened(*reinterpret_cast<const V *>(dy + r * a.C), dz);
+            add_to(n, minus);
+            fma_all(n, n, rstd, zero);
+            if constexpr (SILU) {
+                float z[VEC];
+                fma_all(z, n, w, b);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float n = (widen(v.v[e]) - mean[e]) * rstd[e];
-                const float dz = before_act(widen(d.v[e]), fmaf(n, w[e], b[e]), silu);
-                sum[e] = make_float2(sum[e].x + dz, fmaf(dz, n, sum[e].y));
+                for (int e = 0; e < VEC; ++e)
+                    dz[e] = before_act<SILU>(dz[e], z[e]);
             }
+            add_to(sum_z, dz);
+            fma_all(sum_zn, dz, n, sum_zn);
         }
-        lay_out<VEC>(held, sum, tx, ty, sp.chunk);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            held[ty * sp.chunk + tx * VEC + e] = make_float2(sum_z[e], sum_zn[e]);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < s.cc; c += kThreads) {
@@ -488,52 +603,55 @@ __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs 
         held[c] = make_float2(w * t.x, w * t.y);
     }
     __syncthreads();
-    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
-    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+    const int g0 = s.c0 / a.W, groups = (s.c0 + s.cc - 1) / a.W - g0 + 1, team = team_of(groups);
+    for (int first = 0; first < groups; first += kThreads / team) {
+        const int k = first + threadIdx.x / team, g = g0 + min(k, groups - 1);
         const int lo = max(g * a.W, s.c0) - s.c0, hi = min((g + 1) * a.W, s.c0 + s.cc) - s.c0;
         float2 t = make_float2(0.f, 0.f);
-        for (int c = lo + lane; c < hi; c += 32)
+        for (int c = lo + threadIdx.x % team; c < hi; c += team)
             t = make_float2(t.x + held[c].x, t.y + held[c].y);
-        t = group_sum(t, 32, nullptr);
-        if (lane == 0)
+        t = make_float2(team_sum(t.x, team), team_sum(t.y, team));
+        if (k < groups && threadIdx.x % team == 0)
             a.part[(s.n * sp.slices + s.slice) * sp.entries + g + s.chunk] = make_float4(t.x, t.y, 0.f, 0.f);
     }
 }
 
 // Backward, second pass: dx.
-template <typename T, int VEC>
+template <typename T, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
     extern __shared__ float2 stat[];
     tc::grid_dep_wait();
     const Slice s = slice_of(a, sp);
-    const int g0 = s.c0 / a.W, g1 = (s.c0 + s.cc - 1) / a.W, lane = threadIdx.x % 32;
+    const int g0 = s.c0 / a.W, groups = (s.c0 + s.cc - 1) / a.W - g0 + 1, team = team_of(groups);
     const float inv = 1.f / ((float)a.W * (float)a.S);
-    for (int g = g0 + threadIdx.x / 32; g <= g1; g += kThreads / 32) {
+    for (int first = 0; first < groups; first += kThreads / team) {
+        const int at = first + threadIdx.x / team, g = g0 + min(at, groups - 1);
         const int k0 = g * a.W / sp.chunk, chunks = ((g + 1) * a.W - 1) / sp.chunk - k0 + 1;
+        const float4 *from = a.part + s.n * sp.slices * sp.entries + g + k0;
         float2 t = make_float2(0.f, 0.f);
-        for (int i = lane; i < sp.slices * chunks; i += 32) {
-            const int sl = i / chunks, k = k0 + i - sl * chunks;
-            const float4 p = a.part[(s.n * sp.slices + sl) * sp.entries + g + k];
+#pragma unroll 4
+        for (int i = threadIdx.x % team; i < sp.slices * chunks; i += team) {
+            const int sl = chunks == 1 ? i : i / chunks;
+            const float4 p = from[sl * sp.entries + i - sl * chunks];
             t = make_float2(t.x + p.x, t.y + p.y);
         }
-        t = group_sum(t, 32, nullptr);
-        if (lane == 0)
-            stat[g - g0] = make_float2(t.x * inv, t.y * inv);
+        t = make_float2(team_sum(t.x, team), team_sum(t.y, team));
+        if (at < groups && threadIdx.x % team == 0)
+            stat[at] = make_float2(t.x * inv, t.y * inv);
     }
     __syncthreads();
     const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
     if (ty >= sp.ty || tx * VEC >= s.cc)
         return;
-    const bool silu = a.silu;
-    float mean[VEC], rstd[VEC], w[VEC], b[VEC];
-    float2 st[VEC];
+    float minus[VEC], rstd[VEC], w[VEC], b[VEC], m1[VEC], m2[VEC], zero[VEC] = {};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         const int c = s.c0 + tx * VEC + e;
         const int64_t g = s.n * a.G + c / a.W;
-        st[e] = stat[c / a.W - g0];
-        mean[e] = a.mean_in[g];
+        const float2 st = stat[c / a.W - g0];
+        m1[e] = -st.x, m2[e] = -st.y;
+        minus[e] = -a.mean_in[g];
         rstd[e] = a.rstd_in[g];
         w[e] = a.w ? a.w[c] : 1.f;
         b[e] = a.b ? a.b[c] : 0.f;
@@ -544,15 +662,22 @@ __global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, Gr
     T *dx = static_cast<T *>(a.dx) + at;
 #pragma unroll 2
     for (int64_t r = ty; r < s.rows; r += sp.ty) {
-        const V v = *reinterpret_cast<const V *>(x + r * a.C), d = *reinterpret_cast<const V *>(dy + r * a.C);
-        V o;
+        float n[VEC], dz[VEC], o[VEC];
+        widened(*reinterpret_cast<const V *>(x + r * a.C), n);
+        widened(*reinterpret_cast<const V *>(dy + r * a.C), dz);
+        add_to(n, minus);
+        fma_all(n, n, rstd, zero);
+        if constexpr (SILU) {
+            float z[VEC];
+            fma_all(z, n, w, b);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float n = (widen(v.v[e]) - mean[e]) * rstd[e];
-            const float dz = before_act(widen(d.v[e]), fmaf(n, w[e], b[e]), silu);
-            o.v[e] = narrow<T>(rstd[e] * (fmaf(w[e], dz, -st[e].x) - n * st[e].y));
+            for (int e = 0; e < VEC; ++e)
+                dz[e] = before_act<SILU>(dz[e], z[e]);
         }
-        *reinterpret_cast<V *>(dx + r * a.C) = o;
+        fma_all(o, w, dz, m1);
+        fma_all(o, n, m2, o);
+        fma_all(o, o, rstd, zero);
+        *reinterpret_cast<V *>(dx + r * a.C) = narrowed<T, VEC>(o);
     }
 }
 
@@ -675,8 +800,11 @@ cudaError_t launch_group_norm_tokens(const GroupNormArgs &a, int dtype, bool bac
         auto go = [&](auto count) {
             constexpr int NV = decltype(count)::value;
             constexpr int kUnits = VEC * NV <= 4 ? 4 : VEC * NV <= 8 ? 2 : 1;
-            return back ? launch_early(tokens_grad_kernel<T, VEC, NV>, grid, kThreads, s, a, L)
-                        : launch_early(tokens_kernel<T, VEC, NV, kUnits>, grid, kThreads, s, a, L);
+            if (back)
+                return a.silu ? launch_early(tokens_grad_kernel<T, VEC, NV, true>, grid, kThreads, s, a, L)
+                              : launch_early(tokens_grad_kernel<T, VEC, NV, false>, grid, kThreads, s, a, L);
+            return a.silu ? launch_early(tokens_kernel<T, VEC, NV, kUnits, true>, grid, kThreads, s, a, L)
+                          : launch_early(tokens_kernel<T, VEC, NV, kUnits, false>, grid, kThreads, s, a, L);
         };
         if (nv == 1) return go(std::integral_constant<int, 1>());
         if (nv == 2) return go(std::integral_constant<int, 2>());
@@ -696,11 +824,15 @@ cudaError_t launch_group_norm_maps(const GroupNormArgs &a, const GroupNormSplit 
     return by_norm_type(dtype, vec_of(a, dtype, false), [&](auto t, auto v) {
         typedef std::remove_pointer_t<decltype(t)> T;
         constexpr int VEC = decltype(v)::value;
-        if (pass == 0)
-            return back ? launch_early(maps_grad_sums_kernel<T, VEC>, grid, kThreads, s, a, sp)
-                        : launch_early(maps_sums_kernel<T, VEC>, grid, kThreads, s, a, sp);
-        return back ? launch_early_shared(maps_grad_kernel<T, VEC>, grid, kThreads, stat_bytes(a, sp), s, a, sp)
-                    : launch_early_shared(maps_apply_kernel<T, VEC>, grid, kThreads, stat_bytes(a, sp), s, a, sp);
+        auto by_act = [&](auto silu) {
+            constexpr bool SILU = decltype(silu)::value;
+            if (back)
+                return pass == 0 ? launch_early(maps_grad_sums_kernel<T, VEC, SILU>, grid, kThreads, s, a, sp)
+                                 : launch_early_shared(maps_grad_kernel<T, VEC, SILU>, grid, kThreads, stat_bytes(a, sp), s, a, sp);
+            return pass == 0 ? launch_early(maps_sums_kernel<T, VEC>, grid, kThreads, s, a, sp)
+                             : launch_early_shared(maps_apply_kernel<T, VEC, SILU>, grid, kThreads, stat_bytes(a, sp), s, a, sp);
+        };
+        return a.silu ? by_act(std::true_type()) : by_act(std::false_type());
     });
 }
 
