@@ -171,14 +171,18 @@ __device__ __forceinline__ float3 join_parts(int many, int team, F part)
     return make_float3(n, mean, team_sum(sq, team));
 }
 
-// Sum of two values over the lanes of a group: L lanes of a warp, or L / 32 warps by way of shared memory.
+// Sums over the lanes of a group: L lanes of a warp, or L / 32 warps by way of shared memory.
+__device__ __forceinline__ void lanes_sum(float &v, int L)
+{
+#pragma unroll
+    for (int m = 16; m; m /= 2)
+        if (m < L)
+            v += __shfl_xor_sync(~0u, v, m);
+}
 __device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
 {
-    const int in = L < 32 ? L : 32;
-    for (int m = in / 2; m; m /= 2) {
-        v.x += __shfl_xor_sync(~0u, v.x, m);
-        v.y += __shfl_xor_sync(~0u, v.y, m);
-    }
+    lanes_sum(v.x, L);
+    lanes_sum(v.y, L);
     if (L > 32) {
         const int warp = threadIdx.x / 32, first = warp & ~(L / 32 - 1);
         __syncthreads();
@@ -193,6 +197,13 @@ __device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
     }
     return v;
 }
+__device__ __forceinline__ float group_sum(float v, int L, float2 *part)
+{
+    if (L > 32)
+        return group_sum(make_float2(v, 0.f), L, part).x;
+    lanes_sum(v, L);
+    return v;
+}
 
 // ---------------------------------------------------------------------------------------------------------
 // Tokens: one position a sample.  Unit u is group u % G of sample u / G; a CTA holds kThreads / L units, and the grid's
@@ -200,7 +211,7 @@ __device__ __forceinline__ float2 group_sum(float2 v, int L, float2 *part)
 // ---------------------------------------------------------------------------------------------------------
 // UNITS: of a lane's group at a time, so that enough loads are under way.
 template <typename T, int VEC, int NV, int UNITS, bool SILU>
-__global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L)
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) tokens_kernel(GroupNormArgs a, int L)
 {
     __shared__ float2 part[kThreads / 32];
     tc::grid_dep_wait();
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
         ask(u + UNITS * stride);
 #pragma unroll
         for (int k = 0; k < UNITS; ++k)
-            mean[k] = group_sum(make_float2(mean[k], 0.f), L, part).x * inv;
+            mean[k] = group_sum(mean[k], L, part) * inv;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             rstd[k] = 0.f;
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(GroupNormArgs a, int L
         }
 #pragma unroll
         for (int k = 0; k < UNITS; ++k)
-            rstd[k] = rsqrtf(fmaf(group_sum(make_float2(rstd[k], 0.f), L, part).x, inv, a.eps));
+            rstd[k] = rsqrtf(fmaf(group_sum(rstd[k], L, part), inv, a.eps));
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             const int64_t at = u + k * stride;
@@ -329,56 +340,74 @@ __global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, 
             dw[i][e] = db[i][e] = 0.f;
         }
     }
-    auto ask = [&](const void *p, int64_t u, V (&r)[NV]) {
+    // what is not there counts as zeros: then nothing of it reaches a sum
+    V next[NV], next_dy[NV];
+    float2 next_stat;
+    auto ask = [&](int64_t u) {
+        const bool live = u < units;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on[i] && u < units)
-                r[i] = *reinterpret_cast<const V *>(static_cast<const T *>(p) + u * W + (lane + L * i) * VEC);
+        for (int i = 0; i < NV; ++i) {
+            const int64_t at = u * W + (lane + L * i) * VEC;
+            next[i] = live && on[i] ? *reinterpret_cast<const V *>(static_cast<const T *>(a.x) + at) : V{};
+            next_dy[i] = live && on[i] ? *reinterpret_cast<const V *>(static_cast<const T *>(a.dy) + at) : V{};
+        }
+        next_stat = live ? make_float2(a.mean_in[u], a.rstd_in[u]) : make_float2(0.f, 0.f);
     };
-    V next[NV] = {}, next_dy[NV] = {};
-    ask(a.x, u0, next);
-    ask(a.dy, u0, next_dy);
+    ask(u0);
     // all of a CTA's units take the same turns, as they may share its barriers
     for (int64_t base = (int64_t)blockIdx.x * per; base < units; base += stride) {
         const int64_t u = base + threadIdx.x / L;
-        const bool live = u < units;
         V x[NV], dy[NV];
+        const float2 stat = next_stat;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             x[i] = next[i];
             dy[i] = next_dy[i];
         }
-        ask(a.x, u + stride, next);
-        ask(a.dy, u + stride, next_dy);
-        const float mean = live ? a.mean_in[u] : 0.f, rstd = live ? a.rstd_in[u] : 0.f;
-        float xh[NV][VEC], g[NV][VEC];
+        ask(u + stride);
+        float xh[NV][VEC], g[NV][VEC], minus[VEC], rstd[VEC], s1[VEC] = {}, s2[VEC] = {}, zero[VEC] = {};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            minus[e] = -stat.x, rstd[e] = stat.y;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float dz[VEC];
+            widened(x[i], xh[i]);
+            widened(dy[i], dz);
+            add_to(xh[i], minus);
+            fma_all(xh[i], xh[i], rstd, zero);
+            if constexpr (SILU) {
+                float z[VEC];
+                fma_all(z, xh[i], w[i], b[i]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    dz[e] = before_act<SILU>(dz[e], z[e]);
+            }
+            add_to(db[i], dz);
+            fma_all(dw[i], dz, xh[i], dw[i]);
+            fma_all(g[i], dz, w[i], zero);
+            add_to(s1, g[i]);
+            fma_all(s2, g[i], xh[i], s2);
+        }
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (!on[i] || !live)
-                    continue;
-                const float n = (widen(x[i].v[e]) - mean) * rstd;
-                const float dz = before_act<SILU>(widen(dy[i].v[e]), fmaf(n, w[i][e], b[i][e]));
-                db[i][e] += dz;
-                dw[i][e] = fmaf(dz, n, dw[i][e]);
-                xh[i][e] = n;
-                g[i][e] = dz * w[i][e];
-                sum = make_float2(sum.x + g[i][e], fmaf(g[i][e], n, sum.y));
-            }
+        for (int e = 0; e < VEC; ++e)
+            sum = make_float2(sum.x + s1[e], sum.y + s2[e]);
         sum = group_sum(sum, L, part);
-        if (!live)
+        if (u >= units)
             continue;
+        float m1[VEC], m2[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            m1[e] = -inv * sum.x, m2[e] = -inv * sum.y;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!on[i])
                 continue;
-            V dx;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                dx.v[e] = narrow<T>(rstd * (g[i][e] - inv * fmaf(xh[i][e], sum.y, sum.x)));
-            *reinterpret_cast<V *>(static_cast<T *>(a.dx) + u * W + (lane + L * i) * VEC) = dx;
+            add_to(g[i], m1);
+            fma_all(g[i], xh[i], m2, g[i]);
+            fma_all(g[i], g[i], rstd, zero);
+            *reinterpret_cast<V *>(static_cast<T *>(a.dx) + u * W + (lane + L * i) * VEC) = narrowed<T, VEC>(g[i]);
         }
     }
     if (!a.part_dw)
@@ -398,20 +427,28 @@ __global__ void __launch_bounds__(kThreads) tokens_grad_kernel(GroupNormArgs a, 
 // Maps.  CTA (sample, slice of positions, chunk of channels): TX threads on adjacent vectors, TY rows at a time.
 // ---------------------------------------------------------------------------------------------------------
 struct Slice {
-    int64_t n, row0, rows;     // sample, first position and positions
+    int64_t n, at;             // sample, and first value of this thread's first row of the slice
+    int rows;                  // positions
     int slice, chunk, c0, cc;  // channels [c0, c0 + cc)
+    int tx, ty;                // this thread's vector and first row
+    bool on;
 };
+template <int VEC>
 __device__ __forceinline__ Slice slice_of(const GroupNormArgs &a, const GroupNormSplit &s)
 {
     Slice r;
-    r.chunk = blockIdx.x % s.chunks;
-    const int64_t i = blockIdx.x / s.chunks;
-    r.slice = (int)(i % s.slices);
-    r.n = i / s.slices;
-    r.row0 = r.slice * s.rows;
-    r.rows = min(s.rows, a.S - r.row0);
+    const unsigned i = blockIdx.x / s.chunks, n = i / s.slices;
+    r.chunk = blockIdx.x - i * s.chunks;
+    r.slice = i - n * s.slices;
+    r.n = n;
+    const int64_t row0 = (int64_t)r.slice * s.rows;
+    r.rows = (int)min((int64_t)s.rows, a.S - row0);
     r.c0 = r.chunk * s.chunk;
     r.cc = min(s.chunk, a.C - r.c0);
+    r.ty = threadIdx.x / s.tx;
+    r.tx = threadIdx.x - r.ty * s.tx;
+    r.on = r.ty < s.ty && r.tx * VEC < r.cc;
+    r.at = (r.n * a.S + row0 + r.ty) * a.C + r.c0 + r.tx * VEC;
     return r;
 }
 
@@ -420,26 +457,27 @@ __global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, Gr
 {
     __shared__ float2 held[kThreads * VEC];
     tc::grid_dep_wait();
-    const Slice s = slice_of(a, sp);
-    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
-    const bool on = ty < sp.ty && tx * VEC < s.cc;
+    const Slice s = slice_of<VEC>(a, sp);
+    const int64_t step = (int64_t)sp.ty * a.C;   // between a thread's rows
     typedef Vec<T, VEC> V;
-    const T *x = static_cast<const T *>(a.x) + (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
-    auto rows_of = [&](int y) { return y < s.rows ? (float)((s.rows - y + sp.ty - 1) / sp.ty) : 0.f; };
+    const T *x = static_cast<const T *>(a.x) + s.at;
+    const int turns = s.rows / sp.ty, more = s.rows - turns * sp.ty;   // rows of a thread: one more of the first
+    auto rows_of = [&](int y) { return (float)(turns + (y < more)); };
     const bool whole = a.W % VEC == 0;   // a vector's channels are of one group
-    if (on) {
-        const float many = rows_of(ty), inv = many > 0.f ? 1.f / many : 0.f;
+    if (s.on) {
+        const float many = rows_of(s.ty), inv = many > 0.f ? 1.f / many : 0.f;
         float mean[VEC] = {}, m2[VEC] = {};
         if (many > 0.f) {
             float minus[VEC], s1[VEC] = {}, s2[VEC] = {};
-            widened(*reinterpret_cast<const V *>(x + (int64_t)ty * a.C), minus);
+            widened(*reinterpret_cast<const V *>(x), minus);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 minus[e] = -minus[e];
 #pragma unroll 4
-            for (int64_t r = ty + sp.ty; r < s.rows; r += sp.ty) {
+            for (int r = s.ty + sp.ty; r < s.rows; r += sp.ty) {
                 float d[VEC];
-                widened(*reinterpret_cast<const V *>(x + r * a.C), d);
+                x += step;
+                widened(*reinterpret_cast<const V *>(x), d);
                 add_to(d, minus);
                 add_to(s1, d);
                 fma_all(s2, d, d, s2);
@@ -460,11 +498,11 @@ __global__ void __launch_bounds__(kThreads) maps_sums_kernel(GroupNormArgs a, Gr
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 sq += fmaf(many * (mean[e] - at), mean[e] - at, m2[e]);
-            held[ty * sp.tx + tx] = make_float2(at, sq);
+            held[s.ty * sp.tx + s.tx] = make_float2(at, sq);
         } else {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                held[ty * sp.chunk + tx * VEC + e] = make_float2(mean[e], m2[e]);
+                held[s.ty * sp.chunk + s.tx * VEC + e] = make_float2(mean[e], m2[e]);
         }
     }
     __syncthreads();
@@ -511,36 +549,61 @@ __device__ __forceinline__ void join_slices(const GroupNormArgs &a, const GroupN
 template <typename T, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads) maps_apply_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
+    constexpr int kAhead = 4;
     extern __shared__ float2 stat[];
     tc::grid_dep_wait();
-    const Slice s = slice_of(a, sp);
+    const Slice s = slice_of<VEC>(a, sp);
+    const int64_t step = (int64_t)sp.ty * a.C;   // between a thread's rows
+    const int g0 = s.c0 / a.W;
+    typedef Vec<T, VEC> V;
+    const T *x = static_cast<const T *>(a.x) + s.at;
+    T *y = static_cast<T *>(a.y) + s.at;
+    V next[kAhead] = {};
+    auto ask = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s.on && r + k * sp.ty < s.rows)
+                next[k] = *reinterpret_cast<const V *>(x);
+            x += step;
+        }
+    };
+    ask(s.ty);   // while the statistics are joined
     join_slices(a, sp, s, stat);
-    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx, g0 = s.c0 / a.W;
-    if (ty >= sp.ty || tx * VEC >= s.cc)
+    if (!s.on)
         return;
     float minus[VEC], f[VEC], b[VEC];
+    const bool whole = a.W % VEC == 0;
+    int g = (s.c0 + s.tx * VEC) / a.W - g0;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const int c = s.c0 + tx * VEC + e;
-        const float2 st = stat[c / a.W - g0];
+        const int c = s.c0 + s.tx * VEC + e;
+        if (!whole)
+            g = c / a.W - g0;
+        const float2 st = stat[g];
         minus[e] = -st.x;
         f[e] = a.w ? st.y * a.w[c] : st.y;
         b[e] = a.b ? a.b[c] : 0.f;
     }
-    typedef Vec<T, VEC> V;
-    const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
-    const T *x = static_cast<const T *>(a.x) + at;
-    T *y = static_cast<T *>(a.y) + at;
-#pragma unroll 4
-    for (int64_t r = ty; r < s.rows; r += sp.ty) {
-        float v[VEC];
-        widened(*reinterpret_cast<const V *>(x + r * a.C), v);
-        add_to(v, minus);
-        fma_all(v, v, f, b);
+    for (int r = s.ty; r < s.rows; r += kAhead * sp.ty) {
+        V now[kAhead];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            v[e] = activated<SILU>(v[e]);
-        *reinterpret_cast<V *>(y + r * a.C) = narrowed<T, VEC>(v);
+        for (int k = 0; k < kAhead; ++k)
+            now[k] = next[k];
+        ask(r + kAhead * sp.ty);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (r + k * sp.ty >= s.rows)
+                break;
+            float v[VEC];
+            widened(now[k], v);
+            add_to(v, minus);
+            fma_all(v, v, f, b);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                v[e] = activated<SILU>(v[e]);
+            *reinterpret_cast<V *>(y) = narrowed<T, VEC>(v);
+            y += step;
+        }
     }
 }
 
@@ -550,27 +613,30 @@ __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs 
 {
     __shared__ float2 held[kThreads * VEC];
     tc::grid_dep_wait();
-    const Slice s = slice_of(a, sp);
-    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
-    if (ty < sp.ty && tx * VEC < s.cc) {
+    const Slice s = slice_of<VEC>(a, sp);
+    const int64_t step = (int64_t)sp.ty * a.C;   // between a thread's rows
+    if (s.on) {
         float minus[VEC], rstd[VEC], w[VEC], b[VEC], zero[VEC] = {}, sum_z[VEC] = {}, sum_zn[VEC] = {};
+        const bool whole = a.W % VEC == 0;
+        int64_t g = s.n * a.G + (s.c0 + s.tx * VEC) / a.W;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const int c = s.c0 + tx * VEC + e;
-            const int64_t g = s.n * a.G + c / a.W;
+            const int c = s.c0 + s.tx * VEC + e;
+            if (!whole)
+                g = s.n * a.G + c / a.W;
             minus[e] = -a.mean_in[g];
             rstd[e] = a.rstd_in[g];
             w[e] = a.w ? a.w[c] : 1.f;
             b[e] = a.b ? a.b[c] : 0.f;
         }
         typedef Vec<T, VEC> V;
-        const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
-        const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
+        const T *x = static_cast<const T *>(a.x) + s.at, *dy = static_cast<const T *>(a.dy) + s.at;
 #pragma unroll 4
-        for (int64_t r = ty; r < s.rows; r += sp.ty) {
+        for (int r = s.ty; r < s.rows; r += sp.ty) {
             float n[VEC], dz[VEC];
-            widened(*reinterpret_cast<const V *>(x + r * a.C), n);
-            widened(*reinterpret_cast<const V *>(dy + r * a.C), dz);
+            widened(*reinterpret_cast<const V *>(x), n);
+            widened(*reinterpret_cast<const V *>(dy), dz);
+            x += step, dy += step;
             add_to(n, minus);
             fma_all(n, n, rstd, zero);
             if constexpr (SILU) {
@@ -585,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs 
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            held[ty * sp.chunk + tx * VEC + e] = make_float2(sum_z[e], sum_zn[e]);
+            held[s.ty * sp.chunk + s.tx * VEC + e] = make_float2(sum_z[e], sum_zn[e]);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < s.cc; c += kThreads) {
@@ -620,9 +686,26 @@ __global__ void __launch_bounds__(kThreads) maps_grad_sums_kernel(GroupNormArgs 
 template <typename T, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, GroupNormSplit sp)
 {
+    constexpr int kAhead = VEC == 8 ? 2 : 4;
     extern __shared__ float2 stat[];
     tc::grid_dep_wait();
-    const Slice s = slice_of(a, sp);
+    const Slice s = slice_of<VEC>(a, sp);
+    const int64_t step = (int64_t)sp.ty * a.C;   // between a thread's rows
+    typedef Vec<T, VEC> V;
+    const T *x = static_cast<const T *>(a.x) + s.at, *dy = static_cast<const T *>(a.dy) + s.at;
+    T *dx = static_cast<T *>(a.dx) + s.at;
+    V next[kAhead] = {}, next_dy[kAhead] = {};
+    auto ask = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s.on && r + k * sp.ty < s.rows) {
+                next[k] = *reinterpret_cast<const V *>(x);
+                next_dy[k] = *reinterpret_cast<const V *>(dy);
+            }
+            x += step, dy += step;
+        }
+    };
+    ask(s.ty);   // while the sums are joined
     const int g0 = s.c0 / a.W, groups = (s.c0 + s.cc - 1) / a.W - g0 + 1, team = team_of(groups);
     const float inv = 1.f / ((float)a.W * (float)a.S);
     for (int first = 0; first < groups; first += kThreads / team) {
@@ -641,43 +724,52 @@ __global__ void __launch_bounds__(kThreads) maps_grad_kernel(GroupNormArgs a, Gr
             stat[at] = make_float2(t.x * inv, t.y * inv);
     }
     __syncthreads();
-    const int tx = threadIdx.x % sp.tx, ty = threadIdx.x / sp.tx;
-    if (ty >= sp.ty || tx * VEC >= s.cc)
+    if (!s.on)
         return;
     float minus[VEC], rstd[VEC], w[VEC], b[VEC], m1[VEC], m2[VEC], zero[VEC] = {};
+    const bool whole = a.W % VEC == 0;
+    int in = (s.c0 + s.tx * VEC) / a.W;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const int c = s.c0 + tx * VEC + e;
-        const int64_t g = s.n * a.G + c / a.W;
-        const float2 st = stat[c / a.W - g0];
+        const int c = s.c0 + s.tx * VEC + e;
+        if (!whole)
+            in = c / a.W;
+        const int64_t g = s.n * a.G + in;
+        const float2 st = stat[in - g0];
         m1[e] = -st.x, m2[e] = -st.y;
         minus[e] = -a.mean_in[g];
         rstd[e] = a.rstd_in[g];
         w[e] = a.w ? a.w[c] : 1.f;
         b[e] = a.b ? a.b[c] : 0.f;
     }
-    typedef Vec<T, VEC> V;
-    const int64_t at = (s.n * a.S + s.row0) * a.C + s.c0 + tx * VEC;
-    const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
-    T *dx = static_cast<T *>(a.dx) + at;
-#pragma unroll 2
-    for (int64_t r = ty; r < s.rows; r += sp.ty) {
-        float n[VEC], dz[VEC], o[VEC];
-        widened(*reinterpret_cast<const V *>(x + r * a.C), n);
-        widened(*reinterpret_cast<const V *>(dy + r * a.C), dz);
-        add_to(n, minus);
-        fma_all(n, n, rstd, zero);
-        if constexpr (SILU) {
-            float z[VEC];
-            fma_all(z, n, w, b);
+    for (int r = s.ty; r < s.rows; r += kAhead * sp.ty) {
+        V now[kAhead], now_dy[kAhead];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                dz[e] = before_act<SILU>(dz[e], z[e]);
+        for (int k = 0; k < kAhead; ++k)
+            now[k] = next[k], now_dy[k] = next_dy[k];
+        ask(r + kAhead * sp.ty);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (r + k * sp.ty >= s.rows)
+                break;
+            float n[VEC], dz[VEC], o[VEC];
+            widened(now[k], n);
+            widened(now_dy[k], dz);
+            add_to(n, minus);
+            fma_all(n, n, rstd, zero);
+            if constexpr (SILU) {
+                float z[VEC];
+                fma_all(z, n, w, b);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    dz[e] = before_act<SILU>(dz[e], z[e]);
+            }
+            fma_all(o, w, dz, m1);
+            fma_all(o, n, m2, o);
+            fma_all(o, o, rstd, zero);
+            *reinterpret_cast<V *>(dx) = narrowed<T, VEC>(o);
+            dx += step;
         }
-        fma_all(o, w, dz, m1);
-        fma_all(o, n, m2, o);
-        fma_all(o, o, rstd, zero);
-        *reinterpret_cast<V *>(dx + r * a.C) = narrowed<T, VEC>(o);
     }
 }
 
@@ -733,7 +825,7 @@ int64_t group_norm_token_ctas(const GroupNormArgs &a, int dtype, bool back)
     int L, nv;
     lanes_of(a.W, vec_of(a, dtype, true), L, nv);
     const int64_t per = kThreads / L, q = a.G / std::gcd((int64_t)a.G, per), need = (a.N * a.G + per - 1) / per;
-    const int64_t cap = (int64_t)sm_count() * (back ? 3 : 6);
+    const int64_t cap = (int64_t)sm_count() * (back ? 3 : 4);
     return std::max<int64_t>(1, std::min((need + q - 1) / q, std::max<int64_t>(cap / q, 1))) * q;
 }
 
@@ -744,8 +836,8 @@ int64_t group_norm_token_parts(const GroupNormArgs &a, int dtype)   // rows of C
     return group_norm_token_ctas(a, dtype, true) * (kThreads / L) / a.G;
 }
 
-// Enough slices that the CTAs fill the GPU four times (two CTAs an SM at least stay busy to the end), as long as each has
-// 16 turns of rows, or as many as there are SMs with four turns.
+// Enough slices for two CTAs an SM (8 x 4096 x 512 in bf16, both kernels: 22.4 us; three 25.7, four 30, one 26: a CTA's start
+// and its joins take about 3 us), as long as each has 16 turns of rows, or as many as there are SMs with four turns.
 GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
 {
     const int vec = vec_of(a, dtype, false), vectors = a.C / vec;
@@ -755,12 +847,13 @@ GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
     s.tx = s.chunk / vec;
     s.ty = kThreads / s.tx;
     s.entries = a.G + s.chunks - 1;
-    const int64_t want = std::max<int64_t>(1, (4 * (int64_t)sm_count()) / std::max<int64_t>(1, a.N * s.chunks));
+    const int64_t want = std::max<int64_t>(1, (2 * (int64_t)sm_count()) / std::max<int64_t>(1, a.N * s.chunks));
     const int64_t most = std::max<int64_t>(1, a.S / (16 * s.ty));
     const int64_t least = std::min<int64_t>(std::max<int64_t>(1, a.S / (4 * s.ty)), std::max<int64_t>(1, sm_count() / std::max<int64_t>(1, a.N * s.chunks)));
     const int64_t slices = std::max(least, std::min(want, most));
-    s.rows = (a.S + slices - 1) / slices;
-    s.slices = (int)((a.S + s.rows - 1) / s.rows);
+    const int64_t rows = std::min<int64_t>((a.S + slices - 1) / slices, 1 << 30);
+    s.rows = (int)rows;
+    s.slices = (int)((a.S + rows - 1) / rows);
     return s;
 }
 

@@ -23,8 +23,7 @@ struct GroupNormArgs {
 
 // How the maps' kernels cut a tensor.
 struct GroupNormSplit {
-    int64_t rows;                      // positions of a slice
-    int slices, chunk, chunks;         // slices of a sample, channels of a chunk, chunks
+    int rows, slices, chunk, chunks;   // positions of a slice, slices of a sample, channels of a chunk, chunks
     int tx, ty;                        // threads of a row, rows at a time
     int64_t entries;                   // partial results of a slice: its groups, and one more for each further chunk
 };
