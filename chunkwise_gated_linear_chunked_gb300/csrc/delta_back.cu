@@ -21,11 +21,13 @@ namespace {
 template <typename T, int KD, int VG>
 __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __grid_constant__ ChainMaps maps, DeltaArgs a, int tiles)
 {
-    typedef ChainShared<KD, VG, 2> Shared;
+    typedef ChainShared<KD, VG, 2, DeltaCellRows> Shared;
     constexpr int kThreads = 64 * VG;
     extern __shared__ __align__(1024) char raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     ChainWalk w;
+    bars_init(sh.full);
+    tc::grid_dep_wait();
     if (!chain_walk(a, tiles, 16 * VG, w))
         return;
     const int tid = threadIdx.x, lane = tid % 32, group = tid / 32 % VG;
@@ -35,7 +37,6 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
     const size_t state = (w.head * a.K + two) * a.V;
     const DeltaTrace trace = a.trace;
     const int g16 = (w.v0 >> 4) + group;
-    bars_init(sh.full);
 
     auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4]) {
         const float4 *row = st.cell.row;
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
         }
     };
 
-    constexpr size_t kCell = sizeof(DeltaCellBack), kTriangles = sizeof(DeltaCell);
+    constexpr size_t kCell = sizeof(DeltaCellBack);
     auto walk = [&](auto work) {
         if (tid == kThreads / 2 && w.chunks)
-            ask_chunk(a, maps, w, sh, w.chunks - 1, 0, kCell, kTriangles);
+            ask_chunk(a, maps, w, sh, w.chunks - 1, 0, kCell, kCellRows);
         for (int turn = 0; turn < w.chunks; ++turn) {
             const int c = w.chunks - 1 - turn;
             const bool ok = tc::bar_wait(&sh.full[turn & 1], (turn >> 1) & 1);
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 return;
             }
             if (tid == kThreads / 2 && c > 0)
-                ask_chunk(a, maps, w, sh, c - 1, turn + 1, kCell, kTriangles);
+                ask_chunk(a, maps, w, sh, c - 1, turn + 1, kCell, kCellRows);
             if (w.len - c * kDeltaChunk < kDeltaChunk) {
                 clear_tail<VG>(sh.stage[turn & 1], w.len - c * kDeltaChunk);
                 __syncthreads();
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kDeltaChunk *kDeltaKept) delta_chunk_gates_ker
 {
     constexpr int kRows = kDeltaChunk * kDeltaKept;
     __shared__ float part[kRows / 32];
+    tc::grid_dep_wait();
     const int group = blockIdx.x / a.HV, hv = blockIdx.x - group * a.HV, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     int lo = 0, hi = a.N - 1;   // the last sequence whose groups start at or before this one
     while (lo < hi) {
@@ -314,7 +316,7 @@ cudaError_t launch_delta_chain_back(const DeltaArgs &a, bool half, cudaStream_t 
     auto go = [&](auto t, auto kd, auto vg) {
         typedef std::remove_pointer_t<decltype(t)> T;
         constexpr int KD = decltype(kd)::value, VG = decltype(vg)::value;
-        return launch_chain(delta_chain_back_kernel<T, KD, VG>, sizeof(ChainShared<KD, VG, 2>), VG, half, a, s);
+        return launch_chain(delta_chain_back_kernel<T, KD, VG>, sizeof(ChainShared<KD, VG, 2, DeltaCellRows>), VG, half, a, s);
     };
     auto by_keys = [&](auto t, auto vg) { return a.K == 128 ? go(t, Int<128>(), vg) : go(t, Int<64>(), vg); };
     auto by_type = [&](auto vg) { return half ? by_keys((__half *)0, vg) : by_keys((__nv_bfloat16 *)0, vg); };
@@ -325,8 +327,7 @@ cudaError_t launch_delta_chunk_gates(const DeltaArgs &a, cudaStream_t s)
 {
     constexpr int kRows = kDeltaChunk * kDeltaKept;
     const int groups = a.cu ? a.T / kRows + a.N : a.B * ((a.T + kRows - 1) / kRows);
-    delta_chunk_gates_kernel<<<(unsigned)((size_t)groups * a.HV), kRows, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(delta_chunk_gates_kernel, (unsigned)((size_t)groups * a.HV), kRows, s, a);
 }
 
 }  // namespace gla

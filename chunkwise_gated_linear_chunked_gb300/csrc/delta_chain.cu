@@ -28,12 +28,14 @@ namespace {
 template <typename T, typename To, int KD, int VG, bool SAVE>
 __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_constant__ ChainMaps maps, DeltaArgs a, int tiles)
 {
-    typedef ChainShared<KD, VG, SAVE ? 2 : 1> Shared;
+    typedef ChainShared<KD, VG, SAVE ? 2 : 1, DeltaCell> Shared;
     constexpr int kThreads = 64 * VG;
     constexpr size_t kCell = SAVE ? sizeof(DeltaCellBack) : sizeof(DeltaCell);
     extern __shared__ __align__(1024) char raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     ChainWalk w;
+    bars_init(sh.full);
+    tc::grid_dep_wait();
     if (!chain_walk(a, tiles, 16 * VG, w))
         return;
     const int tid = threadIdx.x, lane = tid % 32, group = tid / 32 % VG;
@@ -41,7 +43,6 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     const int col = w.v0 + 16 * group + lane / 4, two = 2 * (lane % 4);
     const bool on = w.v0 + 16 * group < a.V;   // whole groups of 16 columns
     const size_t state = (w.head * a.K + two) * a.V;
-    bars_init(sh.full);
 
     auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4]) {
         const float4 *row = st.cell.row;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     // the warps of a role go their own ways through a chunk and meet at its end
     auto walk = [&](auto work) {
         if (tid == kThreads / 2 && w.chunks)
-            ask_chunk(a, maps, w, sh, 0, 0, kCell, sizeof(float4) * kDeltaChunk);
+            ask_chunk(a, maps, w, sh, 0, 0, kCell, 0);
         for (int c = 0; c < w.chunks; ++c) {
             const bool ok = tc::bar_wait(&sh.full[c & 1], (c >> 1) & 1);
             if (__syncthreads_or(!ok)) {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 return;
             }
             if (tid == kThreads / 2 && c + 1 < w.chunks)
-                ask_chunk(a, maps, w, sh, c + 1, c + 1, kCell, sizeof(float4) * kDeltaChunk);
+                ask_chunk(a, maps, w, sh, c + 1, c + 1, kCell, 0);
             if (w.len - c * kDeltaChunk < kDeltaChunk) {
                 clear_tail<VG>(sh.stage[c & 1], w.len - c * kDeltaChunk);
                 __syncthreads();
@@ -248,9 +249,9 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, int dtype, bool save, cudaStr
                 constexpr int KD = decltype(kd)::value, VG = decltype(vg)::value;
                 constexpr bool kHalf = std::is_same_v<T, __half>;
                 if (!save)
-                    return launch_chain(delta_chain_kernel<T, To, KD, VG, false>, sizeof(ChainShared<KD, VG, 1>), VG, kHalf, a, s);
+                    return launch_chain(delta_chain_kernel<T, To, KD, VG, false>, sizeof(ChainShared<KD, VG, 1, DeltaCell>), VG, kHalf, a, s);
                 if constexpr (std::is_same_v<To, float>)   // the gradients' pass has no output of another type
-                    return launch_chain(delta_chain_kernel<T, float, KD, VG, true>, sizeof(ChainShared<KD, VG, 2>), VG, kHalf, a, s);
+                    return launch_chain(delta_chain_kernel<T, float, KD, VG, true>, sizeof(ChainShared<KD, VG, 2, DeltaCell>), VG, kHalf, a, s);
                 else
                     return cudaErrorInvalidValue;
             };

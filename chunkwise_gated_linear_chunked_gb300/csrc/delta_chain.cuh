@@ -13,11 +13,11 @@
 namespace gla {
 
 // Shared memory of a CTA of VG groups of 16 columns; ROWS: matrices of 64 rows of values (v, and dO for the gradients).
-template <int KD, int VG, int ROWS>
+template <int KD, int VG, int ROWS, typename Cell>
 struct ChainShared {
     struct Stage {
         uint16_t k[KD / 64][64][64], q[KD / 64][64][64], v[ROWS][64][16 * VG];   // as the tensor copies swizzle them
-        DeltaCell cell;   // row, and the two triangles that this direction takes
+        Cell cell;
     } stage[2];
     static_assert(sizeof(Stage) % 1024 == 0, "swizzled tiles start on 1024 bytes");
     uint4 state[VG][KD / 16][2][32];     // the chain's rounded S and its remainders, as left operands
@@ -231,11 +231,11 @@ struct ChainMaps {
     CUtensorMap q, k, v, d;
 };
 
-// Asks for a chunk's rows, and the cell's rows and two triangles from `tri` bytes on (one thread; a bulk copy for each row
-// took 3400 cycles a chunk to issue, 16-byte copies by all threads 2300 and slowed the loads of the chain).
-template <int KD, int VG, int ROWS>
-__device__ __forceinline__ void ask_chunk(const DeltaArgs &a, const ChainMaps &maps, const ChainWalk &w, ChainShared<KD, VG, ROWS> &sh, int c, int turn,
-                                          size_t cell_bytes, size_t tri)
+// Asks for a chunk's rows, and for its cell from `from` bytes on (one thread; a bulk copy for each row took 3400 cycles a
+// chunk to issue, 16-byte copies by all threads 2300 and slowed the loads of the chain).
+template <int KD, int VG, int ROWS, typename Cell>
+__device__ __forceinline__ void ask_chunk(const DeltaArgs &a, const ChainMaps &maps, const ChainWalk &w, ChainShared<KD, VG, ROWS, Cell> &sh, int c,
+                                          int turn, size_t cell_bytes, size_t from)
 {
     auto &st = sh.stage[turn & 1];
     uint64_t *bar = &sh.full[turn & 1];
@@ -246,9 +246,7 @@ __device__ __forceinline__ void ask_chunk(const DeltaArgs &a, const ChainMaps &m
         tc::tma_load_3d(st.k[i], &maps.k, 64 * i, w.hk, row, bar);
         tc::tma_load_3d(st.q[i], &maps.q, 64 * i, w.hk, row, bar);
     }
-    const char *cell = a.chunk + ((size_t)(w.slot + c) * a.HV + w.hv) * cell_bytes;
-    copy_bulk(st.cell.row, cell, sizeof st.cell.row, bar);
-    copy_bulk(st.cell.inverse, cell + tri, sizeof st.cell.inverse + sizeof st.cell.score, bar);
+    copy_bulk(&st.cell, a.chunk + ((size_t)(w.slot + c) * a.HV + w.hv) * cell_bytes + from, sizeof st.cell, bar);
     tc::tma_load_3d(st.v[0], &maps.v, w.v0, w.hv, row, bar);
     if constexpr (ROWS > 1)
         tc::tma_load_3d(st.v[1], &maps.d, w.v0, w.hv, row, bar);
@@ -319,8 +317,7 @@ cudaError_t launch_chain(F kernel, size_t shared, int groups, bool half, const D
     if (e != cudaSuccess)
         return e;
     const int tiles = (a.V + 16 * groups - 1) / (16 * groups);
-    kernel<<<(unsigned)((size_t)a.N * a.HV * tiles), 64 * groups, shared, s>>>(maps, a, tiles);
-    return cudaGetLastError();
+    return launch_early_shared(kernel, (unsigned)((size_t)a.N * a.HV * tiles), 64 * groups, shared, s, maps, a, tiles);
 }
 
 // Whether CTAs of 32 columns have an SM each.

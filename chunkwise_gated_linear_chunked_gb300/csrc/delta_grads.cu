@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid % 32, r = tid / 32 % 4, h = tid / 128, two = 2 * (lane % 4), i0 = 16 * r + lane / 4;
     const int per = a.HV / a.H;
     bars_init(sh.full);
+    tc::grid_dep_wait();
     auto ask = [&](const GradPiece &p) {
         auto &st = sh.stage[p.turn & 1];
         uint64_t *bar = &sh.full[p.turn & 1];
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
             }
         const size_t cell = (size_t)p.slot * a.HV + hv;
         const char *from = a.chunk + cell * sizeof(DeltaCellBack);
-        copy_bulk(st.row, from, sizeof st.row, bar);
+        copy_bulk(st.row, from + kCellRows, sizeof st.row, bar);
         copy_bulk(st.gate, from + sizeof(DeltaCellBack) - sizeof st.gate, sizeof st.gate, bar);
         tc::tma_load_3d(st.d, &maps.d, 64 * p.c, hv, p.first, bar);
         const size_t narrow_at = cell * a.trace.n_size + (size_t)p.c * 8 * 8 * 32, wide_at = cell * a.trace.s_size + (size_t)p.c * 8 * (KD / 8) * 32;
@@ -271,8 +272,7 @@ cudaError_t launch_delta_grads(const DeltaArgs &a, bool half, int sms, cudaStrea
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess)
             return e;
-        kernel<<<(unsigned)std::min<int64_t>((int64_t)a.slots * a.H, sms), kThreads, shared, s>>>(maps, a);
-        return cudaGetLastError();
+        return launch_early_shared(kernel, (unsigned)std::min<int64_t>((int64_t)a.slots * a.H, sms), kThreads, shared, s, maps, a);
     };
     auto by_keys = [&](auto t) {
         typedef std::remove_pointer_t<decltype(t)> T;

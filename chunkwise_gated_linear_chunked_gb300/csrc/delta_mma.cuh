@@ -18,15 +18,20 @@ namespace gla {
 // two of the remainders.  Result tile j (rows 8 j up) takes steps i (columns 16 i up) with 16 i <= 8 j + 7: 20 in all.
 constexpr int kTriangle = 20, kFragments = kTriangle * 32;
 struct DeltaCell {
-    float4 row[kDeltaChunk];
     uint4 inverse[kFragments];   // T^ = (I + L diag(beta))^-1, L_ij = e^(G_i - G_j) k_i.k_j below the diagonal
     uint4 score[kFragments];     // P_ij = scale e^(G_i - G_j) q_i.k_j up to the diagonal
+    float4 row[kDeltaChunk];
 };
 struct DeltaCellBack : DeltaCell {   // and transposed: rows and columns of the tiles' numbers run from the other end
     uint4 inverse_t[kFragments];     // T' = (I + L' diag(beta))^-1
     uint4 score_t[kFragments];       // P'
     float2 gate[kDeltaChunk];        // G times log2 e in two floats
 };
+struct DeltaCellRows {               // the part of it that the gradients' chain copies, from `row` on
+    float4 row[kDeltaChunk];
+    uint4 inverse[kFragments], score[kFragments];   // T', P'
+};
+constexpr size_t kCellRows = 2 * kFragments * sizeof(uint4);   // where `row` lies in a cell
 __host__ __device__ constexpr int triangle_at(int j, int i) { return (j / 2) * (j / 2 + 1) + (j % 2) * (j / 2 + 1) + i; }
 __host__ __device__ constexpr int triangle_at_t(int j, int i) { return triangle_at(7 - j, 3 - i); }
 

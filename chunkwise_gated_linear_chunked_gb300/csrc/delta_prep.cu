@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
     PrepShared<BACK> &sh = mem.s;
     const int slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     int n, c, first, rows;
+    tc::grid_dep_wait();
     if (!delta_chunk(a, slot, n, c, first, rows))
         return;
     const int per = a.HV / a.H;
@@ -306,8 +307,7 @@ cudaError_t launch_delta_prep(const DeltaArgs &a, bool half, bool backward, cuda
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess)
             return e;
-        kernel<<<(unsigned)((size_t)a.slots * a.H), kThreads, shared, s>>>(a);
-        return cudaGetLastError();
+        return launch_early_shared(kernel, (unsigned)((size_t)a.slots * a.H), kThreads, shared, s, a);
     };
     auto by_back = [&](auto t, auto kd) {
         typedef std::remove_pointer_t<decltype(t)> T;

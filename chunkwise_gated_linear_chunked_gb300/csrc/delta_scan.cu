@@ -10,7 +10,7 @@
 //     dg_t = sum over i >= t of (q.dq - dv.v)_i + <ht, dht>
 //
 // The columns of S and dS do not meet in n and x (delta_cols), nor their rows in dq, e and f (delta_rows), so each CTA
-// walks all tokens for 16 columns (rows) of one head with its part of the state in registers: 16 lanes hold a column,
+// walks all tokens for 8 columns (rows) of one head with its part of the state in registers: 16 lanes hold a column,
 // four adjacent values of every 64 each, so that a warp's loads of a token's vector from shared memory are two lines that
 // its columns share.  Tokens arrive in blocks through registers and two buffers, one block ahead.
 //
@@ -20,13 +20,13 @@
 // the state advances by four at a time.  3 x 1001 tokens, 5 heads of 96 x 80: 264 us token by token, 92 by fours.
 #include <type_traits>
 
+#include "api_common.h"
 #include "delta_internal.h"
-#include "io.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kThreads = 256, kLanes = 16, kTile = kThreads / kLanes;
+constexpr int kThreads = 128, kLanes = 16, kTile = kThreads / kLanes;
 
 // Vectors of four values of a lane, of P values in all; where the lane's i-th starts.
 template <int P>
@@ -126,8 +126,7 @@ struct Four {
 // Columns of the state.  Forward: n, and o where it is asked for; backward: x and dv.
 //     forward:   n_i = b_i (v_i - start_i k_i.S - sum over j < i of l_ij n_j),   o_i = scale start_i q_i.S + sum of m_ij n_j
 //     backward:  x_i = start_i k_i.dS + sum over j <= i of m_ij do_j - sum over j < i of l_ij b_j x_j
-// QUAD: K a multiple of four, rows of keys arrive by fours.
-template <typename Tx, typename To, int P, bool BACK, bool QUAD>
+template <typename Tx, typename To, int P, bool BACK>
 __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int tiles)
 {
     constexpr int kBlock = 2048 / P, kEach = kBlock * P / kThreads, kVals = (kBlock * kTile + kThreads - 1) / kThreads;
@@ -147,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int t
     take<P>(s, start ? start + state : nullptr, a.V, a.K, lane, start && col < a.V);
 
     constexpr int kEachQuads = kEach / 4;
+    const bool quads = a.K % 4 == 0;   // rows of keys arrive by fours
     struct alignas(4 * sizeof(Tx)) Quad {
         Tx v[4];
     };
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int t
     float2 abr;
     auto row_of = [&](int t) { return w.bos + (BACK ? w.len - 1 - t : t); };
     auto fetch = [&](int block) {   // behind the last token: nothing that changes the state
-        if constexpr (QUAD) {
+        if (quads) {
 #pragma unroll
             for (int i = 0; i < kEachQuads; ++i) {
                 const int e = (i * kThreads + tid) * 4, j = e / P, d = e % P, t = block * kBlock + j;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int t
         }
     };
     auto keep = [&](int b) {
-        if constexpr (QUAD) {
+        if (quads) {
 #pragma unroll
             for (int i = 0; i < kEachQuads; ++i) {
                 const int e = (i * kThreads + tid) * 4;
@@ -213,20 +213,21 @@ __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int t
         if (tid < kBlock)
             ab[b][tid] = make_float2(expf(abr.x), abr.y);
     };
-    // a block's fours: P / 32 threads a product, which start at different places of their rows (they lie in the same banks)
+    // a block's fours: kShare threads a product, which start at different places of their rows (they lie in the same banks)
     auto join = [&](int b) {
-        constexpr int kShare = P / 32;
+        constexpr int kShare = kThreads * P / 8192, kQuads = 2048 / kThreads;   // threads of a product, fours of a thread
         const int d = tid / kShare % 16, f = tid / kShare / 16, t0 = 4 * f;
         const bool inner = d < 10;   // m, else l
         const int e = inner ? d : d - 10, i = inner ? (e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0) : (e >= 3 ? 3 : e >= 1 ? 2 : 1);
         const int j = inner ? e - i * (i + 1) / 2 : e - i * (i - 1) / 2;
         const float *x = inner && !BACK ? qs[b][t0 + i] : ks[b][t0 + i], *y = inner && BACK ? qs[b][t0 + j] : ks[b][t0 + j];
-        float sum = 0.f;
-#pragma unroll 4
-        for (int n = 0; n < 8; ++n) {
-            const int at = ((n + d) % 8 * kShare + tid % kShare) * 4;
-            sum = dot4(*reinterpret_cast<const float4 *>(x + at), *reinterpret_cast<const float4 *>(y + at), sum);
+        float sums[4] = {};
+#pragma unroll
+        for (int n = 0; n < kQuads; ++n) {
+            const int at = ((n + d) % kQuads * kShare + tid % kShare) * 4;
+            sums[n % 4] = dot4(*reinterpret_cast<const float4 *>(x + at), *reinterpret_cast<const float4 *>(y + at), sums[n % 4]);
         }
+        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 #pragma unroll
         for (int m = kShare / 2; m; m /= 2)
             sum += __shfl_xor_sync(~0u, sum, m);
@@ -574,18 +575,10 @@ cudaError_t launch_delta_cols(const DeltaArgs &a, int dtype, bool backward, cuda
         typedef std::remove_pointer_t<decltype(o)> To;
         auto go = [&](auto p) {
             constexpr int P = decltype(p)::value;
-            const bool quad = a.K % 4 == 0;
-            if (!backward) {
-                if (quad)
-                    delta_cols_kernel<Tx, To, P, false, true><<<grid, kThreads, 0, s>>>(a, tiles);
-                else
-                    delta_cols_kernel<Tx, To, P, false, false><<<grid, kThreads, 0, s>>>(a, tiles);
-            } else if constexpr (std::is_same_v<To, float>) {   // the backward has no outputs of another type
-                if (quad)
-                    delta_cols_kernel<Tx, float, P, true, true><<<grid, kThreads, 0, s>>>(a, tiles);
-                else
-                    delta_cols_kernel<Tx, float, P, true, false><<<grid, kThreads, 0, s>>>(a, tiles);
-            }
+            if (!backward)
+                delta_cols_kernel<Tx, To, P, false><<<grid, kThreads, 0, s>>>(a, tiles);
+            else if constexpr (std::is_same_v<To, float>)   // the backward has no outputs of another type
+                delta_cols_kernel<Tx, float, P, true><<<grid, kThreads, 0, s>>>(a, tiles);
             return cudaGetLastError();
         };
         return a.K <= 64 ? go(std::integral_constant<int, 64>()) : a.K <= 128 ? go(std::integral_constant<int, 128>())
