@@ -4,10 +4,11 @@
 //     p_ij = scale D_ij dO_i.N_j (j <= i),   b_ij = -beta_i D_ij x_i.N_j (j < i),   D_ij = e^(G_i - G_j)
 //     dq = scale e^G dO S' + p k,   dk = -beta e^G x S' + e^(G_end - G) N dS' + p' q + (b + b') k
 //
-// Persistent CTAs of eight warps: warp (r, h) has 16 rows and half of the keys, with dq and dk in registers over all value
+// Persistent CTAs of 16 warps: warp (r, h) has 16 rows and a quarter of the keys, with dq and dk in registers over all value
 // heads.  The values come 64 columns at a time in two stages (one ahead, across heads and chunks): products over them of
-// 16-row blocks into dO S', x S', N dS' and, by halves, p or b, which pass shared memory once to be left operands both as
-// they are and transposed.
+// 16-row blocks into dO S', x S', N dS' and, by halves of columns, p (h < 2) or b, which pass shared memory once to be left
+// operands both as they are and transposed.  Eight warps with half of the keys each, of 255 registers, took 69 us for 4 x 2048
+// tokens of 8 heads, bound by latency.
 #include <algorithm>
 
 #include "delta_chain.cuh"
@@ -15,7 +16,7 @@
 namespace gla {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 template <int KD>
 struct GradShared {
@@ -35,7 +36,7 @@ struct GradShared {
 
 // What a CTA works on: 64 columns of a value head of a chunk.
 struct GradPiece {
-    int64_t item;   // slot * H + key head
+    int item;   // slot * H + key head
     int first, rows, slot, h, v, c;   // first row and rows of the chunk; value head of the key head; piece of its columns
     int turn, items;                  // pieces and items so far
 };
@@ -43,11 +44,11 @@ struct GradPiece {
 // Whether `p.item` or one after it (a grid apart) is a chunk with rows; p becomes its first piece.
 __device__ __forceinline__ bool find_item(const DeltaArgs &a, GradPiece &p)
 {
-    const int64_t end = (int64_t)a.slots * a.H;
+    const int end = a.slots * a.H;
     for (; p.item < end; p.item += gridDim.x) {
         int n, c;
-        p.slot = (int)(p.item / a.H);
-        p.h = (int)(p.item - (int64_t)p.slot * a.H);
+        p.slot = p.item / a.H;
+        p.h = p.item - p.slot * a.H;
         if (delta_chunk(a, p.slot, n, c, p.first, p.rows)) {
             p.v = p.c = 0;
             return true;
@@ -80,46 +81,60 @@ template <typename T, int KD>
 __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_constant__ ChainMaps maps, DeltaArgs a)
 {
     typedef GradShared<KD> Shared;
-    constexpr int NT = KD / 16;   // tiles of 8 keys of a warp
+    constexpr int NT = KD / 32;   // tiles of 8 keys of a warp
     extern __shared__ __align__(1024) char raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     const int tid = threadIdx.x, lane = tid % 32, r = tid / 32 % 4, h = tid / 128, two = 2 * (lane % 4), i0 = 16 * r + lane / 4;
     const int per = a.HV / a.H;
     bars_init(sh.full);
     tc::grid_dep_wait();
+    // the first lanes of eight warps ask for a part each: a copy takes its thread some 200 cycles to issue
     auto ask = [&](const GradPiece &p) {
+        if (lane)
+            return;
         auto &st = sh.stage[p.turn & 1];
         uint64_t *bar = &sh.full[p.turn & 1];
         const int hv = p.h * per + p.v, blocks = min(8, (a.V - 64 * p.c) / 8);   // rows of blocks
         const bool begins = p.v == 0 && p.c == 0;
         const uint32_t narrow_bytes = blocks * 8 * 128, wide_bytes = blocks * (KD / 8) * 128;
-        tc::bar_expect_tx(bar, (uint32_t)(sizeof st.d + 2 * narrow_bytes + 2 * wide_bytes + sizeof st.row + sizeof st.gate +
-                                          (begins ? sizeof sh.rows[0] : 0)));
-        if (begins)
-#pragma unroll
-            for (int i = 0; i < KD / 64; ++i) {
-                tc::tma_load_3d(sh.rows[p.items & 1].k[i], &maps.k, 64 * i, p.h, p.first, bar);
-                tc::tma_load_3d(sh.rows[p.items & 1].q[i], &maps.q, 64 * i, p.h, p.first, bar);
-            }
         const size_t cell = (size_t)p.slot * a.HV + hv;
-        const char *from = a.chunk + cell * sizeof(DeltaCellBack);
-        copy_bulk(st.row, from + kCellRows, sizeof st.row, bar);
-        copy_bulk(st.gate, from + sizeof(DeltaCellBack) - sizeof st.gate, sizeof st.gate, bar);
-        tc::tma_load_3d(st.d, &maps.d, 64 * p.c, hv, p.first, bar);
         const size_t narrow_at = cell * a.trace.n_size + (size_t)p.c * 8 * 8 * 32, wide_at = cell * a.trace.s_size + (size_t)p.c * 8 * (KD / 8) * 32;
-        copy_bulk(st.n, a.trace.n + narrow_at, narrow_bytes, bar);
-        copy_bulk(st.x, a.trace.x + narrow_at, narrow_bytes, bar);
-        copy_bulk(st.s, a.trace.s + wide_at, wide_bytes, bar);
-        copy_bulk(st.ds, a.trace.ds + wide_at, wide_bytes, bar);
+        const char *from = a.chunk + cell * sizeof(DeltaCellBack);
+        switch (tid / 32) {
+        case 0:
+            tc::bar_expect_tx(bar, (uint32_t)(sizeof st.d + 2 * narrow_bytes + 2 * wide_bytes + sizeof st.row + sizeof st.gate +
+                                              (begins ? sizeof sh.rows[0] : 0)));
+            copy_bulk(st.s, a.trace.s + wide_at, wide_bytes, bar);
+            break;
+        case 1: copy_bulk(st.ds, a.trace.ds + wide_at, wide_bytes, bar); break;
+        case 2: tc::tma_load_3d(st.d, &maps.d, 64 * p.c, hv, p.first, bar); break;
+        case 3: copy_bulk(st.n, a.trace.n + narrow_at, narrow_bytes, bar); break;
+        case 4: copy_bulk(st.x, a.trace.x + narrow_at, narrow_bytes, bar); break;
+        case 5:
+            copy_bulk(st.row, from + kCellRows, sizeof st.row, bar);
+            copy_bulk(st.gate, from + sizeof(DeltaCellBack) - sizeof st.gate, sizeof st.gate, bar);
+            break;
+        case 6:
+            if (begins)
+#pragma unroll
+                for (int i = 0; i < KD / 64; ++i)
+                    tc::tma_load_3d(sh.rows[p.items & 1].k[i], &maps.k, 64 * i, p.h, p.first, bar);
+            break;
+        case 7:
+            if (begins)
+#pragma unroll
+                for (int i = 0; i < KD / 64; ++i)
+                    tc::tma_load_3d(sh.rows[p.items & 1].q[i], &maps.q, 64 * i, p.h, p.first, bar);
+            break;
+        }
     };
     GradPiece now = {}, ahead;
     now.item = blockIdx.x;
     if (!find_item(a, now))
         return;
     ahead = now;
-    if (tid == 0)
-        ask(now);
-    float dq[NT][4], dk[NT][4], m[8][4], ds[NT][4], xs[NT][4], nd[NT][4];
+    ask(now);
+    float dq[NT][4], dk[NT][4], m[4][4], ds[NT][4], xs[NT][4], nd[NT][4];
     auto clear = [](auto &x) {
         for (auto &t : x)
             t[0] = t[1] = t[2] = t[3] = 0.f;
@@ -135,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
             return;
         }
         const bool more = next_piece(a, ahead);
-        if (tid == 0 && more)
+        if (more)
             ask(ahead);
         if (now.rows < kDeltaChunk) {   // rows behind the sequence's end may hold anything
             const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -157,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
             blocks_t<false>(fx, &st.x[0][0][0], 8, 2 * s, 2 * r, lane);
             blocks_t<false>(fn, &st.n[0][0][0], 8, 2 * s, 2 * r, lane);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {   // p of this block of rows, or b
-                if (p > r)
+            for (int p = 0; p < 2; ++p) {   // columns of p, or of b, in this block of rows
+                if (2 * (h & 1) + p > r)
                     break;
                 uint32_t f[4];
-                blocks_t<true>(f, &st.n[0][0][0], 8, 2 * s, 2 * p, lane);
-                mma<T>(m[2 * p], h ? fx : fd, f[0], f[1]);
-                mma<T>(m[2 * p + 1], h ? fx : fd, f[2], f[3]);
+                blocks_t<true>(f, &st.n[0][0][0], 8, 2 * s, 4 * (h & 1) + 2 * p, lane);
+                mma<T>(m[2 * p], h > 1 ? fx : fd, f[0], f[1]);
+                mma<T>(m[2 * p + 1], h > 1 ? fx : fd, f[2], f[3]);
             }
 #pragma unroll
             for (int p = 0; p < NT / 2; ++p) {
@@ -181,16 +196,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
         if ((now.c + 1) * 64 >= a.V) {   // the value head's last columns
             const float4 c0 = st.row[i0], c1 = st.row[i0 + 8];
             const float2 g0 = st.gate[i0], g1 = st.gate[i0 + 8];
-            const float f0 = h ? -c0.x : a.scale, f1 = h ? -c1.x : a.scale;
-            uint16_t(*to)[72] = h ? sh.b : sh.p;
+            const float f0 = h > 1 ? -c0.x : a.scale, f1 = h > 1 ? -c1.x : a.scale;
+            uint16_t(*to)[72] = h > 1 ? sh.b : sh.p;
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int j = 16 * p + 8 * y + two;
+                    const int j = 32 * (h & 1) + 16 * p + 8 * y + two;
                     const float2 ga = st.gate[j], gb = st.gate[j + 1];
                     auto take_if = [&](int i, int jj, float f, float2 gi, float2 gj, float v) {
-                        return i < now.rows && (h ? jj < i : jj <= i) ? f * exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * v : 0.f;
+                        return i < now.rows && (h > 1 ? jj < i : jj <= i) ? f * exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * v : 0.f;
                     };
                     const float(&v)[4] = m[2 * p + y];
                     *reinterpret_cast<uint32_t *>(&to[i0][j]) =
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
 #pragma unroll
                 for (int p = 0; p < NT / 2; ++p) {
                     uint32_t f[4];
-                    const int key = h * (KD / 2) + 16 * p;   // first of 16 keys
+                    const int key = h * (KD / 4) + 16 * p;   // first of 16 keys
                     const uint32_t at = unit_at(16 * s + (lane & 15), key % 64 / 8 + lane / 16);
                     ldsm_t(f, tc::smem_u32(rows.k[key / 64]) + at);
                     if (s <= r) {
@@ -240,17 +255,25 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
                     }
                 }
             }
-            if (now.v + 1 == per) {
+            if (now.v + 1 == per) {   // by way of the keys' and queries' place, to rows of whole units
+                __syncthreads();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (i0 + 8 * e >= now.rows)
-                        continue;
-                    const size_t at = ((size_t)(now.first + i0 + 8 * e) * a.H + now.h) * KD + h * (KD / 2) + two;
+                for (int j = 0; j < NT; ++j) {
+                    const int key = h * (KD / 4) + 8 * j;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        *reinterpret_cast<uint32_t *>(static_cast<T *>(a.dq) + at + 8 * j) = narrow2<T>(make_float2(dq[j][2 * e], dq[j][2 * e + 1]));
-                        *reinterpret_cast<uint32_t *>(static_cast<T *>(a.dk) + at + 8 * j) = narrow2<T>(make_float2(dk[j][2 * e], dk[j][2 * e + 1]));
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t at = unit_at(i0 + 8 * e, key % 64 / 8) + 2 * two;
+                        *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(rows.k[key / 64]) + at) = narrow2<T>(make_float2(dq[j][2 * e], dq[j][2 * e + 1]));
+                        *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(rows.q[key / 64]) + at) = narrow2<T>(make_float2(dk[j][2 * e], dk[j][2 * e + 1]));
                     }
+                }
+                __syncthreads();
+                for (int u = tid; u < now.rows * (KD / 8); u += kThreads) {
+                    const int t = u / (KD / 8), unit = u % (KD / 8);
+                    const uint32_t at = unit_at(t, unit % 8);
+                    const size_t to = ((size_t)(now.first + t) * a.H + now.h) * KD + 8 * unit;
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(a.dq) + to) = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(rows.k[unit / 8]) + at);
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(a.dk) + to) = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(rows.q[unit / 8]) + at);
                 }
                 clear(dq), clear(dk);
             }
