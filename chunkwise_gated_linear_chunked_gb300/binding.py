@@ -815,6 +815,14 @@ DELTA_CODE = {(torch.float32, torch.float32): GLA_F32, (torch.bfloat16, torch.fl
 _ACTIVATION = {None: 0, "silu": 1}
 
 
+def _status_of(what, status, device):
+    """The address of a call's status word: the caller's 256 zeroed bytes, or the library's own."""
+    if status is not None and (status.get_device() != device or not status.is_contiguous() or
+                               status.numel() * status.element_size() < _STATUS_BYTES):
+        raise GlaError(GLA_ERR_WORKSPACE, f"{what}: status must be {_STATUS_BYTES} contiguous bytes on cuda:{device}")
+    return _status_workspace(status, device)[0]
+
+
 def _scratch(what, workspace, nbytes, device):
     """(tensor, address, bytes) of a call's scratch: the caller's, or memory of the call's own."""
     if workspace is None:
@@ -891,7 +899,7 @@ def _delta_fwd_checked(q, k, v, g, beta, scale, initial_state, output_final_stat
     workspace, at, nbytes = _scratch(what, workspace, need, device)
     rc = _lib.gla_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), o.data_ptr(),
                             K ** -0.5 if scale is None else scale, _at(initial_state), _at(ht), _at(cu_seqlens), N, B, T,
-                            H, HV, K, V, code, _status_workspace(status, device)[0], at, nbytes, _raw_stream(device))
+                            H, HV, K, V, code, _status_of(what, status, device), at, nbytes, _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, what)
     return o, ht
@@ -902,7 +910,7 @@ def delta_bwd(q, k, v, g, beta, do, scale=None, initial_state=None, dht=None, cu
     """Gradients of ``delta_fwd`` for L = sum(o * do) + sum(ht * dht); the states are computed again.
 
     The inputs as for delta_fwd; do: [B, T, HV, V] of q's type; dht: fp32 [N, HV, K, V] or None.  Returns (dq, dk, dv in
-    q's type, dg, dbeta fp32 [B, T, HV], dh0 fp32 [N, HV, K, V] or None).
+    q's type, dg, dbeta fp32 [B, T, HV], dh0 fp32 [N, HV, K, V] or None); rows outside all sequences are not written.
     """
     if status is None and workspace is None and stream is None:
         got = _calls.delta_bwd(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqlens, want_dh0)
@@ -932,7 +940,7 @@ def _delta_bwd_checked(q, k, v, g, beta, do, scale, initial_state, dht, cu_seqle
     rc = _lib.gla_delta_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), do.data_ptr(),
                             K ** -0.5 if scale is None else scale, _at(initial_state), _at(dht), dq.data_ptr(),
                             dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _at(dh0), _at(cu_seqlens), N, B,
-                            T, H, HV, K, V, code, _status_workspace(status, device)[0], at, nbytes, _raw_stream(device))
+                            T, H, HV, K, V, code, _status_of(what, status, device), at, nbytes, _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, what)
     return dq, dk, dv, dg, dbeta, dh0
@@ -965,7 +973,7 @@ def _delta_step_checked(q, k, v, g, beta, state, scale, slots, state_out, out_dt
     o = torch.empty(v.shape, dtype=out_dtype or q.dtype, device=device)
     rc = _lib.gla_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), o.data_ptr(),
                              K ** -0.5 if scale is None else scale, state.data_ptr(), state_out.data_ptr(), _at(slots), B,
-                             S, H, HV, K, V, code, _status_workspace(status, device)[0], _raw_stream(device))
+                             S, H, HV, K, V, code, _status_of(what, status, device), _raw_stream(device))
     if rc != GLA_OK:
         raise GlaError(rc, what)
     return o

@@ -268,6 +268,7 @@ __device__ __forceinline__ void clear_tail(Stage &st, int rows)
 #pragma unroll
         for (int x = 0; x < kRows; ++x)
             reinterpret_cast<uint4 *>(st.v[x])[i] = zero;
+    tc::fence_proxy_async();   // before a later copy to the same place
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder()

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
                         reinterpret_cast<uint4 *>(rows.q[x])[i] = zero;
                     }
             }
+            tc::fence_proxy_async();   // before a later copy to the same place
             __syncthreads();
         }
         const int steps = min(4, (a.V - 64 * now.c) / 16);
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
                     *reinterpret_cast<uint4 *>(static_cast<T *>(a.dq) + to) = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(rows.k[unit / 8]) + at);
                     *reinterpret_cast<uint4 *>(static_cast<T *>(a.dk) + to) = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(rows.q[unit / 8]) + at);
                 }
+                tc::fence_proxy_async();
                 clear(dq), clear(dk);
             }
         }

@@ -456,8 +456,9 @@ size_t gla_norm_bwd_workspace_size(int64_t rows, int D);
  *     S~ = exp(g_t) S_{t-1},   n_t = beta_t (v_t - k_t S~),   S_t = S~ + k_t^T n_t,   o_t = scale q_t S_t
  *
  *   q, k        [rows, H, K] device, input type;  v [rows, HV, V];  HV a multiple of H
- *   g, beta     [rows, HV] fp32 whatever the input type: log-decay (usually <= 0; -inf clears the state) and write strength.
- *               The state stays bounded for beta in [0, 2] and keys of length at most 1; neither is checked
+ *   g, beta     [rows, HV] fp32 whatever the input type: log-decay (usually <= 0; -inf clears the state; sums of consecutive
+ *               gates must stay below 88, where their exponential leaves fp32) and write strength.  The state stays bounded
+ *               for beta in [0, 2] and keys of length at most 1; neither is checked
  *   o           [rows, HV, V] device, written
  *   h0, ht      [N, HV, K, V] fp32 device or NULL; ht may equal h0.  A sequence of length zero has ht = h0 (or 0)
  *   cu_seqlens  int32 [N + 1] device offsets (B == 1; T the packed rows) or NULL (N == B).  They must not decrease and

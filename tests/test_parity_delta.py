@@ -109,7 +109,7 @@ def check_bwd(B, s, x, scale=None):
 
 
 HEADS = [(1, 1, 64, 64), (2, 2, 128, 128), (1, 3, 128, 64), (2, 4, 64, 256), (1, 2, 128, 16), (1, 1, 64, 48), (3, 3, 96, 80), (1, 1, 7, 5),
-         (1, 2, 128, 100), (1, 1, 256, 256), (1, 1, 1, 1)]
+         (1, 2, 128, 100), (1, 1, 256, 256), (1, 1, 1, 1), (1, 2, 64, 240), (1, 1, 128, 80)]
 LENGTHS = [dict(Bn=1, T=1), dict(Bn=2, T=63), dict(Bn=1, T=64), dict(Bn=3, T=130), dict(lengths=[1, 0, 64, 65, 130, 3, 0])]
 
 
@@ -309,6 +309,43 @@ def test_bad_slots_are_reported(B):
     pool = torch.ones(3, 1, 64, 64, device="cuda")
     o = B.delta_step(*args, pool, slots=torch.tensor([3, -2], dtype=torch.int32, device="cuda"))
     assert B.layer_status() == B.GLA_ERR_INVALID_ARG and (o == 0).all() and (pool == 1).all()
+
+
+def test_offsets_beyond_32_bits(B):
+    """Values of more than 2^31 elements: the last head of the last rows as in a call with that head alone."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    T, HV, V = 1 << 17, 136, 128
+    q, k = (torch.nn.functional.normalize(torch.randn(1, T, 1, 64, device="cuda", generator=gen), dim=-1).to(TB) for _ in range(2))
+    v = torch.randn(1, T, HV, V, device="cuda", generator=gen, dtype=TB)
+    g, beta = -0.1 * torch.rand(1, T, HV, device="cuda", generator=gen), torch.rand(1, T, HV, device="cuda", generator=gen)
+    assert v.numel() > 1 << 31
+    o, ht = B.delta_fwd(q, k, v, g, beta)
+    last = [t[:, :, -1:].contiguous() for t in (v, g, beta)]
+    one, end = B.delta_fwd(q, k, *last)
+    assert torch.equal(o[:, :, -1:], one) and torch.equal(ht[:, -1:], end)
+    del o
+    got = B.delta_bwd(q, k, v, g, beta, v)
+    one = B.delta_bwd(q, k, *last, last[0])
+    for x, y in zip(got[2:5], one[2:5]):
+        assert torch.equal(x[:, :, -1:], y)
+    assert torch.equal(got[5][:, -1:], one[5])
+
+
+def test_own_status_and_scratch(B):
+    """A status word of the call's own that is too small, and scratch that is."""
+    s, x = make(TB, Bn=1, T=70, K=64, V=64)
+    args = [dev(s[n]) for n in ("q", "k", "v", "g", "beta")]
+    with pytest.raises(B.GlaError):
+        B.delta_fwd(*args, status=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(B.GlaError):
+        B.delta_fwd(*args, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    need = B.lib().gla_delta_bwd_workspace_size(1, 1, 70, 1, 1, 64, 64, B.GLA_BF16, 0)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is read before it is written
+    for a, b in zip(B.delta_bwd(*args, dev(x["do"]), workspace=ws), B.delta_bwd(*args, dev(x["do"]))):
+        assert torch.equal(a, b)
+    need = B.lib().gla_delta_fwd_workspace_size(1, 1, 70, 1, 1, 64, 64, B.GLA_BF16_OBF16, 0)
+    for a, b in zip(B.delta_fwd(*args, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda")), B.delta_fwd(*args)):
+        assert torch.equal(a, b)
 
 
 def test_fp16_range_is_reported(B):

@@ -133,6 +133,23 @@ def test_repeats_graph_and_other_stream(B):
             assert all(torch.equal(p, r) for p, r in zip(got, (*want, *want_back)))
 
 
+@pytest.mark.parametrize("shape,G", [((1 << 21, 1040), 8), ((2, 1 << 20, 1040), 8)], ids=str)
+def test_offsets_beyond_32_bits(B, shape, G):
+    x = torch.randn(shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(8), dtype=TB)
+    assert x.numel() > 1 << 31
+    w = torch.randn(shape[-1], device="cuda")
+    y, mean, rstd = B.group_norm_fwd(x, G, weight=w, bias=w, activation="silu")
+    one = B.group_norm_fwd(x[-1:].contiguous(), G, weight=w, bias=w, activation="silu")
+    # one sample alone is cut into other slices: statistics within their bound of one another
+    assert (mean[-1:] - one[1]).abs().max() <= 2 * do.SUM and ((rstd[-1:] - one[2]) / one[2]).abs().max() <= 4 * do.SUM
+    assert (y[-1:].float() - one[0].float()).abs().max() <= 2 ** -7 * one[0].abs().max()   # neighbours in bf16
+    del y
+    dx, dw, db = B.group_norm_bwd(x, mean, rstd, x, weight=w, bias=w, activation="silu")
+    alone = B.group_norm_bwd(x[-1:].contiguous(), mean[-1:].contiguous(), rstd[-1:].contiguous(), x[-1:].contiguous(), weight=w, bias=w,
+                             activation="silu")[0]
+    assert (dx[-1:].float() - alone.float()).abs().max() <= 2 ** -7 * alone.abs().max()
+
+
 def test_nothing_to_do(B):
     x, w = torch.zeros(0, 7, 64, device="cuda"), torch.ones(64, device="cuda")
     y, mean, rstd = B.group_norm_fwd(x, 4, weight=w)
