@@ -12,7 +12,10 @@
 //     dbeta = x.Y,   dg_t = sum over i >= t of (o_i.dO_i - dv_i.v_i) + <S, dS> at the end of the sum
 //
 // (scaling a token's S by a factor scales every later o but not what a token adds), where the sums run to the end of a group
-// of eight chunks, whose state the forward has kept in fp32.
+// of eight chunks, whose state the forward has kept in fp32.  (The longer the sums, the more of a row's rounding is left in
+// dg: 3.6e-5 of it with groups of eight, 2e-5 with groups of four, which take 1 to 2 % longer.)
+//
+// 3.5 us a chunk of 32 columns (4 x 2048 tokens of 8 heads 114 us), bound by the second warp's 232 products and its outputs.
 #include "delta_chain.cuh"
 
 namespace gla {

@@ -17,7 +17,8 @@
 // Where there are few heads the chain from token to token bounds it, and of that the sums over the lanes.  So
 // four tokens go together: their products with the state that enters the four are summed at once, what they add to one
 // another comes from products of their keys and queries (found once a block of tokens, times the decays between them), and
-// the state advances by four at a time.  3 x 1001 tokens, 5 heads of 96 x 80: 264 us token by token, 92 by fours.
+// the state advances by four at a time.  3 x 1001 tokens, 5 heads of 96 x 80 in fp32: 165 us (660 ns a four, of which the
+// products and the update take some 370 instructions a warp); 264 us token by token with eight lanes a column.
 #include <type_traits>
 
 #include "api_common.h"

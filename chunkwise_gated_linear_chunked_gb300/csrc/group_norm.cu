@@ -3,17 +3,20 @@
 //     mean, var over S x W values,   rstd = 1 / sqrt(var + eps),   xh = (x - mean) rstd,   z = xh w + b,   y = act(z)
 //     dz = dy act'(z),   a = w dz,   dx = rstd (a - mean(a) - xh mean(a xh)),   dw = sum dz xh,   db = sum dz
 //
-// Bound by HBM (two instructions an element a byte or so).  Two ways:
+// Two ways:
 //
 // One position a sample (tokens) and at most 4096 channels a group: a group is a run of memory that up to 256 lanes hold
 // in registers, so that it is read once; variances are sums of squares about the mean.  A lane keeps its channels from
-// sample to sample, with their weights and its share of dw and db in registers.
+// sample to sample, with their weights and its share of dw and db in registers.  32768 tokens of 2048 channels in 16 groups,
+// bf16: 50 us, 5.4 TB/s, bound by instructions (72 % of the issue slots): two groups a lane at a time and four CTAs an SM
+// (five: 63 us, four groups at a time: 66).
 //
 // Otherwise (maps): samples are cut into slices of positions.  A CTA walks a slice with a vector of channels a thread and
 // sums per channel, about the thread's first value (a value of the group itself, so the sum of squares loses at most the
 // thread's count of units to the cancellation), joins the threads' means and squares by group, and a second kernel joins
-// the slices and writes y (dx); it reads x again, from L2 where the tensor fits.  Every join has a fixed order, so results
-// do not depend on timing.
+// the slices and writes y (dx); it reads x again, from L2 where the tensor fits.  8 x 4096 positions of 512 channels with
+// SiLU, bf16: 22 us forward, 43 backward, bound by the latency of two (three) kernels of one wave and by the two special
+// functions of a sigmoid (each pass 7 us of them).  Every join has a fixed order, so results do not depend on timing.
 #include <algorithm>
 #include <numeric>
 #include <type_traits>
