@@ -12,10 +12,12 @@
 //     dbeta = x.Y,   dg_t = sum over i >= t of (o_i.dO_i - dv_i.v_i) + <S, dS> at the end of the sum
 //
 // (scaling a token's S by a factor scales every later o but not what a token adds), where the sums run to the end of a group
-// of eight chunks, whose state the forward has kept in fp32.  (The longer the sums, the more of a row's rounding is left in
-// dg: 3.6e-5 of it with groups of eight, 2e-5 with groups of four, which take 1 to 2 % longer.)
+// of two chunks, whose state the forward has kept in fp32, and dS is the sum of the two terms that the products have of it.
+// (The longer the sums, the more of a row's rounding is left in dg: 5.8e-6 of it at 4 x 2048 tokens of 8 heads; groups of four
+// and eight chunks 6.5e-6 and 8.4e-6 in 2 to 4 % less time, one chunk 3 to 6 % more.  Where a head keeps little of its
+// state from token to token the sums cancel most: there groups of two leave 8e-6, of eight 1.4e-5.)
 //
-// 3.5 us a chunk of 32 columns (4 x 2048 tokens of 8 heads 114 us), bound by the second warp's 232 products and its outputs.
+// 3.8 us a chunk of 32 columns (4 x 2048 tokens of 8 heads 123 us), bound by the second warp's 232 products and its outputs.
 #include "delta_chain.cuh"
 
 namespace gla {
@@ -63,9 +65,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             for (int e = 0; e < 4; ++e)
                 s[j][e] *= last;
         bar_sync(kBarShare + group);
-        uint32_t hi[4][4], lo[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // g
+        for (int i = 0; i < 4; ++i) {   // g, and x = g + (T' - I) g
+            uint32_t hi[4];
             float r[2][4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -74,11 +76,11 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 const float f0 = row[8 * j + two].z, f1 = row[8 * j + two + 1].z;
                 r[y][0] = fmaf(f0, x[j][0], p.x), r[y][1] = fmaf(f1, x[j][1], p.y);
                 r[y][2] = fmaf(f0, x[j][2], p.z), r[y][3] = fmaf(f1, x[j][3], p.w);
-                x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+                x[j][0] = r[y][0], x[j][1] = r[y][1], x[j][2] = r[y][2], x[j][3] = r[y][3];
             }
-            split_pair<T>(r[0], r[1], hi[i], lo[i]);
+            triangle_step<T, true, 2>(x, r[0], r[1], hi, i, st.cell.inverse, lane);
         }
-        triangle<T, true>(x, hi, lo, st.cell.inverse, lane);
+        uint32_t hi[4][4], lo[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float u[2][4];
@@ -234,23 +236,28 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
     if (!output) {
         float s[KD / 8][4];
         state_io<KD>(s, nullptr, a.dht, state, a.V, col, on, false);
-        walk([&](auto &st, int c) {
-            if (on && ((c + 1) % kDeltaKept == 0 || c + 1 == w.chunks)) {   // <S, dS> at the end of a group of chunks
-                const size_t at = delta_kept_at(a, w.n, c, w.hv, g16);
-                const float4 *kept = trace.kept + at * (KD / 8 * 32) + lane;
-                float sum = 0.f;
+        auto across = [&](int c) {   // <S, dS> behind chunk c, of the dS that the products have
+            const size_t at = delta_kept_at(a, w.n, c, w.hv, g16);
+            const float4 *kept = trace.kept + at * (KD / 8 * 32) + lane;
+            float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < KD / 8; ++j) {
-                    const float4 p = kept[j * 32];
-                    sum += (p.x * s[j][0] + p.y * s[j][1]) + (p.z * s[j][2] + p.w * s[j][3]);
-                }
-#pragma unroll
-                for (int m = 16; m; m /= 2)
-                    sum += __shfl_xor_sync(~0u, sum, m);
-                if (lane == 0)
-                    trace.across[at] = sum;
+            for (int j = 0; j < KD / 8; ++j) {
+                const float4 p = kept[j * 32];
+                const float2 d0 = in_two<T>(s[j][0], s[j][1]), d1 = in_two<T>(s[j][2], s[j][3]);
+                sum += (p.x * d0.x + p.y * d0.y) + (p.z * d1.x + p.w * d1.y);
             }
+#pragma unroll
+            for (int m = 16; m; m /= 2)
+                sum += __shfl_xor_sync(~0u, sum, m);
+            if (lane == 0)
+                trace.across[at] = sum;
+        };
+        if (on && w.chunks)
+            across(w.chunks - 1);
+        walk([&](auto &st, int c) {
             chain(st, s);
+            if (on && c > 0 && c % kDeltaKept == 0)   // while the other warp is at its outputs
+                across(c - 1);
         });
         report_lost<T>(a, s, false);
         if (a.dh0)

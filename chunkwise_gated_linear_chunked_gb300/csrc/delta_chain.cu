@@ -25,12 +25,18 @@
 namespace gla {
 namespace {
 
-// SAVE: for the gradients, instead of o its products with dO, the rounded states and rows, Y, and every eighth state.
+// SAVE: for the gradients, instead of o its products with dO, the rounded states and rows, Y, and every second state.  The
+// gradient of a gate is a sum of o.dO - dv.v over rows that cancel but for what later rows have of earlier ones, so that the
+// two have to be of one linear map where they cancel: the diagonals of T^ and T' are exact, P' is P to the bit, and N is an
+// operand of three terms where it meets P, and behind the last chunk where it meets K, since the gradient of the final state
+// can be of any size (4 x 2048 tokens of 8 heads, a gradient of the final state as large as its values: dg off by 5.8e-6 of
+// it; 3.6e-5 with two terms throughout and T^ with its diagonal).
 template <typename T, typename To, int KD, int VG, bool SAVE>
 __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_constant__ ChainMaps maps, DeltaArgs a, int tiles)
 {
     typedef ChainShared<KD, VG, SAVE ? 2 : 1, DeltaCell> Shared;
     constexpr int kThreads = 64 * VG;
+    constexpr bool kThree = SAVE && std::is_same_v<T, __nv_bfloat16>;   // fp16's second term already ends at the type's last bit
     constexpr size_t kCell = SAVE ? sizeof(DeltaCellBack) : sizeof(DeltaCell);
     extern __shared__ __align__(1024) char raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
@@ -45,7 +51,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     const bool on = w.v0 + 16 * group < a.V;   // whole groups of 16 columns
     const size_t state = (w.head * a.K + two) * a.V;
 
-    auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4]) {
+    auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4], bool end) {
         const float4 *row = st.cell.row;
         float n[8][4] = {};
         {
@@ -67,10 +73,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             for (int e = 0; e < 4; ++e)
                 s[j][e] *= last;
         bar_sync(kBarShare + group);
-        uint32_t hi[4][4], lo[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // R
-            uint32_t v[4];
+        for (int i = 3; i >= 0; --i) {   // R, and Y = R + (T^ - I) R
+            uint32_t v[4], hi[4];
             values_t<VG>(v, st.v[0], i, group, lane);
             float r[2][4];
 #pragma unroll
@@ -83,11 +88,11 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 r[y][1] = fmaf(-f1, n[j][1] + p.y, v0.y);
                 r[y][2] = fmaf(-f0, n[j][2] + p.z, v1.x);
                 r[y][3] = fmaf(-f1, n[j][3] + p.w, v1.y);
-                n[j][0] = n[j][1] = n[j][2] = n[j][3] = 0.f;
+                n[j][0] = r[y][0], n[j][1] = r[y][1], n[j][2] = r[y][2], n[j][3] = r[y][3];
             }
-            split_pair<T>(r[0], r[1], hi[i], lo[i]);
+            triangle_step<T, false, 2>(n, r[0], r[1], hi, i, st.cell.inverse, lane);
         }
-        triangle<T, false>(n, hi, lo, st.cell.inverse, lane);
+        uint32_t hi[4][4], lo[4][4], least[kThree ? 4 : 1][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float u[2][4];
@@ -99,10 +104,16 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 const float f0 = c0.z * c0.x, f1 = c1.z * c1.x;
                 u[y][0] = f0 * n[j][0], u[y][1] = f1 * n[j][1], u[y][2] = f0 * n[j][2], u[y][3] = f1 * n[j][3];
             }
-            split_pair<T>(u[0], u[1], hi[i], lo[i]);
+            if constexpr (kThree)
+                split_pair<T>(u[0], u[1], hi[i], lo[i], least[i]);
+            else
+                split_pair<T>(u[0], u[1], hi[i], lo[i]);
         }
         bar_tell(kBarRows + group);
         state_add<T, KD>(s, hi, lo, st.k, lane);
+        if constexpr (kThree)
+            if (end)
+                state_add<T, KD>(s, least, st.k, lane);
     };
     const DeltaTrace trace = SAVE ? a.trace : DeltaTrace();
     const int g16 = (w.v0 >> 4) + group;   // this group of 16 columns among the head's
@@ -138,9 +149,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
         }
         bar_sync(kBarRows + group);
-        uint32_t hi[4][4], lo[4][4];
+        uint32_t hi[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 3; i >= 0; --i) {
             float n[2][4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -151,9 +162,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 const float b0 = row[8 * j + two].x, b1 = row[8 * j + two + 1].x;
                 n[y][0] = b0 * p.x, n[y][1] = b1 * p.y, n[y][2] = b0 * p.z, n[y][3] = b1 * p.w;
             }
-            split_pair<T>(n[0], n[1], hi[i], lo[i]);
+            triangle_step<T, false, kThree ? 3 : 2, SAVE>(o, n[0], n[1], hi[i], i, st.cell.score, lane);
         }
-        triangle<T, false>(o, hi, lo, st.cell.score, lane);
         if constexpr (kChecked)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
         float s[KD / 8][4];
         state_io<KD>(s, nullptr, a.h0, state, a.V, col, on, false);
         walk([&](auto &st, int c) {
-            chain(st, s);
+            chain(st, s, c + 1 == w.chunks);
             if (SAVE && on && ((c + 1) % kDeltaKept == 0 || c + 1 == w.chunks)) {
                 float4 *to = a.trace.kept + delta_kept_at(a, w.n, c, w.hv, g16) * (KD / 8 * 32) + lane;
 #pragma unroll

@@ -41,31 +41,38 @@ __device__ __forceinline__ float4 as_float4(const float (&c)[4]) { return make_f
 __device__ __forceinline__ uint4 as_uint4(const uint32_t (&c)[4]) { return make_uint4(c[0], c[1], c[2], c[3]); }
 __device__ __forceinline__ void take(uint32_t (&r)[4], uint4 v) { r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w; }
 
-// c (64 tokens) += left operands of the four steps of 16 tokens times a triangle of the cell, lower or upper.
-template <typename T, bool UPPER>
-__device__ __forceinline__ void triangle(float (&c)[8][4], const uint32_t (&hi)[4][4], const uint32_t (&lo)[4][4], const uint4 *m, int lane)
+// c (64 tokens) += the products of 16 tokens' values (two tiles of results, v0 and v1, as left operands of TERMS terms) with
+// their step i of a triangle of the cell, lower or upper.  Steps taken from 3 down (lower) or from 0 up (upper) add to no
+// tile of c that a later step still has to read, so that c's own tiles can be where the values come from.  hi: the first terms.
+// ALL: with the second term's product with the matrix's remainders too.
+template <typename T, bool UPPER, int TERMS, bool ALL = false>
+__device__ __forceinline__ void triangle_step(float (&c)[8][4], const float (&v0)[4], const float (&v1)[4], uint32_t (&hi)[4], int i,
+                                              const uint4 *m, int lane)
 {
+    uint32_t mid[4], lo[4];
+    if constexpr (TERMS == 3)
+        split_pair<T>(v0, v1, hi, mid, lo);
+    else
+        split_pair<T>(v0, v1, hi, mid);
+    uint4 b[8];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int i = UPPER ? 3 - x : x;   // the longest first
-        uint4 b[8];
+    for (int j = 0; j < 8; ++j)
+        if (UPPER ? i >= j / 2 : i <= j / 2)
+            b[j] = m[(UPPER ? triangle_at_t(j, i) : triangle_at(j, i)) * 32 + lane];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (UPPER ? i >= j / 2 : i <= j / 2)
-                b[j] = m[(UPPER ? triangle_at_t(j, i) : triangle_at(j, i)) * 32 + lane];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (UPPER ? i >= j / 2 : i <= j / 2)
-                mma<T>(c[j], hi[i], b[j].x, b[j].y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (UPPER ? i >= j / 2 : i <= j / 2)
-                mma<T>(c[j], lo[i], b[j].x, b[j].y);
+    for (int term = 0; term < 5; ++term)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (UPPER ? i >= j / 2 : i <= j / 2)
-                mma<T>(c[j], hi[i], b[j].z, b[j].w);
-    }
+            if (UPPER ? i >= j / 2 : i <= j / 2) {
+                if (term < 2)
+                    mma<T>(c[j], term == 0 ? hi : mid, b[j].x, b[j].y);
+                else if (term == 2)
+                    mma<T>(c[j], hi, b[j].z, b[j].w);
+                else if (term == 3 && TERMS == 3)
+                    mma<T>(c[j], lo, b[j].x, b[j].y);
+                else if (term == 4 && ALL)
+                    mma<T>(c[j], mid, b[j].z, b[j].w);
+            }
 }
 
 // Offset of 16-byte unit u (eight keys) of row r in a tile of 64 keys of 64 rows.
@@ -120,6 +127,21 @@ __device__ __forceinline__ void state_add(float (&s)[KD / 8][4], const uint32_t 
                 mma<T>(s[4 * p + 2 * x], lo[i], b[x][0], b[x][1]);
                 mma<T>(s[4 * p + 2 * x + 1], lo[i], b[x][2], b[x][3]);
             }
+        }
+}
+
+// The same with one term more.
+template <typename T, int KD>
+__device__ __forceinline__ void state_add(float (&s)[KD / 8][4], const uint32_t (&x)[4][4], const uint16_t (*rows)[64][64], int lane)
+{
+#pragma unroll
+    for (int p = 0; p < KD / 16; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t b[4];
+            ldsm_t(b, tc::smem_u32(rows[p / 4]) + unit_at(16 * i + (lane & 15), 2 * (p % 4) + lane / 16));
+            mma<T>(s[2 * p], x[i], b[0], b[1]);
+            mma<T>(s[2 * p + 1], x[i], b[2], b[3]);
         }
 }
 

@@ -55,7 +55,7 @@ struct DeltaStepArgs {
 };
 
 constexpr int kDeltaChunk = 64;        // rows of a chunk
-constexpr int kDeltaKept = 8;          // chunks between two states that are kept in fp32
+constexpr int kDeltaKept = 2;          // chunks between two states that are kept in fp32
 
 // Rows of sequence n, [bos, bos + len).  False for offsets outside [0, T] or decreasing.
 __device__ __forceinline__ bool delta_sequence(const DeltaArgs &a, int n, int &bos, int &len)

@@ -18,18 +18,18 @@ namespace gla {
 // two of the remainders.  Result tile j (rows 8 j up) takes steps i (columns 16 i up) with 16 i <= 8 j + 7: 20 in all.
 constexpr int kTriangle = 20, kFragments = kTriangle * 32;
 struct DeltaCell {
-    uint4 inverse[kFragments];   // T^ = (I + L diag(beta))^-1, L_ij = e^(G_i - G_j) k_i.k_j below the diagonal
+    uint4 inverse[kFragments];   // T^ - I, T^ = (I + L diag(beta))^-1, L_ij = e^(G_i - G_j) k_i.k_j below the diagonal
     uint4 score[kFragments];     // P_ij = scale e^(G_i - G_j) q_i.k_j up to the diagonal
     float4 row[kDeltaChunk];
 };
 struct DeltaCellBack : DeltaCell {   // and transposed: rows and columns of the tiles' numbers run from the other end
-    uint4 inverse_t[kFragments];     // T' = (I + L' diag(beta))^-1
+    uint4 inverse_t[kFragments];     // T' - I, T' = (I + L' diag(beta))^-1
     uint4 score_t[kFragments];       // P'
     float2 gate[kDeltaChunk];        // G times log2 e in two floats
 };
 struct DeltaCellRows {               // the part of it that the gradients' chain copies, from `row` on
     float4 row[kDeltaChunk];
-    uint4 inverse[kFragments], score[kFragments];   // T', P'
+    uint4 inverse[kFragments], score[kFragments];   // T' - I, P'
 };
 constexpr size_t kCellRows = 2 * kFragments * sizeof(uint4);   // where `row` lies in a cell
 __host__ __device__ constexpr int triangle_at(int j, int i) { return (j / 2) * (j / 2 + 1) + (j % 2) * (j / 2 + 1) + i; }
@@ -78,6 +78,33 @@ __device__ __forceinline__ void split_pair(const float (&c0)[4], const float (&c
     split2<T>(c0[2], c0[3], hi[1], lo[1]);
     split2<T>(c1[0], c1[1], hi[2], lo[2]);
     split2<T>(c1[2], c1[3], hi[3], lo[3]);
+}
+
+// The sum of the two terms that split2 leaves.
+template <typename T>
+__device__ __forceinline__ float2 in_two(float x, float y)
+{
+    uint32_t hi, lo;
+    split2<T>(x, y, hi, lo);
+    const float2 h = widen2<T>(hi), l = widen2<T>(lo);
+    return make_float2(h.x + l.x, h.y + l.y);
+}
+
+// The same in three terms, which hold all of an fp32 value (bf16; fp16's range ends with the second).
+template <typename T>
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = narrow2<T>(make_float2(x, y));
+    const float2 h = widen2<T>(hi);
+    split2<T>(x - h.x, y - h.y, mid, lo);
+}
+template <typename T>
+__device__ __forceinline__ void split_pair(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4], uint32_t (&mid)[4], uint32_t (&lo)[4])
+{
+    split3<T>(c0[0], c0[1], hi[0], mid[0], lo[0]);
+    split3<T>(c0[2], c0[3], hi[1], mid[1], lo[1]);
+    split3<T>(c1[0], c1[1], hi[2], mid[2], lo[2]);
+    split3<T>(c1[2], c1[3], hi[3], mid[3], lo[3]);
 }
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on)

@@ -8,7 +8,8 @@
 // on the diagonal is found by substitution in fp32, a lane a column (W_ij = -(L_ij + sum over j < m < i of L_im beta_m
 // W_mj)); what lies left of it by warp products, W_wp = -sum over p <= m < w of (T^_ww L_wm) T_mp, rows of blocks one after
 // the other.  A sum of powers of L would need no substitution and is not taken: for keys that look alike its terms grow
-// like binomials.  Products of two rounded matrices take three terms, so that blocks are within 2^-16 of their size.
+// like binomials.  Products of two rounded matrices take three terms, so that blocks are within 2^-16 of their size.  Both
+// inverses are stored without their diagonal of ones, which the chains add in fp32.
 //
 // Differences of G decide the decays, and G may run far from zero, so it is summed in 64 bits and kept in two floats.
 // Gates count as at least -1000 (a decay of 0), which keeps differences of two cleared rows finite.
@@ -224,14 +225,15 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
             }
         }
         __syncwarp();
+        const uint32_t below = lane / 4 == two ? 0xffff0000u : lane / 4 == two + 1 ? 0xffffu : ~0u;   // clears ones on a diagonal
         uint32_t m_hi[3][4], m_lo[3][4];   // -T^ L of this row of blocks
         {
             uint32_t d_hi[4], d_lo[4], f_hi[4], f_lo[4];
             ldsm(d_hi, tc::smem_u32(&sh.d_hi[warp][lane % 16][(lane / 16) * 8]));
             ldsm(d_lo, tc::smem_u32(&sh.d_lo[warp][lane % 16][(lane / 16) * 8]));
             // as a right operand its rows are the columns: words 0, 2 hold rows up to 8, words 1, 3 the others
-            cell.inverse[triangle_at(2 * warp, warp) * 32 + lane] = make_uint4(d_hi[0], d_hi[2], d_lo[0], d_lo[2]);
-            cell.inverse[triangle_at(2 * warp + 1, warp) * 32 + lane] = make_uint4(d_hi[1], d_hi[3], d_lo[1], d_lo[3]);
+            cell.inverse[triangle_at(2 * warp, warp) * 32 + lane] = make_uint4(d_hi[0] & below, d_hi[2], d_lo[0], d_lo[2]);
+            cell.inverse[triangle_at(2 * warp + 1, warp) * 32 + lane] = make_uint4(d_hi[1], d_hi[3] & below, d_lo[1], d_lo[3]);
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
                 if (p >= warp)
@@ -290,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
                 uint32_t hi[4], lo[4];
                 ldsm_t(hi, tc::smem_u32(&sh.t_hi[16 * i + step_row][16 * warp + step_col]));
                 ldsm_t(lo, tc::smem_u32(&sh.t_lo[16 * i + step_row][16 * warp + step_col]));
+                if (i == warp)
+                    hi[0] &= below, hi[3] &= below;
                 back.inverse_t[triangle_at_t(2 * warp, i) * 32 + lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                 back.inverse_t[triangle_at_t(2 * warp + 1, i) * 32 + lane] = make_uint4(hi[2], hi[3], lo[2], lo[3]);
                 ldsm_t(hi, tc::smem_u32(&sh.p_hi[16 * i + step_row][16 * warp + step_col]));

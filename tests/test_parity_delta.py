@@ -159,6 +159,30 @@ def test_edges_of_gates_and_strengths(B, dtype, K):
     check_bwd(B, s, x)
 
 
+@pytest.mark.parametrize("dtype", [TB, TH], ids=lambda t: KIND[t])
+@pytest.mark.parametrize("K", [64, 128])
+@pytest.mark.parametrize("HV", [1, 8])
+def test_gate_gradients_of_fast_decays(B, dtype, K, HV):
+    """Gradients of gates after which little is left, behind a final state whose gradient is large: sums of products that
+    cancel.  dg is <e^g S, dS>, and S, dS, the rows between them and the chunk's inverse are held in two 16-bit terms, each
+    off by at most UNIT^2 of its size: 4 UNIT^2 of dg's norm.  (fp16's second term is a multiple of 2^-24: of values from
+    2^-7 on, which make the norm, off by at most 2^-25, 2^-18 of them.)  And a row's o and dv are fp32 sums of 2 K / 16
+    partial products of a tensor core, each cut to 24 bits: off by at most 2 K / 16 2^-23 of their size, of random signs over
+    columns and rows, in sums of o dO and dv v that run over up to 128 rows."""
+    s, x = make(dtype, T=400, H=1, HV=HV, K=K, V=128, gate=1.6, seed=71)
+    x["dht"] = 2 * x["dht"]
+    names = ("q", "k", "v", "g", "beta")
+    dg = B.delta_bwd(*(dev(s[n]) for n in names), dev(x["do"]), initial_state=dev(x["h0"]), dht=dev(x["dht"]))[3]
+    wide = [f64(s[n]) for n in names]
+    o = do.delta_fwd(*wide, K ** -0.5, f64(x["h0"]))[0]
+    _, _, dv, ref, _, _ = do.delta_bwd(*wide, f64(x["do"]), K ** -0.5, f64(x["h0"]), f64(x["dht"]))
+    terms = ((o * f64(x["do"])) ** 2 + (dv * wide[2]) ** 2).sum(-1)
+    sums = np.concatenate([np.cumsum(terms[:, a:a + 128][:, ::-1], 1) for a in range(0, 400, 128)], 1) ** 0.5
+    bound = 4 * max(lo.UNIT[KIND[dtype]] ** 2, 2.0 ** -18) * np.linalg.norm(ref) + 2 * K / 16 * 2.0 ** -23 * np.linalg.norm(sums)
+    error = np.linalg.norm(f64(dg) - ref)
+    assert error <= bound
+
+
 @pytest.mark.parametrize("dtype", [T32, TB], ids=lambda t: KIND[t])
 def test_gates_above_zero(B, dtype):
     s, x = make(dtype, Bn=1, T=140, K=64, V=64, seed=6)
