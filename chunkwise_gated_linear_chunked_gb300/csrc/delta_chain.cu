@@ -13,8 +13,8 @@
 //
 // A CTA takes 32 columns where those make fewer CTAs than the GPU has SMs: its four warps have a quarter of the SM each, and
 // a chunk takes 1.95 us.  Otherwise 64: shared memory, which every warp's right operands pass, and the quarters are then
-// about equally busy, 3.4 us a chunk.  (4 x 2048 tokens of 8 heads, prep included: 88 us with 32 columns, 135 with 64; the
-// pack of 16 sequences of 16 heads: 1010 and 944.  Two warps that share 16 columns by keys, and add their partial sums
+// about equally busy, 3.4 us a chunk.  (4 x 2048 tokens of 8 heads, prep included: 87 us with 32 columns, 135 with 64; the
+// pack of 16 sequences of 16 heads: 1010 and 934.  Two warps that share 16 columns by keys, and add their partial sums
 // through shared memory, were bound by it: 2.7 us a chunk of 32 columns where the products take 1.0.)
 //
 // Warp matrix instructions and not tcgen05: the chain is bound by its latency, with 32 columns a CTA, and there a
