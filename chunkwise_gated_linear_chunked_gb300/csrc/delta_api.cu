@@ -49,6 +49,19 @@ void place(E *&p, char *base, size_t &at, size_t count)
     at += align_up(count * sizeof(E));
 }
 
+// The chunked forward's workspace.
+size_t place_fwd(DeltaArgs &a, int dtype, char *base)
+{
+    size_t at = 0;
+    if (delta_chunked(dtype, a.K, a.V)) {
+        const size_t cells = (size_t)a.slots * a.HV;
+        place(a.chunk, base, at, cells * delta_cell_bytes(false));
+        if (delta_half(dtype))
+            place(a.score, base, at, cells);
+    }
+    return at;
+}
+
 // The backward's workspace.
 size_t place_bwd(DeltaArgs &a, int dtype, char *base)
 {
@@ -69,6 +82,10 @@ size_t place_bwd(DeltaArgs &a, int dtype, char *base)
         place(t.dots, base, at, cells * columns * 3 * kDeltaChunk);
         place(t.kept, base, at, kept * (a.K / 8) * 32);
         place(t.across, base, at, kept);
+        if (delta_half(dtype)) {
+            place(t.power, base, at, cells * columns * 8);
+            place(a.score, base, at, cells);
+        }
         return at;
     }
     const size_t heads = (size_t)a.rows * a.HV;
@@ -90,12 +107,12 @@ using namespace gla;
 extern "C" size_t gla_delta_fwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen)
 {
     size_t x, o;
-    if (!delta_sizes(dtype, false, x, o) || check_shape(N, B, T, H, HV, K, V, varlen != 0) || !delta_chunked(dtype, K, V))
+    if (!delta_sizes(dtype, false, x, o) || check_shape(N, B, T, H, HV, K, V, varlen != 0))
         return 0;
     DeltaArgs a;
     std::memset(&a, 0, sizeof a);
     plan(a, N, B, T, H, HV, K, V, varlen != 0);
-    return (size_t)a.slots * HV * delta_cell_bytes(false);
+    return place_fwd(a, dtype, nullptr);
 }
 
 extern "C" size_t gla_delta_bwd_workspace_size(int N, int B, int T, int H, int HV, int K, int V, int dtype, int varlen)
@@ -153,8 +170,8 @@ extern "C" int gla_delta_fwd(const void *q, const void *k, const void *v, const 
     if (!delta_chunked(dtype, K, V))
         return profiled(K_DELTA_COLS, s, [&] { return launch_delta_cols(a, dtype, false, s); }) == cudaSuccess
                    ? GLA_OK : GLA_ERR_CUDA;
-    a.chunk = static_cast<char *>(workspace);
-    const bool half = dtype == GLA_F16 || dtype == GLA_F16_OF16;
+    place_fwd(a, dtype, static_cast<char *>(workspace));
+    const bool half = delta_half(dtype);
     if (a.slots && profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, false, s); }) != cudaSuccess)
         return GLA_ERR_CUDA;
     if (profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, false, s); }) != cudaSuccess)
@@ -208,7 +225,7 @@ extern "C" int gla_delta_bwd(const void *q, const void *k, const void *v, const 
         a.hd = nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (delta_chunked(dtype, K, V)) {
-        const bool half = dtype == GLA_F16;
+        const bool half = delta_half(dtype);
         if (a.slots && (profiled(K_DELTA_PREP, s, [&] { return launch_delta_prep(a, half, true, s); }) != cudaSuccess ||
                         profiled(K_DELTA_CHAIN, s, [&] { return launch_delta_chain(a, dtype, true, s); }) != cudaSuccess))
             return GLA_ERR_CUDA;

@@ -43,15 +43,21 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
     const DeltaTrace trace = a.trace;
     const int g16 = (w.v0 >> 4) + group;
 
+    Power in[2] = {{1.f, 1.f}, {1.f, 1.f}};   // fp16: the powers of the columns of dS
     auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4]) {
         const float4 *row = st.cell.row;
         float x[8][4] = {};
         {
             uint32_t s_hi[KD / 16][4];
+            if constexpr (kScaled<T>)
+                if (lane % 4 == 0) {
+                    sh.power[group][lane / 4] = in[0].from;
+                    sh.power[group][lane / 4 + 8] = in[1].from;
+                }
 #pragma unroll
             for (int i = 0; i < KD / 16; ++i) {
                 uint32_t s_lo[4];
-                split_pair<T>(s[2 * i], s[2 * i + 1], s_hi[i], s_lo);
+                split_rows<T>(s[2 * i], s[2 * i + 1], in, s_hi[i], s_lo);
                 sh.state[group][i][0][lane] = as_uint4(s_hi[i]);
                 sh.state[group][i][1][lane] = as_uint4(s_lo);
             }
@@ -65,6 +71,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             for (int e = 0; e < 4; ++e)
                 s[j][e] *= last;
         bar_sync(kBarShare + group);
+        // of products with a column of dS that was divided by its power
+        auto of = [](float f, const Power &p) { return kScaled<T> ? f * p.from : f; };
+        Power by[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {   // g, and x = g + (T' - I) g
             uint32_t hi[4];
@@ -74,13 +83,35 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 const int j = 2 * i + y;
                 const float4 p = sh.ks[group][j][lane];
                 const float f0 = row[8 * j + two].z, f1 = row[8 * j + two + 1].z;
-                r[y][0] = fmaf(f0, x[j][0], p.x), r[y][1] = fmaf(f1, x[j][1], p.y);
-                r[y][2] = fmaf(f0, x[j][2], p.z), r[y][3] = fmaf(f1, x[j][3], p.w);
+                r[y][0] = fmaf(of(f0, in[0]), x[j][0], p.x), r[y][1] = fmaf(of(f1, in[0]), x[j][1], p.y);
+                r[y][2] = fmaf(of(f0, in[1]), x[j][2], p.z), r[y][3] = fmaf(of(f1, in[1]), x[j][3], p.w);
                 x[j][0] = r[y][0], x[j][1] = r[y][1], x[j][2] = r[y][2], x[j][3] = r[y][3];
             }
-            triangle_step<T, true, 2>(x, r[0], r[1], hi, i, st.cell.inverse, lane);
+            if constexpr (!kScaled<T>)
+                triangle_step<T, true, 2>(x, r[0], r[1], hi, i, st.cell.inverse, lane);
         }
+        if constexpr (kScaled<T>)
+            triangle_rows<T, true, 2>(x, st.cell.inverse, lane);
         uint32_t hi[4][4], lo[4][4];
+        auto update = [&](float (&u)[4], int j) {
+            const float4 c0 = row[8 * j + two], c1 = row[8 * j + two + 1];
+            const float f0 = -c0.x * c0.y, f1 = -c1.x * c1.y;
+            u[0] = f0 * x[j][0], u[1] = f1 * x[j][1], u[2] = f0 * x[j][2], u[3] = f1 * x[j][3];
+        };
+        if constexpr (kScaled<T>) {   // they are added to dS: one power for both
+            float most[2] = {};
+            rows_largest(s, most);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float u[1][4];
+                update(u[0], j);
+                rows_largest(u, most);
+            }
+            rows_power<true>(most, by);
+#pragma unroll
+            for (int j = 0; j < KD / 8; ++j)
+                times_rows(s[j], s[j], by[0].to, by[1].to);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float u[2][4];
@@ -88,11 +119,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             for (int y = 0; y < 2; ++y) {
                 const int j = 2 * i + y;
                 sh.n[group][j][lane] = as_float4(x[j]);
-                const float4 c0 = row[8 * j + two], c1 = row[8 * j + two + 1];
-                const float f0 = -c0.x * c0.y, f1 = -c1.x * c1.y;
-                u[y][0] = f0 * x[j][0], u[y][1] = f1 * x[j][1], u[y][2] = f0 * x[j][2], u[y][3] = f1 * x[j][3];
+                update(u[y], j);
             }
-            split_pair<T>(u[0], u[1], hi[i], lo[i]);
+            split_rows<T>(u[0], u[1], by, hi[i], lo[i]);
         }
         bar_tell(kBarRows + group);
         state_add<T, KD>(s, hi, lo, st.k, lane);
@@ -101,14 +130,23 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < KD / 8; ++j) {
             const float4 p = part[j * 32];
-            s[j][0] += p.x, s[j][1] += p.y, s[j][2] += p.z, s[j][3] += p.w;
+            if constexpr (kScaled<T>) {
+                s[j][0] = fmaf(by[0].from, s[j][0], p.x), s[j][1] = fmaf(by[0].from, s[j][1], p.y);
+                s[j][2] = fmaf(by[1].from, s[j][2], p.z), s[j][3] = fmaf(by[1].from, s[j][3], p.w);
+            } else {
+                s[j][0] += p.x, s[j][1] += p.y, s[j][2] += p.z, s[j][3] += p.w;
+            }
         }
+        if constexpr (kScaled<T>)
+            rows_power<true>(s, in);
     };
     constexpr bool kChecked = std::is_same_v<T, __half>;
     bool bad = false;
     auto help = [&](typename Shared::Stage &st, int c) {
         const float4 *row = st.cell.row;
         const size_t cell = (size_t)(w.slot + c) * a.HV + w.hv;
+        const float score = kScaled<T> ? a.score[cell] : 1.f;   // P's factor
+        float in_from[2] = {1.f, 1.f};
         uint32_t d_hi[4][4], d_lo[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -126,6 +164,12 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
         {
             uint32_t s_in[KD / 16][4];
             float k[8][4] = {};
+            if constexpr (kScaled<T>) {
+                in_from[0] = sh.power[group][lane / 4], in_from[1] = sh.power[group][lane / 4 + 8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    times_rows(g[j], g[j], score, score);
+            }
 #pragma unroll
             for (int i = 0; i < KD / 16; ++i)
                 take(s_in[i], sh.state[group][i][1][lane]);
@@ -133,6 +177,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float f0 = row[8 * j + two].z, f1 = row[8 * j + two + 1].z;
+                if constexpr (kScaled<T>)
+                    times_rows(k[j], k[j], in_from[0], in_from[1]);
                 sh.ks[group][j][lane] = make_float4(fmaf(f0, k[j][0], g[j][0]), fmaf(f1, k[j][1], g[j][1]), fmaf(f0, k[j][2], g[j][2]),
                                                     fmaf(f1, k[j][3], g[j][3]));
             }
@@ -140,23 +186,47 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < KD / 16; ++i)
                 take(s_in[i], sh.state[group][i][0][lane]);
+            if constexpr (kScaled<T>) {
+                const float most = group_power(in_from);
+                to_group<KD / 16>(s_in, in_from, most);
+                if (on && lane == 0)
+                    trace.power[(cell * (a.V / 16) + g16) * 8 + 4] = most;
+            }
             if (on)
                 put_blocks<KD / 16>(trace.ds + cell * trace.s_size, s_in, 2 * g16, KD / 8, lane);
         }
         {   // (scale e^G dO)' q, to where the state's rounded values lay
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float r[2][4];
+            auto started = [&](float (&r)[2][4], int i) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float f0 = row[16 * i + 8 * e + two].w, f1 = row[16 * i + 8 * e + two + 1].w;
                     const float2 d0 = widen2<T>(d_hi[i][2 * e]), d1 = widen2<T>(d_hi[i][2 * e + 1]);
                     r[e][0] = f0 * d0.x, r[e][1] = f1 * d0.y, r[e][2] = f0 * d1.x, r[e][3] = f1 * d1.y;
                 }
-                split_pair<T>(r[0], r[1], d_hi[i], d_lo[i]);
+            };
+            Power by[2];
+            if constexpr (kScaled<T>) {
+                float most[2] = {};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float r[2][4];
+                    started(r, i);
+                    rows_largest(r, most);
+                }
+                rows_power<false>(most, by);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float r[2][4];
+                started(r, i);
+                split_rows<T>(r[0], r[1], by, d_hi[i], d_lo[i]);
             }
             float s[KD / 8][4] = {};
             state_add<T, KD>(s, d_hi, d_lo, st.q, lane);
+            if constexpr (kScaled<T>)
+#pragma unroll
+                for (int j = 0; j < KD / 8; ++j)
+                    times_rows(s[j], s[j], by[0].from, by[1].from);
             float4 *part = reinterpret_cast<float4 *>(sh.state[group]) + lane;
             __syncwarp();   // all lanes have the rounded values
 #pragma unroll
@@ -172,6 +242,19 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
         const int rows = min(kDeltaChunk, w.len - c * kDeltaChunk);
         T *dv = static_cast<T *>(a.dv) + (((size_t)w.bos + (size_t)c * kDeltaChunk) * a.HV + w.hv) * a.V + col;
         float sum[32];   // x.Y, then dv.v
+        Power to_x = {1.f, 1.f};
+        if constexpr (kScaled<T>) {   // beta x goes to the gradients of k, as a group's columns have one power
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 x = sh.n[group][j][lane];
+                const float b0 = row[8 * j + two].x, b1 = row[8 * j + two + 1].x;
+                most = fmaxf(most, fmaxf(fmaxf(fabsf(b0 * x.x), fabsf(b1 * x.y)), fmaxf(fabsf(b0 * x.z), fabsf(b1 * x.w))));
+            }
+            to_x = power_of<false>(warp_largest(most));
+            if (on && lane == 0)
+                trace.power[(cell * (a.V / 16) + g16) * 8 + 5] = to_x.from;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t v[4], xw[4];
@@ -184,8 +267,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 if constexpr (kChecked)
                     bad |= lost(x.x) || lost(x.y) || lost(x.z) || lost(x.w);
                 const float2 v0 = widen2<T>(v[2 * e]), v1 = widen2<T>(v[2 * e + 1]);
-                xw[2 * e] = narrow2<T>(make_float2(x.x, x.y));
-                xw[2 * e + 1] = narrow2<T>(make_float2(x.z, x.w));
+                const float r0 = kScaled<T> ? b0 * to_x.to : 1.f, r1 = kScaled<T> ? b1 * to_x.to : 1.f;
+                xw[2 * e] = narrow2<T>(make_float2(r0 * x.x, r1 * x.y));
+                xw[2 * e + 1] = narrow2<T>(make_float2(r0 * x.z, r1 * x.w));
                 sum[2 * j] = fmaf(x.x, y[j].x, x.z * y[j].z);
                 sum[2 * j + 1] = fmaf(x.y, y[j].y, x.w * y[j].w);
                 sum[16 + 2 * j] = b0 * fmaf(x.x, v0.x, x.z * v1.x);
@@ -243,7 +327,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
 #pragma unroll
             for (int j = 0; j < KD / 8; ++j) {
                 const float4 p = kept[j * 32];
-                const float2 d0 = in_two<T>(s[j][0], s[j][1]), d1 = in_two<T>(s[j][2], s[j][3]);
+                const float2 d0 = in_two<T>(s[j][0], s[j][1], in[0]), d1 = in_two<T>(s[j][2], s[j][3], in[1]);
                 sum += (p.x * d0.x + p.y * d0.y) + (p.z * d1.x + p.w * d1.y);
             }
 #pragma unroll
@@ -252,6 +336,8 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             if (lane == 0)
                 trace.across[at] = sum;
         };
+        if constexpr (kScaled<T>)
+            rows_power<true>(s, in);
         if (on && w.chunks)
             across(w.chunks - 1);
         walk([&](auto &st, int c) {

@@ -51,11 +51,17 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     const bool on = w.v0 + 16 * group < a.V;   // whole groups of 16 columns
     const size_t state = (w.head * a.K + two) * a.V;
 
+    Power in[2] = {{1.f, 1.f}, {1.f, 1.f}};   // fp16: the powers that the state's columns are held over
     auto chain = [&](typename Shared::Stage &st, float (&s)[KD / 8][4], bool end) {
         const float4 *row = st.cell.row;
         float n[8][4] = {};
         {
             uint32_t s_hi[KD / 16][4];
+            if constexpr (kScaled<T>)
+                if (lane % 4 == 0) {
+                    sh.power[group][lane / 4] = in[0].from;
+                    sh.power[group][lane / 4 + 8] = in[1].from;
+                }
 #pragma unroll
             for (int i = 0; i < KD / 16; ++i) {
                 uint32_t s_lo[4];
@@ -72,7 +78,15 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 s[j][e] *= last;
+        float most[2] = {};
+        if constexpr (kScaled<T>) {
+            rows_largest(s, most);
+            most[0] *= in[0].from, most[1] *= in[1].from;
+        }
         bar_sync(kBarShare + group);
+        // of products with a column of the state that was divided by its power
+        auto of = [](float f, const Power &p) { return kScaled<T> ? f * p.from : f; };
+        Power by[2];
 #pragma unroll
         for (int i = 3; i >= 0; --i) {   // R, and Y = R + (T^ - I) R
             uint32_t v[4], hi[4];
@@ -84,15 +98,36 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 const float4 p = sh.ks[group][j][lane];
                 const float f0 = row[8 * j + two].y, f1 = row[8 * j + two + 1].y;
                 const float2 v0 = widen2<T>(v[2 * y]), v1 = widen2<T>(v[2 * y + 1]);
-                r[y][0] = fmaf(-f0, n[j][0] + p.x, v0.x);
-                r[y][1] = fmaf(-f1, n[j][1] + p.y, v0.y);
-                r[y][2] = fmaf(-f0, n[j][2] + p.z, v1.x);
-                r[y][3] = fmaf(-f1, n[j][3] + p.w, v1.y);
+                r[y][0] = fmaf(-of(f0, in[0]), n[j][0] + p.x, v0.x);
+                r[y][1] = fmaf(-of(f1, in[0]), n[j][1] + p.y, v0.y);
+                r[y][2] = fmaf(-of(f0, in[1]), n[j][2] + p.z, v1.x);
+                r[y][3] = fmaf(-of(f1, in[1]), n[j][3] + p.w, v1.y);
                 n[j][0] = r[y][0], n[j][1] = r[y][1], n[j][2] = r[y][2], n[j][3] = r[y][3];
             }
-            triangle_step<T, false, 2>(n, r[0], r[1], hi, i, st.cell.inverse, lane);
+            if constexpr (!kScaled<T>)
+                triangle_step<T, false, 2>(n, r[0], r[1], hi, i, st.cell.inverse, lane);
         }
+        if constexpr (kScaled<T>)
+            triangle_rows<T, false, 2>(n, st.cell.inverse, lane);
         uint32_t hi[4][4], lo[4][4], least[kThree ? 4 : 1][4];
+        auto update = [&](float (&u)[4], int j) {   // rows that update the state, as its end has them
+            const float4 c0 = row[8 * j + two], c1 = row[8 * j + two + 1];
+            const float f0 = c0.z * c0.x, f1 = c1.z * c1.x;
+            u[0] = f0 * n[j][0], u[1] = f1 * n[j][1], u[2] = f0 * n[j][2], u[3] = f1 * n[j][3];
+        };
+        if constexpr (kScaled<T>) {   // they are added to the state: one power for both
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float u[1][4];
+                update(u[0], j);
+                rows_largest(u, most);
+            }
+            rows_power<true>(most, by);
+            const float f0 = in[0].from * by[0].to, f1 = in[1].from * by[1].to;
+#pragma unroll
+            for (int j = 0; j < KD / 8; ++j)
+                times_rows(s[j], s[j], f0, f1);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float u[2][4];
@@ -100,17 +135,17 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             for (int y = 0; y < 2; ++y) {
                 const int j = 2 * i + y;
                 sh.n[group][j][lane] = as_float4(n[j]);
-                const float4 c0 = row[8 * j + two], c1 = row[8 * j + two + 1];
-                const float f0 = c0.z * c0.x, f1 = c1.z * c1.x;
-                u[y][0] = f0 * n[j][0], u[y][1] = f1 * n[j][1], u[y][2] = f0 * n[j][2], u[y][3] = f1 * n[j][3];
+                update(u[y], j);
             }
             if constexpr (kThree)
                 split_pair<T>(u[0], u[1], hi[i], lo[i], least[i]);
             else
-                split_pair<T>(u[0], u[1], hi[i], lo[i]);
+                split_rows<T>(u[0], u[1], by, hi[i], lo[i]);
         }
         bar_tell(kBarRows + group);
         state_add<T, KD>(s, hi, lo, st.k, lane);
+        if constexpr (kScaled<T>)
+            in[0] = by[0], in[1] = by[1];
         if constexpr (kThree)
             if (end)
                 state_add<T, KD>(s, least, st.k, lane);
@@ -123,7 +158,11 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
         const float4 *row = st.cell.row;
         const size_t cell = (size_t)(w.slot + c) * a.HV + w.hv;
         float o[8][4] = {};
+        const float score = kScaled<T> ? a.score[cell] : 1.f;   // P's factor
         bar_sync(kBarState + group);
+        float in[2] = {1.f, 1.f};
+        if constexpr (kScaled<T>)
+            in[0] = sh.power[group][lane / 4], in[1] = sh.power[group][lane / 4 + 8];
         {
             uint32_t s_hi[KD / 16][4], s_lo[KD / 16][4];
 #pragma unroll
@@ -139,30 +178,75 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < KD / 16; ++i)
                 take(s_hi[i], sh.state[group][i][0][lane]);
-            if (SAVE && on)
-                put_blocks<KD / 16>(trace.s + cell * trace.s_size, s_hi, 2 * g16, KD / 8, lane);
+            if constexpr (!kScaled<T>)
+                if (SAVE && on)
+                    put_blocks<KD / 16>(trace.s + cell * trace.s_size, s_hi, 2 * g16, KD / 8, lane);
             state_by_rows<T, KD, true>(o, s_hi, s_lo, st.q, lane);
+            if constexpr (SAVE && kScaled<T>) {
+                const float most = group_power(in);
+                to_group<KD / 16>(s_hi, in, most);
+                if (on) {
+                    put_blocks<KD / 16>(trace.s + cell * trace.s_size, s_hi, 2 * g16, KD / 8, lane);
+                    if (lane == 0)
+                        trace.power[(cell * (a.V / 16) + g16) * 8] = most;
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float f0 = row[8 * j + two].w, f1 = row[8 * j + two + 1].w;
-            o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
+            if constexpr (kScaled<T>)
+                o[j][0] *= f0 * in[0], o[j][1] *= f1 * in[0], o[j][2] *= f0 * in[1], o[j][3] *= f1 * in[1];
+            else
+                o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
         }
         bar_sync(kBarRows + group);
         uint32_t hi[4][4];
+        if constexpr (kScaled<T>) {
+            float n[8][4], p[8][4] = {};
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-            float n[2][4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int j = 2 * i + y;
-                const float4 p = sh.n[group][j][lane];
+            for (int j = 0; j < 8; ++j) {
+                const float4 y = sh.n[group][j][lane];
                 if (SAVE && on)
-                    trace.y[(cell * (a.V / 16) + g16) * 256 + j * 32 + lane] = p;
+                    trace.y[(cell * (a.V / 16) + g16) * 256 + j * 32 + lane] = y;
                 const float b0 = row[8 * j + two].x, b1 = row[8 * j + two + 1].x;
-                n[y][0] = b0 * p.x, n[y][1] = b1 * p.y, n[y][2] = b0 * p.z, n[y][3] = b1 * p.w;
+                n[j][0] = b0 * y.x, n[j][1] = b1 * y.y, n[j][2] = b0 * y.z, n[j][3] = b1 * y.w;
             }
-            triangle_step<T, false, kThree ? 3 : 2, SAVE>(o, n[0], n[1], hi[i], i, st.cell.score, lane);
+            Power by[2];
+            rows_power<false>(n, by);
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                times_rows(n[2 * i], n[2 * i], by[0].to, by[1].to);
+                times_rows(n[2 * i + 1], n[2 * i + 1], by[0].to, by[1].to);
+                triangle_step<T, false, 2, SAVE>(p, n[2 * i], n[2 * i + 1], hi[i], i, st.cell.score, lane);
+            }
+            const float f0 = score * by[0].from, f1 = score * by[1].from;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j][0] = fmaf(f0, p[j][0], o[j][0]), o[j][1] = fmaf(f0, p[j][1], o[j][1]);
+                o[j][2] = fmaf(f1, p[j][2], o[j][2]), o[j][3] = fmaf(f1, p[j][3], o[j][3]);
+            }
+            if constexpr (SAVE) {
+                const float from[2] = {by[0].from, by[1].from}, most = group_power(from);
+                to_group<4>(hi, from, most);
+                if (on && lane == 0)
+                    trace.power[(cell * (a.V / 16) + g16) * 8 + 1] = most;
+            }
+        } else {
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                float n[2][4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = 2 * i + y;
+                    const float4 p = sh.n[group][j][lane];
+                    if (SAVE && on)
+                        trace.y[(cell * (a.V / 16) + g16) * 256 + j * 32 + lane] = p;
+                    const float b0 = row[8 * j + two].x, b1 = row[8 * j + two + 1].x;
+                    n[y][0] = b0 * p.x, n[y][1] = b1 * p.y, n[y][2] = b0 * p.z, n[y][3] = b1 * p.w;
+                }
+                triangle_step<T, false, kThree ? 3 : 2, SAVE>(o, n[0], n[1], hi[i], i, st.cell.score, lane);
+            }
         }
         if constexpr (kChecked)
 #pragma unroll
@@ -174,6 +258,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             if (on)
                 put_blocks<4>(trace.n + cell * trace.n_size, hi, 2 * g16, 8, lane);
             float sum[16];   // o.dO of this lane's columns, of rows 8 j + two and + 1
+            float most = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t d[4];
@@ -181,10 +266,17 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const float2 d0 = widen2<T>(d[2 * y]), d1 = widen2<T>(d[2 * y + 1]);
+                    if constexpr (kScaled<T>)
+                        most = fmaxf(fmaxf(most, fmaxf(fabsf(d0.x), fabsf(d0.y))), fmaxf(fabsf(d1.x), fabsf(d1.y)));
                     const float(&r)[4] = o[2 * i + y];
                     sum[4 * i + 2 * y] = fmaf(r[0], d0.x, r[2] * d1.x);
                     sum[4 * i + 2 * y + 1] = fmaf(r[1], d0.y, r[3] * d1.y);
                 }
+            }
+            if constexpr (kScaled<T>) {
+                most = warp_largest(most);
+                if (on && lane == 0)
+                    trace.power[(cell * (a.V / 16) + g16) * 8 + 2] = power_of<false>(most).from;
             }
             // over the eight lanes of a row pair: of the 16 sums each lane is left with two, rows of tile lane / 4
             sum_over_columns<16>(sum, lane);
@@ -227,15 +319,29 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
     if (!output) {
         float s[KD / 8][4];
         state_io<KD>(s, nullptr, a.h0, state, a.V, col, on, false);
+        if constexpr (kScaled<T>) {
+            rows_power<true>(s, in);
+#pragma unroll
+            for (int j = 0; j < KD / 8; ++j)
+                times_rows(s[j], s[j], in[0].to, in[1].to);
+        }
         walk([&](auto &st, int c) {
             chain(st, s, c + 1 == w.chunks);
             if (SAVE && on && ((c + 1) % kDeltaKept == 0 || c + 1 == w.chunks)) {
                 float4 *to = a.trace.kept + delta_kept_at(a, w.n, c, w.hv, g16) * (KD / 8 * 32) + lane;
 #pragma unroll
-                for (int j = 0; j < KD / 8; ++j)
-                    to[j * 32] = as_float4(s[j]);
+                for (int j = 0; j < KD / 8; ++j) {
+                    float r[4] = {s[j][0], s[j][1], s[j][2], s[j][3]};
+                    if constexpr (kScaled<T>)
+                        times_rows(r, r, in[0].from, in[1].from);
+                    to[j * 32] = as_float4(r);
+                }
             }
         });
+        if constexpr (kScaled<T>)
+#pragma unroll
+            for (int j = 0; j < KD / 8; ++j)
+                times_rows(s[j], s[j], in[0].from, in[1].from);
         report_lost<T>(a, s, false);
         if (!SAVE && a.ht)
             state_io<KD>(s, a.ht, nullptr, state, a.V, col, on, true);

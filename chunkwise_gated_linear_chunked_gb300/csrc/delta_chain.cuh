@@ -22,6 +22,7 @@ struct ChainShared {
     static_assert(sizeof(Stage) % 1024 == 0, "swizzled tiles start on 1024 bytes");
     uint4 state[VG][KD / 16][2][32];     // the chain's rounded S and its remainders, as left operands
     float4 ks[VG][8][32], n[VG][8][32];  // the remainders' share of k S; Y
+    float power[VG][16];                 // fp16: what the columns of the rounded state were divided by
     uint64_t full[2];
 };
 
@@ -73,6 +74,28 @@ __device__ __forceinline__ void triangle_step(float (&c)[8][4], const float (&v0
                 else if (term == 4 && ALL)
                     mma<T>(c[j], mid, b[j].z, b[j].w);
             }
+}
+
+// The same over all steps (fp16), times the powers of c's rows: c += c (the triangle).
+template <typename T, bool UPPER, int TERMS>
+__device__ __forceinline__ void triangle_rows(float (&c)[8][4], const uint4 *m, int lane)
+{
+    Power by[2];
+    rows_power<false>(c, by);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        times_rows(c[j], c[j], by[0].to, by[1].to);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int i = UPPER ? x : 3 - x;
+        uint32_t hi[4];
+        const float v0[4] = {c[2 * i][0], c[2 * i][1], c[2 * i][2], c[2 * i][3]};
+        const float v1[4] = {c[2 * i + 1][0], c[2 * i + 1][1], c[2 * i + 1][2], c[2 * i + 1][3]};
+        triangle_step<T, UPPER, TERMS>(c, v0, v1, hi, i, m, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        times_rows(c[j], c[j], by[0].from, by[1].from);
 }
 
 // Offset of 16-byte unit u (eight keys) of row r in a tile of 64 keys of 64 rows.
@@ -163,6 +186,27 @@ __device__ __forceinline__ void put_blocks(uint32_t *to, const uint32_t (&r)[STE
 #pragma unroll
         for (int e = 0; e < 4; ++e)   // rows + 8 (e & 1), columns + 8 (e >> 1)
             to[((block_row + (e & 1)) * across + 2 * i + (e >> 1)) * 32 + lane] = r[i][e];
+}
+
+// The largest of a group's 16 columns' powers, of which each lane has those of its two rows.
+__device__ __forceinline__ float group_power(const float (&p)[2])
+{
+    float most = fmaxf(p[0], p[1]);
+#pragma unroll
+    for (int m = 4; m < 32; m *= 2)
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
+    return most;
+}
+// Rounded values (left operands) of columns divided by their own powers, divided by the group's; in place.
+template <int STEPS>
+__device__ __forceinline__ void to_group(uint32_t (&r)[STEPS][4], const float (&p)[2], float group)
+{
+    const float f0 = p[0] * inverse_power(group), f1 = p[1] * inverse_power(group);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r[i][e] = times_power(r[i][e], e & 1 ? f1 : f0);
 }
 
 // Sums over the eight lanes that share lane % 4 of N values each: lane is left with those from N / 8 (lane / 4) on.

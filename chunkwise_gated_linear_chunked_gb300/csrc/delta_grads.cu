@@ -29,6 +29,7 @@ struct GradShared {
         uint32_t s[8][KD / 8][32], ds[8][KD / 8][32];   // columns by keys
         float4 row[kDeltaChunk];
         float2 gate[kDeltaChunk];
+        float power[16][8];                        // fp16: of the head's groups of 16 columns (DeltaTrace)
     } stage[2];
     uint16_t p[64][72], b[64][72];
     uint64_t full[2];
@@ -96,14 +97,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
         uint64_t *bar = &sh.full[p.turn & 1];
         const int hv = p.h * per + p.v, blocks = min(8, (a.V - 64 * p.c) / 8);   // rows of blocks
         const bool begins = p.v == 0 && p.c == 0;
-        const uint32_t narrow_bytes = blocks * 8 * 128, wide_bytes = blocks * (KD / 8) * 128;
+        const uint32_t narrow_bytes = blocks * 8 * 128, wide_bytes = blocks * (KD / 8) * 128, power_bytes = a.V / 16 * sizeof st.power[0];
         const size_t cell = (size_t)p.slot * a.HV + hv;
         const size_t narrow_at = cell * a.trace.n_size + (size_t)p.c * 8 * 8 * 32, wide_at = cell * a.trace.s_size + (size_t)p.c * 8 * (KD / 8) * 32;
         const char *from = a.chunk + cell * sizeof(DeltaCellBack);
         switch (tid / 32) {
         case 0:
             tc::bar_expect_tx(bar, (uint32_t)(sizeof st.d + 2 * narrow_bytes + 2 * wide_bytes + sizeof st.row + sizeof st.gate +
-                                              (begins ? sizeof sh.rows[0] : 0)));
+                                              (kScaled<T> ? power_bytes : 0) + (begins ? sizeof sh.rows[0] : 0)));
             copy_bulk(st.s, a.trace.s + wide_at, wide_bytes, bar);
             break;
         case 1: copy_bulk(st.ds, a.trace.ds + wide_at, wide_bytes, bar); break;
@@ -113,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
         case 5:
             copy_bulk(st.row, from + kCellRows, sizeof st.row, bar);
             copy_bulk(st.gate, from + sizeof(DeltaCellBack) - sizeof st.gate, sizeof st.gate, bar);
+            if constexpr (kScaled<T>)
+                copy_bulk(st.power, a.trace.power + cell * (a.V / 16) * 8, power_bytes, bar);
             break;
         case 6:
             if (begins)
@@ -167,17 +170,40 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
             __syncthreads();
         }
         const int steps = min(4, (a.V - 64 * now.c) / 16);
+        // fp16: the largest powers of the head's columns.  Products are sums over columns: each group's operands are taken
+        // over the largest, and what comes of them times it
+        float most[6] = {};
+        auto over = [](uint32_t (&f)[4], float p) {
+            if constexpr (kScaled<T>)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[e] = times_power(f[e], p);
+        };
+        if constexpr (kScaled<T>)
+            for (int g = 0; g < a.V / 16; ++g)
+#pragma unroll
+                for (int e = 0; e < 6; ++e)
+                    if (e != 3)
+                        most[e] = fmaxf(most[e], st.power[g][e]);
         for (int s = 0; s < steps; ++s) {
             uint32_t fd[4], fx[4], fn[4];
+            float p_s = 1.f, p_n = 1.f, p_ds = 1.f;
             ldsm(fd, tc::smem_u32(st.d) + unit_at(16 * r + lane % 16, 2 * s + lane / 16));
             blocks_t<false>(fx, &st.x[0][0][0], 8, 2 * s, 2 * r, lane);
             blocks_t<false>(fn, &st.n[0][0][0], 8, 2 * s, 2 * r, lane);
+            if constexpr (kScaled<T>) {
+                const float *p = st.power[4 * now.c + s];
+                p_s = p[0] * inverse_power(most[0]), p_n = p[1] * inverse_power(most[1]), p_ds = p[4] * inverse_power(most[4]);
+                over(fx, p[5] * inverse_power(most[5]));
+                over(fn, p_n);
+            }
 #pragma unroll
             for (int p = 0; p < 2; ++p) {   // columns of p, or of b, in this block of rows
                 if (2 * (h & 1) + p > r)
                     break;
                 uint32_t f[4];
                 blocks_t<true>(f, &st.n[0][0][0], 8, 2 * s, 4 * (h & 1) + 2 * p, lane);
+                over(f, p_n);
                 mma<T>(m[2 * p], h > 1 ? fx : fd, f[0], f[1]);
                 mma<T>(m[2 * p + 1], h > 1 ? fx : fd, f[2], f[3]);
             }
@@ -186,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
                 uint32_t f[4], g[4];
                 blocks_t<true>(f, &st.s[0][0][0], KD / 8, 2 * s, h * NT + 2 * p, lane);
                 blocks_t<true>(g, &st.ds[0][0][0], KD / 8, 2 * s, h * NT + 2 * p, lane);
+                over(f, p_s);
+                over(g, p_ds);
                 mma<T>(ds[2 * p], fd, f[0], f[1]);
                 mma<T>(ds[2 * p + 1], fd, f[2], f[3]);
                 mma<T>(xs[2 * p], fx, f[0], f[1]);
@@ -197,7 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
         if ((now.c + 1) * 64 >= a.V) {   // the value head's last columns
             const float4 c0 = st.row[i0], c1 = st.row[i0 + 8];
             const float2 g0 = st.gate[i0], g1 = st.gate[i0 + 8];
-            const float f0 = h > 1 ? -c0.x : a.scale, f1 = h > 1 ? -c1.x : a.scale;
+            // fp16: p over scale and the powers of dO and N, b over those of beta x and N
+            const float by = h > 1 ? -1.f : inverse_power(most[2]);
+            const float f0 = kScaled<T> ? by : h > 1 ? -c0.x : a.scale, f1 = kScaled<T> ? by : h > 1 ? -c1.x : a.scale;
+            const float of_p = a.scale * most[1] * most[2], of_b = most[1] * most[5];
             uint16_t(*to)[72] = h > 1 ? sh.b : sh.p;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
@@ -219,10 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float4 &c = e < 2 ? c0 : c1;
-                    dq[j][e] = fmaf(c.w, ds[j][e], dq[j][e]);
-                    dk[j][e] = fmaf(c.z, nd[j][e], fmaf(-c.x * c.y, xs[j][e], dk[j][e]));
+                    if constexpr (kScaled<T>) {
+                        dq[j][e] = fmaf(c.w * most[0], ds[j][e], dq[j][e]);
+                        dk[j][e] = fmaf(c.z * (most[1] * most[4]), nd[j][e], fmaf(-c.y * (most[5] * most[0]), xs[j][e], dk[j][e]));
+                    } else {
+                        dq[j][e] = fmaf(c.w, ds[j][e], dq[j][e]);
+                        dk[j][e] = fmaf(c.z, nd[j][e], fmaf(-c.x * c.y, xs[j][e], dk[j][e]));
+                    }
                 }
             clear(m), clear(ds), clear(xs), clear(nd);
+            float(&pk)[NT][4] = kScaled<T> ? ds : dq, (&bk)[NT][4] = kScaled<T> ? xs : dk, (&pq)[NT][4] = kScaled<T> ? nd : dk;
             __syncthreads();
             const int m8 = lane / 8;
             for (int s = 0; s < 4; ++s) {
@@ -242,19 +279,33 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
                     const uint32_t at = unit_at(16 * s + (lane & 15), key % 64 / 8 + lane / 16);
                     ldsm_t(f, tc::smem_u32(rows.k[key / 64]) + at);
                     if (s <= r) {
-                        mma<T>(dq[2 * p], fp, f[0], f[1]);
-                        mma<T>(dq[2 * p + 1], fp, f[2], f[3]);
-                        mma<T>(dk[2 * p], fb, f[0], f[1]);
-                        mma<T>(dk[2 * p + 1], fb, f[2], f[3]);
+                        mma<T>(pk[2 * p], fp, f[0], f[1]);
+                        mma<T>(pk[2 * p + 1], fp, f[2], f[3]);
+                        mma<T>(bk[2 * p], fb, f[0], f[1]);
+                        mma<T>(bk[2 * p + 1], fb, f[2], f[3]);
                     }
                     if (s >= r) {
-                        mma<T>(dk[2 * p], fu, f[0], f[1]);
-                        mma<T>(dk[2 * p + 1], fu, f[2], f[3]);
+                        mma<T>(bk[2 * p], fu, f[0], f[1]);
+                        mma<T>(bk[2 * p + 1], fu, f[2], f[3]);
                         ldsm_t(f, tc::smem_u32(rows.q[key / 64]) + at);
-                        mma<T>(dk[2 * p], ft, f[0], f[1]);
-                        mma<T>(dk[2 * p + 1], ft, f[2], f[3]);
+                        mma<T>(pq[2 * p], ft, f[0], f[1]);
+                        mma<T>(pq[2 * p + 1], ft, f[2], f[3]);
                     }
                 }
+            }
+            if constexpr (kScaled<T>) {
+                bool bad = false;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dq[j][e] = fmaf(of_p, pk[j][e], dq[j][e]);
+                        dk[j][e] = fmaf(of_b, bk[j][e], fmaf(of_p, pq[j][e], dk[j][e]));
+                        bad |= lost(dq[j][e]) || lost(dk[j][e]);
+                    }
+                if (bad)
+                    report(a.status, GLA_ERR_RANGE);
+                clear(pk), clear(bk), clear(pq);
             }
             if (now.v + 1 == per) {   // by way of the keys' and queries' place, to rows of whole units
                 __syncthreads();

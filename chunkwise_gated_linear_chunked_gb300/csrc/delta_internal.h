@@ -16,6 +16,8 @@ struct DeltaTrace {
     float *dots;                       // [cell][V / 16][3][64] o.dO, x.Y and dv.v over 16 columns
     float4 *kept;                      // [kept group][HV][V / 16][K / 8][32] states at the ends of groups of chunks
     float *across;                     // [kept group][HV][V / 16] their products with their gradients
+    float *power;                      // fp16: [cell][V / 16][8] powers of two that the 16 columns of S, N, dO (0 .. 2), dS and
+                                       // beta x (4, 5) were divided by
     size_t s_size, n_size;
 };
 
@@ -39,6 +41,7 @@ struct DeltaArgs {
     float *hd;                         // [N, HV, K]: rows of <ht, dht>
     // workspace of the chunked kernels
     char *chunk;                       // cells (DeltaCell, or DeltaCellBack)
+    float *score;                      // fp16: [cell] factor of P, which is stored with its largest q.k in [1, 2)
     DeltaTrace trace;
 };
 
@@ -116,6 +119,7 @@ __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int &n
     return true;
 }
 
+inline bool delta_half(int dtype) { return dtype == GLA_F16 || dtype == GLA_F16_OF16; }
 // 16-bit inputs whose keys are whole warp products and whose values are whole groups of 16 columns go in chunks.
 inline bool delta_chunked(int dtype, int K, int V) { return dtype != GLA_F32 && (K == 64 || K == 128) && V % 16 == 0; }
 size_t delta_cell_bytes(bool backward);

@@ -19,7 +19,7 @@ namespace gla {
 constexpr int kTriangle = 20, kFragments = kTriangle * 32;
 struct DeltaCell {
     uint4 inverse[kFragments];   // T^ - I, T^ = (I + L diag(beta))^-1, L_ij = e^(G_i - G_j) k_i.k_j below the diagonal
-    uint4 score[kFragments];     // P_ij = scale e^(G_i - G_j) q_i.k_j up to the diagonal
+    uint4 score[kFragments];     // P_ij = scale e^(G_i - G_j) q_i.k_j up to the diagonal (fp16: over DeltaArgs::score)
     float4 row[kDeltaChunk];
 };
 struct DeltaCellBack : DeltaCell {   // and transposed: rows and columns of the tiles' numbers run from the other end
@@ -61,13 +61,80 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 
-// Two values as 16-bit ones and their remainders: bf16 keeps 2^-18 of the value, fp16 2^-22 (down to 2^-25 in all).
+// Two values as 16-bit ones and their remainders: bf16 keeps 2^-18 of the value, fp16 2^-22 (down to 2^-25 in all: Power).
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
 {
     hi = narrow2<T>(make_float2(x, y));
     const float2 h = widen2<T>(hi);
     lo = narrow2<T>(make_float2(x - h.x, y - h.y));
+}
+
+// Powers of two for operands of fp16, whose remainders end at 2^-25 whatever the value is: a row of a left operand (a column of
+// the state, of the rows that update it, of their gradients) goes in times `to`, which takes its largest value to [1, 2), and
+// what comes of it is taken times `from`.  Both are exact, so that fp16's operands are within 2^-22 of a row's largest value
+// however small that is.  bf16 has fp32's range: kScaled is false, and nothing of this is compiled.  The price in fp16 (times of
+// operands as they are, where values of 1e-4 leave 1e-2 in the gradients): 4 x 2048 tokens of 8 heads forward 129 us (100),
+// backward 380 (309); packs of 16 and 8 sequences of 16 heads 1074 (971) and 1036 (911).
+template <typename T>
+constexpr bool kScaled = std::is_same_v<T, __half>;
+struct Power {
+    float to, from;
+};
+// For a largest magnitude.  STATE: of what the next chunk adds to as it is, which is left 2^4 to grow (a chunk's rows add at
+// most 64 times the largest of them and the keys' length), and not divided: a state that leaves fp16's range is reported.
+template <bool STATE>
+__device__ __forceinline__ Power power_of(float largest)
+{
+    const uint32_t at = (__float_as_uint(largest) >> 23) + (STATE ? 4u : 0u), e = min(max(at, 27u), STATE ? 127u : 227u);
+    return {__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};   // 2^-100 to 2^100 (STATE: to 1)
+}
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
+// Largest magnitudes of a lane's two rows (of the result's, over the four lanes that share them).
+template <int N>
+__device__ __forceinline__ void rows_largest(const float (&c)[N][4], float (&most)[2])
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        most[0] = fmaxf(most[0], fmaxf(fabsf(c[j][0]), fabsf(c[j][1])));
+        most[1] = fmaxf(most[1], fmaxf(fabsf(c[j][2]), fabsf(c[j][3])));
+    }
+}
+template <bool STATE>
+__device__ __forceinline__ void rows_power(float (&most)[2], Power (&p)[2])
+{
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        most[x] = fmaxf(most[x], __shfl_xor_sync(~0u, most[x], 1));
+        most[x] = fmaxf(most[x], __shfl_xor_sync(~0u, most[x], 2));
+        p[x] = power_of<STATE>(most[x]);
+    }
+}
+template <bool STATE, int N>
+__device__ __forceinline__ void rows_power(const float (&c)[N][4], Power (&p)[2])
+{
+    float most[2] = {};
+    rows_largest(c, most);
+    rows_power<STATE>(most, p);
+}
+__device__ __forceinline__ float warp_largest(float v)
+{
+#pragma unroll
+    for (int m = 16; m; m /= 2)
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, m));
+    return v;
+}
+// d = a result's tile times its rows' factors.
+__device__ __forceinline__ void times_rows(float (&d)[4], const float (&c)[4], float f0, float f1)
+{
+    d[0] = f0 * c[0], d[1] = f0 * c[1], d[2] = f1 * c[2], d[3] = f1 * c[3];
+}
+// Two fp16 values times a power of two of at most 1 (what falls below 2^-25 is lost).
+__device__ __forceinline__ uint32_t times_power(uint32_t v, float p)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(p));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // A left operand's 16 columns from two adjacent results.
@@ -79,6 +146,19 @@ __device__ __forceinline__ void split_pair(const float (&c0)[4], const float (&c
     split2<T>(c1[0], c1[1], hi[2], lo[2]);
     split2<T>(c1[2], c1[3], hi[3], lo[3]);
 }
+// The same times the rows' powers (fp16 alone).
+template <typename T>
+__device__ __forceinline__ void split_rows(const float (&c0)[4], const float (&c1)[4], const Power (&p)[2], uint32_t (&hi)[4], uint32_t (&lo)[4])
+{
+    if constexpr (kScaled<T>) {
+        float d0[4], d1[4];
+        times_rows(d0, c0, p[0].to, p[1].to);
+        times_rows(d1, c1, p[0].to, p[1].to);
+        split_pair<T>(d0, d1, hi, lo);
+    } else {
+        split_pair<T>(c0, c1, hi, lo);
+    }
+}
 
 // The sum of the two terms that split2 leaves.
 template <typename T>
@@ -88,6 +168,16 @@ __device__ __forceinline__ float2 in_two(float x, float y)
     split2<T>(x, y, hi, lo);
     const float2 h = widen2<T>(hi), l = widen2<T>(lo);
     return make_float2(h.x + l.x, h.y + l.y);
+}
+
+// The same of a row that goes in times its power (fp16).
+template <typename T>
+__device__ __forceinline__ float2 in_two(float x, float y, const Power &p)
+{
+    if constexpr (!kScaled<T>)
+        return in_two<T>(x, y);
+    const float2 r = in_two<T>(x * p.to, y * p.to);
+    return make_float2(r.x * p.from, r.y * p.from);
 }
 
 // The same in three terms, which hold all of an fp32 value (bf16; fp16's range ends with the second).

@@ -30,6 +30,7 @@ struct PrepShared {
     uint16_t d_hi[4][16][24], d_lo[4][16][24];   // T^ on the diagonal
     float l[4][16][20];                    // L on the diagonal
     float g_hi[64], g_lo[64], beta[64];
+    float most[4];                         // largest q.k of each warp's rows (fp16)
     uint16_t p_hi[BACK ? 64 : 1][72], p_lo[BACK ? 64 : 1][72];
 };
 template <int KD, bool BACK>
@@ -124,6 +125,24 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
         }
     }
 
+    // fp16: P goes in over the power of two of the largest q.k, and without `scale`
+    float most = 0.f;
+    Power power = {1.f, 1.f};
+    if constexpr (kScaled<T>) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p > warp)
+                break;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (16 * p + 8 * y + 2 * (lane % 4) + (e & 1) <= 16 * warp + lane / 4 + (e >> 1) * 8)
+                        most = fmaxf(most, fabsf(qk[2 * p + y][e]));
+        }
+        most = warp_largest(most);
+    }
+
     // a block of 16-bit values [rows][columns] as a right operand: rows are its steps (ldsm_t), or its columns (ldsm)
     const int step_row = (lane & 7) + ((lane / 8) & 1) * 8, step_col = (lane / 16) * 8;
     const int t0 = 16 * warp + lane / 4, two = 2 * (lane % 4);
@@ -158,7 +177,15 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
             }
         }
         ask(v + 1);
+        if (kScaled<T> && lane == 0)
+            sh.most[warp] = most;
         __syncthreads();
+        if constexpr (kScaled<T>) {
+            power = power_of<false>(fmaxf(fmaxf(sh.most[0], sh.most[1]), fmaxf(sh.most[2], sh.most[3])));
+            if (tid == 0)
+                a.score[(size_t)slot * a.HV + h * per + v] = a.scale * power.from;
+        }
+        const float by = kScaled<T> ? power.to : a.scale;
         // decays of this lane's rows t0 and t0 + 8 times k k^T and q k^T: P goes to the cell as it lies (a result's rows
         // are a right operand's columns), L to shared memory
         const float hi0 = sh.g_hi[t0], lo0 = sh.g_lo[t0], hi1 = sh.g_hi[t0 + 8], lo1 = sh.g_lo[t0 + 8];
@@ -175,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
                     const float hj = sh.g_hi[j], lj = sh.g_lo[j];
                     const float d0 = j <= t0 ? exp2_fast((hi0 - hj) + (lo0 - lj)) : 0.f;
                     const float d1 = j <= t0 + 8 ? exp2_fast((hi1 - hj) + (lo1 - lj)) : 0.f;
-                    s[y][e] = j <= t0 ? a.scale * (d0 * qk[2 * p + y][e]) : 0.f;
-                    s[y][2 + e] = j <= t0 + 8 ? a.scale * (d1 * qk[2 * p + y][2 + e]) : 0.f;
+                    s[y][e] = j <= t0 ? by * (d0 * qk[2 * p + y][e]) : 0.f;
+                    s[y][2 + e] = j <= t0 + 8 ? by * (d1 * qk[2 * p + y][2 + e]) : 0.f;
                     l[y][e] = j < t0 ? d0 * kk[2 * p + y][e] : 0.f;
                     l[y][2 + e] = j < t0 + 8 ? d1 * kk[2 * p + y][2 + e] : 0.f;
                 }
