@@ -95,7 +95,8 @@ size_t place_bwd(DeltaArgs &a, int dtype, char *base)
     place(a.eh, base, at, heads * a.K);
     place(a.fh, base, at, heads * a.K);
     place(a.dG, base, at, heads);
-    place(a.hd, base, at, (size_t)a.N * a.HV * a.K);
+    place(a.kept, base, at, (size_t)a.slots * a.HV * a.K * a.V);
+    place(a.hd, base, at, (size_t)a.slots * a.HV * a.K);
     return at;
 }
 
@@ -221,8 +222,6 @@ extern "C" int gla_delta_bwd(const void *q, const void *k, const void *v, const 
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0; a.scale = scale;
     a.status = static_cast<int *>(status);
     place_bwd(a, dtype, static_cast<char *>(workspace));
-    if (!dht)
-        a.hd = nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (delta_chunked(dtype, K, V)) {
         const bool half = delta_half(dtype);

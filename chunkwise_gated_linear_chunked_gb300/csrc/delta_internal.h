@@ -38,7 +38,8 @@ struct DeltaArgs {
     float *upd, *dx;                   // [rows, HV, V]: update rows of the state, and their gradients over beta
     float *dqh, *eh, *fh;              // [rows, HV, K]: gradients of q, and of k by way of k S and of k^T n
     float *dG;                         // [rows, HV]: gradient of the running sum of gates
-    float *hd;                         // [N, HV, K]: rows of <ht, dht>
+    float *kept;                       // [slots, HV, K, V]: states at the chunks' ends
+    float *hd;                         // [slots, HV, K]: rows of their products with their gradients
     // workspace of the chunked kernels
     char *chunk;                       // cells (DeltaCell, or DeltaCellBack)
     float *score;                      // fp16: [cell] factor of P, which is stored with its largest q.k in [1, 2)

@@ -7,7 +7,13 @@
 //
 //     dS_t += scale q_t^T do_t,   x_t = k_t dS_t,   dS_{t-1} = a (dS_t - b k_t^T x_t)
 //     dv = b x,   dq = scale S do,   e = -S~ x,   f = dS n,   dk = b e + f,   dbeta = x.v + k.e
-//     dg_t = sum over i >= t of (q.dq - dv.v)_i + <ht, dht>
+//     dg_t = sum over i >= t of (q.dq - dv.v)_i + <S, dS> at the sum's end
+//
+// The terms of a gate's sum cancel but for what a few tokens have of one another, so that it starts again at the end of every
+// 64 tokens, from a state that the rows' pass forward keeps for the one backward.  Heads of 64 x 64 in fp32 are off by at most
+// 1.6e-6 of dg whatever the length, where sums to the sequence's end, in 64 bits but with all later tokens' roundings in their
+// terms, left 1.4e-5 at 16384 tokens (2.5e-5 in the first 256), for K V / 64 floats of workspace a token and head and the same
+// time (4 x 2048 tokens, 8 heads of 128 x 128: 3.71 ms of fp32, 3.75 before).
 //
 // The columns of S and dS do not meet in n and x (delta_cols), nor their rows in dq, e and f (delta_rows), so each CTA
 // walks all tokens for 8 columns (rows) of one head with its part of the state in registers: 16 lanes hold a column,
@@ -357,9 +363,10 @@ __global__ void __launch_bounds__(kThreads) delta_cols_kernel(DeltaArgs a, int t
         put<P>(s, end + state, a.V, a.K, lane);
 }
 
-// Rows of the state, with n and x known.  Forward: dq and e; backward: f.
+// Rows of the state, with n and x known.  Forward: dq and e; backward: f.  Four CTAs an SM, with 16 bytes of spills: left to
+// itself the compiler takes 139 and 168 registers and orders the loads so that bf16 rows of 96 take 858 us (709).
 template <typename Tx, int P, bool BACK>
-__global__ void __launch_bounds__(kThreads) delta_rows_kernel(DeltaArgs a, int tiles)
+__global__ void __launch_bounds__(kThreads, 4) delta_rows_kernel(DeltaArgs a, int tiles)
 {
     constexpr int kBlock = 1024 / P, kEach = kBlock * P / kThreads, kVals = (kBlock * kTile + kThreads - 1) / kThreads;
     __shared__ __align__(16) float ns[2][kBlock][P], xs[2][kBlock][P], ds[2][kBlock][P];
@@ -378,12 +385,19 @@ __global__ void __launch_bounds__(kThreads) delta_rows_kernel(DeltaArgs a, int t
 
     float nr[kEach], xr[kEach], dr[kEach], kr[kVals], qr[kVals];
     float2 abr;
-    auto row_of = [&](int t) { return w.bos + (BACK ? w.len - 1 - t : t); };
+    // backward, blocks begin behind the end, so that chunks end between blocks there too
+    static_assert(kDeltaChunk % kBlock == 0, "chunks are whole blocks");
+    const int pad = BACK ? (kBlock - w.len % kBlock) % kBlock : 0, all = w.len + pad;
+    auto row_of = [&](int t) { return w.bos + (BACK ? all - 1 - t : t); };
+    auto there = [&](int t) { return t >= pad && t < all; };
+    // this row of the state at the end of the chunk with token e
+    const size_t first = (size_t)delta_first_slot(a, w.n) * a.HV + w.hv;
+    auto kept_at = [&](int e) { return (first + (size_t)(e / kDeltaChunk) * a.HV) * a.K + row; };
     auto fetch = [&](int block) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int e = i * kThreads + tid, j = e / P, c = e % P, t = block * kBlock + j;
-            const bool on = t < w.len && c < a.V;
+            const bool on = there(t) && c < a.V;
             const size_t at = on ? ((size_t)row_of(t) * a.HV + w.hv) * a.V + c : 0;
             nr[i] = on ? a.upd[at] : 0.f;
             xr[i] = on ? a.dx[at] : 0.f;
@@ -392,13 +406,13 @@ __global__ void __launch_bounds__(kThreads) delta_rows_kernel(DeltaArgs a, int t
 #pragma unroll
         for (int i = 0; i < kVals; ++i) {
             const int e = i * kThreads + tid, j = e / kTile, r = w.tile * kTile + e % kTile, t = block * kBlock + j;
-            const bool on = j < kBlock && t < w.len && r < a.K;
+            const bool on = j < kBlock && there(t) && r < a.K;
             const size_t at = on ? ((size_t)row_of(t) * a.H + hk) * a.K + r : 0;
             kr[i] = on ? widen(k[at]) : 0.f;
             qr[i] = on ? widen(q[at]) : 0.f;
         }
         abr = make_float2(0.f, 0.f);
-        if (tid < kBlock && block * kBlock + tid < w.len) {
+        if (tid < kBlock && there(block * kBlock + tid)) {
             const size_t at = (size_t)row_of(block * kBlock + tid) * a.HV + w.hv;
             abr = make_float2(a.g[at], a.beta[at]);
         }
@@ -422,64 +436,72 @@ __global__ void __launch_bounds__(kThreads) delta_rows_kernel(DeltaArgs a, int t
         if (tid < kBlock)
             ab[b][tid] = make_float2(expf(abr.x), abr.y);
     };
-    const int blocks = (w.len + kBlock - 1) / kBlock;
+    const int blocks = (all + kBlock - 1) / kBlock;
     if (blocks) {
         fetch(0);
         keep(0);
     }
     __syncthreads();
-    for (int block = 0; block < blocks; ++block) {
-        const int b = block & 1;
-        if (block + 1 < blocks)
-            fetch(block + 1);
-        const int many = min(kBlock, w.len - block * kBlock);
-        for (int t0 = 0; t0 < many; t0 += 4) {   // four tokens' sums over the lanes together
-            float part[BACK ? 4 : 8] = {};
+    constexpr int kPer = kDeltaChunk / kBlock;   // blocks of a chunk
+    for (int block = 0, end; block < blocks; block = end) {
+        end = min(blocks, BACK ? block + (blocks - block - 1) % kPer + 1 : block + kPer);
+        if constexpr (BACK) {   // this row of <S, dS> at a chunk's end
+            const size_t at = kept_at(all - 1 - block * kBlock);
+            float4 kept[kHeld<P>];
+            take<P>(kept, a.kept + at * a.V, 1, a.V, lane, row < a.K);
+            float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 c = ab[b][t0 + j];
-                const float kj = ks[b][t0 + j][mine], qj = qs[b][t0 + j][mine];
+            for (int i = 0; i < kHeld<P>; ++i)
+                sum += (s[i].x * kept[i].x + s[i].y * kept[i].y) + (s[i].z * kept[i].z + s[i].w * kept[i].w);
+            sum = group_sum(sum);
+            if (lane == 0 && row < a.K)
+                a.hd[at] = sum;
+        }
+        const size_t ends = kept_at(block * kBlock) * a.V;
+        for (; block < end; ++block) {
+            const int b = block & 1;
+            if (block + 1 < blocks)
+                fetch(block + 1);
+            const int many = min(kBlock, all - block * kBlock);
+            for (int t0 = 0; t0 < many; t0 += 4) {   // four tokens' sums over the lanes together
+                float part[BACK ? 4 : 8] = {};
 #pragma unroll
-                for (int i = 0; i < kHeld<P>; ++i) {
-                    const float4 n = *reinterpret_cast<const float4 *>(&ns[b][t0 + j][held_at(i, lane)]);
-                    const float4 x = *reinterpret_cast<const float4 *>(&xs[b][t0 + j][held_at(i, lane)]);
-                    const float4 d = *reinterpret_cast<const float4 *>(&ds[b][t0 + j][held_at(i, lane)]);
-                    if constexpr (!BACK) {
-                        s[i] = times(s[i], c.x);
-                        part[j] = dot4(s[i], x, part[j]);
-                        s[i] = add4(s[i], n, kj);
-                        part[4 + j] = dot4(s[i], d, part[4 + j]);
-                    } else {
-                        s[i] = add4(s[i], d, qj);
-                        part[j] = dot4(s[i], n, part[j]);
-                        s[i] = times(add4(s[i], x, -c.y * kj), c.x);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 c = ab[b][t0 + j];
+                    const float kj = ks[b][t0 + j][mine], qj = qs[b][t0 + j][mine];
+#pragma unroll
+                    for (int i = 0; i < kHeld<P>; ++i) {
+                        const float4 n = *reinterpret_cast<const float4 *>(&ns[b][t0 + j][held_at(i, lane)]);
+                        const float4 x = *reinterpret_cast<const float4 *>(&xs[b][t0 + j][held_at(i, lane)]);
+                        const float4 d = *reinterpret_cast<const float4 *>(&ds[b][t0 + j][held_at(i, lane)]);
+                        if constexpr (!BACK) {
+                            s[i] = times(s[i], c.x);
+                            part[j] = dot4(s[i], x, part[j]);
+                            s[i] = add4(s[i], n, kj);
+                            part[4 + j] = dot4(s[i], d, part[4 + j]);
+                        } else {
+                            s[i] = add4(s[i], d, qj);
+                            part[j] = dot4(s[i], n, part[j]);
+                            s[i] = times(add4(s[i], x, -c.y * kj), c.x);
+                        }
                     }
                 }
+                const float sum = sums_by_lane<BACK ? 4 : 8>(part, lane);
+                const int token = BACK ? lane / 4 : lane / 2 % 4;
+                if (row < a.K && t0 + token < many && block * kBlock + t0 + token >= pad && lane % (BACK ? 4 : 2) == 0) {
+                    const size_t at = ((size_t)row_of(block * kBlock + t0 + token) * a.HV + w.hv) * a.K + row;
+                    if constexpr (!BACK)
+                        (lane < 8 ? a.eh : a.dqh)[at] = lane < 8 ? -sum : sum;
+                    else
+                        a.fh[at] = sum;
+                }
             }
-            const float sum = sums_by_lane<BACK ? 4 : 8>(part, lane);
-            const int token = BACK ? lane / 4 : lane / 2 % 4;
-            if (row < a.K && t0 + token < many && lane % (BACK ? 4 : 2) == 0) {
-                const size_t at = ((size_t)row_of(block * kBlock + t0 + token) * a.HV + w.hv) * a.K + row;
-                if constexpr (!BACK)
-                    (lane < 8 ? a.eh : a.dqh)[at] = lane < 8 ? -sum : sum;
-                else
-                    a.fh[at] = sum;
-            }
+            if (block + 1 < blocks)
+                keep(b ^ 1);
+            __syncthreads();
         }
-        if (block + 1 < blocks)
-            keep(b ^ 1);
-        __syncthreads();
-    }
-    if (!BACK && a.hd) {   // this row of <ht, dht>
-        float4 t[kHeld<P>];
-        take<P>(t, a.dht + state, 1, a.V, lane, row < a.K);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kHeld<P>; ++i)
-            sum += (s[i].x * t[i].x + s[i].y * t[i].y) + (s[i].z * t[i].z + s[i].w * t[i].w);
-        sum = group_sum(sum);
-        if (lane == 0 && row < a.K)
-            a.hd[w.head * a.K + row] = sum;
+        if (!BACK && row < a.K)   // rows behind the sequence's end have changed nothing
+            put<P>(s, a.kept + ends, 1, a.V, lane);
     }
 }
 
@@ -528,41 +550,30 @@ __global__ void __launch_bounds__(kThreads) delta_join_kernel(DeltaArgs a)
     }
 }
 
-// dg: sums of dG from the end of each sequence, held in 64 bits as they run over all its tokens.
-__global__ void __launch_bounds__(256) delta_gates_kernel(DeltaArgs a)
+// dg: sums of dG from the end of each chunk, and <S, dS> there; a thread a token.
+__global__ void __launch_bounds__(kDeltaChunk) delta_gates_kernel(DeltaArgs a)
 {
-    __shared__ double part[8];
-    const size_t head = blockIdx.x;
-    const int n = (int)(head / a.HV), hv = (int)(head - (size_t)n * a.HV), tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    int bos, len;
-    if (!delta_sequence(a, n, bos, len))
+    __shared__ double part[2], ends[2];
+    const int slot = blockIdx.x / a.HV, hv = blockIdx.x - slot * a.HV, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    int n, c, first, rows;
+    if (!delta_chunk(a, slot, n, c, first, rows))
         return;
-    double carry = 0.;
-    if (a.hd)
-        for (int d = 0; d < a.K; ++d)
-            carry += a.hd[head * a.K + d];
-    for (int base = 0; base < len; base += 256) {
-        const int t = base + tid;   // from the end
-        const size_t at = (size_t)(bos + len - 1 - t) * a.HV + hv;
-        double v = t < len ? (double)a.dG[at] : 0.;
+    const size_t at = (size_t)(first + tid) * a.HV + hv;
+    double sum = tid < rows ? (double)a.dG[at] : 0., end = 0.;
+    for (int d = tid; d < a.K; d += kDeltaChunk)
+        end += a.hd[((size_t)slot * a.HV + hv) * a.K + d];
 #pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const double u = __shfl_up_sync(~0u, v, m);
-            if (lane >= m)
-                v += u;
-        }
-        if (lane == 31)
-            part[warp] = v;
-        __syncthreads();
-        double before = carry;
-        for (int i = 0; i < 8; ++i) {
-            if (i == warp && t < len)
-                a.dg[at] = (float)(before + v);
-            before += part[i];
-        }
-        carry = before;
-        __syncthreads();
+    for (int m = 1; m < 32; m *= 2) {
+        const double u = __shfl_down_sync(~0u, sum, m);
+        if (lane + m < 32)
+            sum += u;
+        end += __shfl_xor_sync(~0u, end, m);
     }
+    if (lane == 0)
+        part[warp] = sum, ends[warp] = end;
+    __syncthreads();
+    if (tid < rows)
+        a.dg[at] = (float)(sum + (warp == 0 ? part[1] : 0.) + (ends[0] + ends[1]));
 }
 
 }  // namespace
@@ -621,7 +632,7 @@ cudaError_t launch_delta_join(const DeltaArgs &a, int dtype, cudaStream_t s)
 
 cudaError_t launch_delta_gates(const DeltaArgs &a, cudaStream_t s)
 {
-    delta_gates_kernel<<<(unsigned)((size_t)a.N * a.HV), 256, 0, s>>>(a);
+    delta_gates_kernel<<<(unsigned)((size_t)a.slots * a.HV), kDeltaChunk, 0, s>>>(a);
     return cudaGetLastError();
 }
 
