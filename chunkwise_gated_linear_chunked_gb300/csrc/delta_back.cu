@@ -304,8 +304,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             const int c = w.chunks - 1 - turn;
             const bool ok = tc::bar_wait(&sh.full[turn & 1], (turn >> 1) & 1);
             if (__syncthreads_or(!ok)) {
-                if (tid == 0)
-                    report(a.status, GLA_ERR_TIMEOUT);
+                give_up(a.status, &sh.full[turn & 1], (turn >> 1) & 1);
                 return;
             }
             if (tid == kThreads / 2 && c > 0)

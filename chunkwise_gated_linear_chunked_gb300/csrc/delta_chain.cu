@@ -303,8 +303,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
         for (int c = 0; c < w.chunks; ++c) {
             const bool ok = tc::bar_wait(&sh.full[c & 1], (c >> 1) & 1);
             if (__syncthreads_or(!ok)) {
-                if (tid == 0)
-                    report(a.status, GLA_ERR_TIMEOUT);
+                give_up(a.status, &sh.full[c & 1], (c >> 1) & 1);
                 return;
             }
             if (tid == kThreads / 2 && c + 1 < w.chunks)

@@ -292,6 +292,18 @@ __device__ __forceinline__ void bars_init(uint64_t (&full)[2])
     __syncthreads();
 }
 
+// Where a wait for copies ran out, before the CTA ends: the copies under way get as long again, since a CTA's shared memory goes
+// to the next one.  All threads call it; nothing but what this barrier counts is under way.  (Inlined, it costs the forward
+// chain 3 % by the order of the instructions around it.)
+__device__ __noinline__ static void give_up(int *status, uint64_t *bar, uint32_t parity)
+{
+    if (threadIdx.x == 0) {
+        report(status, GLA_ERR_TIMEOUT);
+        tc::bar_wait(bar, parity);
+    }
+    __syncthreads();
+}
+
 // Tensor maps of q, k, v and dO: boxes of 64 rows of one head.
 struct ChainMaps {
     CUtensorMap q, k, v, d;

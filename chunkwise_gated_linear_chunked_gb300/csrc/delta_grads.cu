@@ -148,8 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const __grid_c
         auto &rows = sh.rows[now.items & 1];
         const bool ok = tc::bar_wait(&sh.full[now.turn & 1], (now.turn >> 1) & 1);
         if (__syncthreads_or(!ok)) {
-            if (tid == 0)
-                report(a.status, GLA_ERR_TIMEOUT);
+            give_up(a.status, &sh.full[now.turn & 1], (now.turn >> 1) & 1);
             return;
         }
         const bool more = next_piece(a, ahead);
