@@ -868,11 +868,11 @@ def delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, output_final_sta
 
     q, k: [B, T, H, K]; v: [B, T, HV, V] (cuda, contiguous, all fp32, bf16 or fp16; HV a multiple of H, each key head
     serving HV / H value heads in a row; K, V up to 256); g, beta: fp32 [B, T, HV].  Keys are taken as they are: normalise
-    them before (``norm_fwd`` with a weight of K^-0.5 gives unit length).  scale: K^-0.5 by default.  initial_state: fp32
-    [N, HV, K, V] or None.  cu_seqlens: int32 [N+1] cuda offsets (B == 1); rows outside all sequences keep what the
-    allocator left in them.  out_dtype: q's type (default) or fp32.  Returns (o [B, T, HV, V], final state fp32
-    [N, HV, K, V] or None).  Bad offsets are reported on the device, see ``layer_status`` (or the call's own ``status``,
-    256 zeroed bytes).
+    them before (``norm_fwd`` with a weight of K^-0.5 gives unit length; an eps above 0 leaves keys of zero at zero).
+    scale: K^-0.5 by default.  initial_state: fp32 [N, HV, K, V] or None.  cu_seqlens: int32 [N+1] cuda offsets (B == 1);
+    rows outside all sequences keep what the allocator left in them.  out_dtype: q's type (default) or fp32.  Returns
+    (o [B, T, HV, V], final state fp32 [N, HV, K, V] or None).  Bad offsets, and fp16 states that leave fp16's range, are
+    reported on the device, see ``layer_status`` (or the call's own ``status``, 256 zeroed bytes).
     """
     if status is None and workspace is None and stream is None:
         got = _calls.delta_fwd(q, k, v, g, beta, scale, initial_state, output_final_state, cu_seqlens, out_dtype)
