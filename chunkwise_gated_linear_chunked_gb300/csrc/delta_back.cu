@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 update(u[0], j);
                 rows_largest(u, most);
             }
-            rows_power<true>(most, by);
+            rows_power<kState>(most, by);
 #pragma unroll
             for (int j = 0; j < KD / 8; ++j)
                 times_rows(s[j], s[j], by[0].to, by[1].to);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             }
         }
         if constexpr (kScaled<T>)
-            rows_power<true>(s, in);
+            rows_power<kState>(s, in);
     };
     constexpr bool kChecked = std::is_same_v<T, __half>;
     bool bad = false;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
             for (int i = 0; i < KD / 16; ++i)
                 take(s_in[i], sh.state[group][i][0][lane]);
             if constexpr (kScaled<T>) {
-                const float most = group_power(in_from);
+                const float most = group_largest(in_from);
                 to_group<KD / 16>(s_in, in_from, most);
                 if (on && lane == 0)
                     trace.power[(cell * (a.V / 16) + g16) * 8 + 4] = most;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                     started(r, i);
                     rows_largest(r, most);
                 }
-                rows_power<false>(most, by);
+                rows_power<kOperand>(most, by);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 const float b0 = row[8 * j + two].x, b1 = row[8 * j + two + 1].x;
                 most = fmaxf(most, fmaxf(fmaxf(fabsf(b0 * x.x), fabsf(b1 * x.y)), fmaxf(fabsf(b0 * x.z), fabsf(b1 * x.w))));
             }
-            to_x = power_of<false>(warp_largest(most));
+            to_x = power_of<kTerm>(warp_largest(most));
             if (on && lane == 0)
                 trace.power[(cell * (a.V / 16) + g16) * 8 + 5] = to_x.from;
         }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_back_kernel(const __gr
                 trace.across[at] = sum;
         };
         if constexpr (kScaled<T>)
-            rows_power<true>(s, in);
+            rows_power<kState>(s, in);
         if (on && w.chunks)
             across(w.chunks - 1);
         walk([&](auto &st, int c) {

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 update(u[0], j);
                 rows_largest(u, most);
             }
-            rows_power<true>(most, by);
+            rows_power<kState>(most, by);
             const float f0 = in[0].from * by[0].to, f1 = in[1].from * by[1].to;
 #pragma unroll
             for (int j = 0; j < KD / 8; ++j)
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                     put_blocks<KD / 16>(trace.s + cell * trace.s_size, s_hi, 2 * g16, KD / 8, lane);
             state_by_rows<T, KD, true>(o, s_hi, s_lo, st.q, lane);
             if constexpr (SAVE && kScaled<T>) {
-                const float most = group_power(in);
+                const float most = group_largest(in);
                 to_group<KD / 16>(s_hi, in, most);
                 if (on) {
                     put_blocks<KD / 16>(trace.s + cell * trace.s_size, s_hi, 2 * g16, KD / 8, lane);
@@ -213,7 +213,9 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 n[j][0] = b0 * y.x, n[j][1] = b1 * y.y, n[j][2] = b0 * y.z, n[j][3] = b1 * y.w;
             }
             Power by[2];
-            rows_power<false>(n, by);
+            float largest[2] = {};
+            rows_largest(n, largest);
+            rows_power<kOperand>(largest, by);
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
                 times_rows(n[2 * i], n[2 * i], by[0].to, by[1].to);
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
                 o[j][2] = fmaf(f1, p[j][2], o[j][2]), o[j][3] = fmaf(f1, p[j][3], o[j][3]);
             }
             if constexpr (SAVE) {
-                const float from[2] = {by[0].from, by[1].from}, most = group_power(from);
+                const float from[2] = {by[0].from, by[1].from}, most = power_of<kTerm>(group_largest(largest)).from;
                 to_group<4>(hi, from, most);
                 if (on && lane == 0)
                     trace.power[(cell * (a.V / 16) + g16) * 8 + 1] = most;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
             if constexpr (kScaled<T>) {
                 most = warp_largest(most);
                 if (on && lane == 0)
-                    trace.power[(cell * (a.V / 16) + g16) * 8 + 2] = power_of<false>(most).from;
+                    trace.power[(cell * (a.V / 16) + g16) * 8 + 2] = power_of<kTerm>(most).from;
             }
             // over the eight lanes of a row pair: of the 16 sums each lane is left with two, rows of tile lane / 4
             sum_over_columns<16>(sum, lane);
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(64 * VG, 1) delta_chain_kernel(const __grid_co
         float s[KD / 8][4];
         state_io<KD>(s, nullptr, a.h0, state, a.V, col, on, false);
         if constexpr (kScaled<T>) {
-            rows_power<true>(s, in);
+            rows_power<kState>(s, in);
 #pragma unroll
             for (int j = 0; j < KD / 8; ++j)
                 times_rows(s[j], s[j], in[0].to, in[1].to);

@@ -81,7 +81,7 @@ template <typename T, bool UPPER, int TERMS>
 __device__ __forceinline__ void triangle_rows(float (&c)[8][4], const uint4 *m, int lane)
 {
     Power by[2];
-    rows_power<false>(c, by);
+    rows_power<kOperand>(c, by);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         times_rows(c[j], c[j], by[0].to, by[1].to);
@@ -188,8 +188,8 @@ __device__ __forceinline__ void put_blocks(uint32_t *to, const uint32_t (&r)[STE
             to[((block_row + (e & 1)) * across + 2 * i + (e >> 1)) * 32 + lane] = r[i][e];
 }
 
-// The largest of a group's 16 columns' powers, of which each lane has those of its two rows.
-__device__ __forceinline__ float group_power(const float (&p)[2])
+// The largest over a group's 16 columns of values of which each lane has those of its two rows.
+__device__ __forceinline__ float group_largest(const float (&p)[2])
 {
     float most = fmaxf(p[0], p[1]);
 #pragma unroll
@@ -197,7 +197,7 @@ __device__ __forceinline__ float group_power(const float (&p)[2])
         most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
     return most;
 }
-// Rounded values (left operands) of columns divided by their own powers, divided by the group's; in place.
+// Rounded values (left operands) of columns over their own powers p, over one of the group's that is no smaller; in place.
 template <int STEPS>
 __device__ __forceinline__ void to_group(uint32_t (&r)[STEPS][4], const float (&p)[2], float group)
 {

@@ -42,7 +42,7 @@ struct DeltaArgs {
     float *hd;                         // [slots, HV, K]: rows of their products with their gradients
     // workspace of the chunked kernels
     char *chunk;                       // cells (DeltaCell, or DeltaCellBack)
-    float *score;                      // fp16: [cell] factor of P, which is stored with its largest q.k in [1, 2)
+    float *score;                      // fp16: [cell] factor of P, which is stored over a power of two and `scale`
     DeltaTrace trace;
 };
 

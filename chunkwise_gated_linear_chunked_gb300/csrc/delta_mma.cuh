@@ -71,23 +71,32 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 }
 
 // Powers of two for operands of fp16, whose remainders end at 2^-25 whatever the value is: a row of a left operand (a column of
-// the state, of the rows that update it, of their gradients) goes in times `to`, which takes its largest value to [1, 2), and
-// what comes of it is taken times `from`.  Both are exact, so that fp16's operands are within 2^-22 of a row's largest value
-// however small that is.  bf16 has fp32's range: kScaled is false, and nothing of this is compiled.  The price in fp16 (times of
-// operands as they are, where values of 1e-4 leave 1e-2 in the gradients): 4 x 2048 tokens of 8 heads forward 129 us (100),
-// backward 380 (309); packs of 16 and 8 sequences of 16 heads 1074 (971) and 1036 (911).
+// the state, of the rows that update it, of their gradients) goes in times `to`, which brings its largest value up to fp16's
+// upper end, and what comes of it is taken times `from`.  Both are exact, so that operands are within 2^-22 of their own size,
+// however small, down to 2^-37 of the row's largest (of a state 2^-29).  What is large already stays as it is, and costs the
+// small ones beside it nothing.  bf16 has fp32's range: kScaled is false, and nothing of this is compiled.  The price in fp16
+// (times of operands as they are, where values of 1e-4 leave 1e-2 in the gradients): 4 x 2048 tokens of 8 heads forward
+// 131 us (100), backward 379 (309); packs of 16 and 8 sequences of 16 heads 1088 (971) and 1019 (911).
 template <typename T>
 constexpr bool kScaled = std::is_same_v<T, __half>;
 struct Power {
     float to, from;
 };
-// For a largest magnitude.  STATE: of what the next chunk adds to as it is, which is left 2^4 to grow (a chunk's rows add at
-// most 64 times the largest of them and the keys' length), and not divided: a state that leaves fp16's range is reported.
-template <bool STATE>
-__device__ __forceinline__ Power power_of(float largest)
+// Where the largest value goes: [2^at, 2^(at + 1)).  kOperand: values from there to 2^15 stay, larger ones come down to it.
+// kState: to a state a chunk's rows add at most 64 times the largest of them and the keys' length, and it does not come
+// down, so that one which leaves fp16's range is seen.  kTerm: values of one term, whose products are operands again.
+enum { kTerm = 0, kState = 4, kOperand = 12 };
+template <int AT>
+__device__ __forceinline__ Power power_of(float largest)   // from 2^-100 to 2^100
 {
-    const uint32_t at = (__float_as_uint(largest) >> 23) + (STATE ? 4u : 0u), e = min(max(at, 27u), STATE ? 127u : 227u);
-    return {__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};   // 2^-100 to 2^100 (STATE: to 1)
+    const int exponent = (int)(__float_as_uint(largest) >> 23);
+    int e = 254 + AT - exponent;
+    if (AT == kState)
+        e = max(e, 127);
+    if (AT == kOperand)
+        e = max(e, min(127, 254 + 14 - exponent));
+    e = min(max(e, 27), 227);
+    return {__uint_as_float((uint32_t)e << 23), __uint_as_float((uint32_t)(254 - e) << 23)};
 }
 __device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
@@ -101,22 +110,22 @@ __device__ __forceinline__ void rows_largest(const float (&c)[N][4], float (&mos
         most[1] = fmaxf(most[1], fmaxf(fabsf(c[j][2]), fabsf(c[j][3])));
     }
 }
-template <bool STATE>
+template <int AT>
 __device__ __forceinline__ void rows_power(float (&most)[2], Power (&p)[2])
 {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         most[x] = fmaxf(most[x], __shfl_xor_sync(~0u, most[x], 1));
         most[x] = fmaxf(most[x], __shfl_xor_sync(~0u, most[x], 2));
-        p[x] = power_of<STATE>(most[x]);
+        p[x] = power_of<AT>(most[x]);
     }
 }
-template <bool STATE, int N>
+template <int AT, int N>
 __device__ __forceinline__ void rows_power(const float (&c)[N][4], Power (&p)[2])
 {
     float most[2] = {};
     rows_largest(c, most);
-    rows_power<STATE>(most, p);
+    rows_power<AT>(most, p);
 }
 __device__ __forceinline__ float warp_largest(float v)
 {

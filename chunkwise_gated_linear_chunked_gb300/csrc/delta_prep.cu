@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? 3 : 4) delta_prep_kernel(Delt
             sh.most[warp] = most;
         __syncthreads();
         if constexpr (kScaled<T>) {
-            power = power_of<false>(fmaxf(fmaxf(sh.most[0], sh.most[1]), fmaxf(sh.most[2], sh.most[3])));
+            power = power_of<kOperand>(fmaxf(fmaxf(sh.most[0], sh.most[1]), fmaxf(sh.most[2], sh.most[3])));
             if (tid == 0)
                 a.score[(size_t)slot * a.HV + h * per + v] = a.scale * power.from;
         }

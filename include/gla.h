@@ -472,10 +472,10 @@ size_t gla_norm_bwd_workspace_size(int64_t rows, int D);
  * 16-bit inputs with K = 64 or 128 and V a multiple of 16 run in chunks of 64 tokens on the tensor cores, with every
  * operand that is not an input in two terms of the inputs' type (bf16: 2^-16 of its size, 2^-18 in the mean square);
  * everything else runs token by token in fp32.  States and sums are fp32.  With fp16 inputs those operands (the state, v
- * less what it stores, update rows) go in over powers of two, one for each column, so that small values keep their bits
- * (2^-21 of a column's largest); the state itself is not brought down, and has fp16's range: a result of the chunked path
- * that is not finite, because a state left it or an input was not finite, is reported as GLA_ERR_RANGE.  The decays of a
- * chunk are formed from differences of the running sum of its gates.
+ * less what it stores, update rows) go in times powers of two, one for each column, so that small values keep their bits
+ * (2^-22 of their size, down to 2^-29 of a column's largest); the state itself does not come down, and has fp16's range: a
+ * result of the chunked path that is not finite, because a state left it or an input was not finite, is reported as
+ * GLA_ERR_RANGE.  The decays of a chunk are formed from differences of the running sum of its gates.
  */
 int gla_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta, void *o, float scale,
                   const float *h0, float *ht, const int32_t *cu_seqlens, int N, int B, int T, int H, int HV, int K, int V,

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import delta_oracle as do
+import test_parity_delta as parity
 from test_parity_delta import B, T32, TB, TH, _built, check_bwd, check_fwd, dev, f64, make   # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +112,54 @@ def test_products_beyond_the_range_of_their_factors(B):   # noqa: F811
     s, x = make(TH, T=64, K=64, V=64, h0=False, seed=105)
     s["v"], x["do"] = s["v"] * 16, x["do"] * 2048
     check_bwd(B, s, x)
+
+
+@pytest.mark.parametrize("K", [64, 128])
+def test_edges_in_fp16(B, K):   # noqa: F811
+    """What the other types are tested with: cleared states and strengths of 0 to 2; and gates above zero."""
+    parity.test_edges_of_gates_and_strengths(B, TH, K)
+    parity.test_gates_above_zero(B, TH)
+
+
+def test_rows_behind_and_repeats_in_fp16(B):   # noqa: F811
+    """NaN behind the last sequence reaches no column's largest value; packs repeat bit for bit, in graphs and on streams."""
+    parity.test_rows_behind_the_last_sequence(B, TH)
+    parity.test_graph_and_other_stream(B, TH)
+    s, x = make(TH, lengths=[3, 0, 64, 65, 1, 130, 200] * 12, H=2, HV=4, K=64, V=64, seed=10)
+    args, kw = [dev(s[n]) for n in NAMES], dict(initial_state=dev(x["h0"]), cu_seqlens=dev(x["cu"]))
+    one, two = B.delta_fwd(*args, **kw), B.delta_fwd(*args, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    one, two = (B.delta_bwd(*args, dev(x["do"]), dht=dev(x["dht"]), **kw) for _ in range(2))
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+def test_scratch_needs_no_zeroing_in_fp16(B):   # noqa: F811
+    s, x = make(TH, lengths=[1, 0, 64, 65, 130, 3], H=2, HV=4, K=64, V=80, seed=106)
+    args, kw = [dev(s[n]) for n in NAMES], dict(initial_state=dev(x["h0"]), cu_seqlens=dev(x["cu"]))
+    sizes = (6, 1, 263, 2, 4, 64, 80)
+    for call, need in ((B.delta_fwd, B.lib().gla_delta_fwd_workspace_size(*sizes, B.GLA_F16_OF16, 1)),
+                       (lambda *a, **kw: B.delta_bwd(*a, dev(x["do"]), **kw), B.lib().gla_delta_bwd_workspace_size(*sizes, B.GLA_F16, 1))):
+        scratch = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        for a, b in zip(call(*args, workspace=scratch, **kw), call(*args, **kw)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [TH, TB], ids=["f16", "bf16"])
+@pytest.mark.parametrize("K", [64, 128])
+def test_a_large_row_among_ordinary_ones(B, K, dtype):   # noqa: F811
+    """A value row, a query and an output's gradient a few thousand times the others': rows that it does not reach (those before
+    it; for the gradients those behind) are as near as without it, relative to their own largest values."""
+    s, x = make(dtype, T=60, K=K, V=64, seed=107)
+    s["v"][0, 40], s["q"][0, 20], x["do"][0, 20] = s["v"][0, 40] * 4096, s["q"][0, 20] * 4096, x["do"][0, 20] * 2048
+    wide = [f64(s[n]) for n in NAMES]
+    o, _ = B.delta_fwd(*(dev(s[n]) for n in NAMES), initial_state=dev(x["h0"]), out_dtype=T32)
+    ro, _ = do.delta_fwd(*wide, K ** -0.5, f64(x["h0"]))
+    rows = [t for t in range(40) if t != 20]
+    rel = do.bound("chunk", K, 64, 60)
+    assert np.abs(f64(o) - ro)[0, rows].max() <= rel * np.abs(ro[0, rows]).max()
+    got = B.delta_bwd(*(dev(s[n]) for n in NAMES), dev(x["do"]), initial_state=dev(x["h0"]), dht=dev(x["dht"]))
+    ref = do.delta_bwd(*wide, f64(x["do"]), K ** -0.5, f64(x["h0"]), f64(x["dht"]))
+    for name, i in (("dv", 2), ("dh0", 5)):
+        y, r = (f64(got[i]), ref[i]) if name == "dh0" else (f64(got[i])[:, 21:40], ref[i][:, 21:40])
+        own = 0 if name == "dh0" else (2.0 ** -11 if dtype == TH else 2.0 ** -8) * np.abs(r)
+        assert (np.abs(y - r) <= 2 * rel * np.abs(r).max() + own).all(), name
