@@ -73,7 +73,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 // Powers of two for operands of fp16, whose remainders end at 2^-25 whatever the value is: a row of a left operand (a column of
 // the state, of the rows that update it, of their gradients) goes in times `to`, which brings its largest value up to fp16's
 // upper end, and what comes of it is taken times `from`.  Both are exact, so that operands are within 2^-22 of their own size,
-// however small, down to 2^-37 of the row's largest (of a state 2^-29).  What is large already stays as it is, and costs the
+// however small, down to 2^-37 of the row's largest (of a state 2^-26).  What is large already stays as it is, and costs the
 // small ones beside it nothing.  bf16 has fp32's range: kScaled is false, and nothing of this is compiled.  The price in fp16
 // (times of operands as they are, where values of 1e-4 leave 1e-2 in the gradients): 4 x 2048 tokens of 8 heads forward
 // 131 us (100), backward 379 (309); packs of 16 and 8 sequences of 16 heads 1088 (971) and 1019 (911).
@@ -83,9 +83,9 @@ struct Power {
     float to, from;
 };
 // Where the largest value goes: [2^at, 2^(at + 1)).  kOperand: values from there to 2^15 stay, larger ones come down to it.
-// kState: to a state a chunk's rows add at most 64 times the largest of them and the keys' length, and it does not come
-// down, so that one which leaves fp16's range is seen.  kTerm: values of one term, whose products are operands again.
-enum { kTerm = 0, kState = 4, kOperand = 12 };
+// kState: to a state a chunk's rows add at most 64 times the largest of them and the keys' length, which may be 250, and it
+// does not come down, so that one which leaves fp16's range is seen.  kTerm: values of one term, whose products are operands again.
+enum { kTerm = 0, kState = 1, kOperand = 12 };
 template <int AT>
 __device__ __forceinline__ Power power_of(float largest)   // from 2^-100 to 2^100
 {

@@ -473,7 +473,7 @@ size_t gla_norm_bwd_workspace_size(int64_t rows, int D);
  * operand that is not an input in two terms of the inputs' type (bf16: 2^-16 of its size, 2^-18 in the mean square);
  * everything else runs token by token in fp32.  States and sums are fp32.  With fp16 inputs those operands (the state, v
  * less what it stores, update rows) go in times powers of two, one for each column, so that small values keep their bits
- * (2^-22 of their size, down to 2^-29 of a column's largest); the state itself does not come down, and has fp16's range: a
+ * (2^-22 of their size, down to 2^-26 of a column's largest); the state itself does not come down, and has fp16's range: a
  * result of the chunked path that is not finite, because a state left it or an input was not finite, is reported as
  * GLA_ERR_RANGE.  The decays of a chunk are formed from differences of the running sum of its gates.
  */

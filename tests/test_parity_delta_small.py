@@ -163,3 +163,14 @@ def test_a_large_row_among_ordinary_ones(B, K, dtype):   # noqa: F811
         y, r = (f64(got[i]), ref[i]) if name == "dh0" else (f64(got[i])[:, 21:40], ref[i][:, 21:40])
         own = 0 if name == "dh0" else (2.0 ** -11 if dtype == TH else 2.0 ** -8) * np.abs(r)
         assert (np.abs(y - r) <= 2 * rel * np.abs(r).max() + own).all(), name
+
+
+def test_long_keys_and_weak_writes(B):   # noqa: F811
+    """Keys of one entry of 100, as long as beta |k|^2 stays below 2: a chunk then adds to its state 6400 times its largest update
+    row, from nothing, and no more than fits."""
+    s, x = make(TH, T=130, K=64, V=64, h0=False, seed=108)
+    s["k"][:] = 0
+    s["k"][0, :, 0, 3] = 100
+    s["beta"][:], s["v"] = 1e-5, s["v"].abs()
+    check_fwd(B, s, x, T32)
+    check_bwd(B, s, x)
