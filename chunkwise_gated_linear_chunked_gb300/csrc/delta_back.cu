@@ -18,6 +18,7 @@
 // state from token to token the sums cancel most: there groups of two leave 8e-6, of eight 1.4e-5.)
 //
 // 3.8 us a chunk of 32 columns (4 x 2048 tokens of 8 heads 123 us), bound by the second warp's 232 products and its outputs.
+// Both roles share one count of registers, 255, and keys of 128 spill 180 to 192 bytes (bf16; the forward's chain 20).
 #include "delta_chain.cuh"
 
 namespace gla {

@@ -16,8 +16,9 @@
 // mean far from zero costs nothing, and the sum of squares loses at most 32 units to the cancellation where that value is an
 // outlier), joins the threads' means and squares by group, and a second kernel joins
 // the slices and writes y (dx); it reads x again, from L2 where the tensor fits.  8 x 4096 positions of 512 channels with
-// SiLU, bf16: 22 us forward, 43 backward, bound by the latency of two (three) kernels of one wave and by the two special
-// functions of a sigmoid (each pass 7 us of them).  Every join has a fixed order, so results do not depend on timing.
+// SiLU, bf16: 29 us forward, 52 backward with inputs in memory (22 and 45 where the last pass left them in L2), bound by the
+// loads under way in kernels of one wave (27 % of the copy rate in the sums), by the latency of two (three) of them and by the
+// two special functions of a sigmoid (each pass 7 us of them).  Every join has a fixed order, so results do not depend on timing.
 #include <algorithm>
 #include <numeric>
 #include <type_traits>
@@ -38,7 +39,8 @@ struct alignas(VEC * sizeof(T)) Vec {
     T v[VEC];
 };
 
-// sigmoid(z); its error is that of ex2 and rcp, about 3 units in the last place.
+// sigmoid(z); its error is that of ex2 and rcp, about 3 units in the last place, and for negative z that of rounding z log2 e,
+// which ex2 turns into 0.4 |z| units (8 at z = -20, 31 at -80) of a value that is small there: |z| sigmoid(z) <= 0.28.
 __device__ __forceinline__ float sigmoid(float z)
 {
     float r;
@@ -857,7 +859,7 @@ int64_t group_norm_token_parts(const GroupNormArgs &a, int dtype)   // rows of C
     return group_norm_token_ctas(a, dtype, true) * (kThreads / L) / a.G;
 }
 
-// Enough slices for two CTAs an SM (8 x 4096 x 512 in bf16, both kernels: 22.4 us; three 25.7, four 30, one 26: a CTA's start
+// Enough slices for two CTAs an SM (8 x 4096 x 512 in bf16 in L2, both kernels: 22.4 us; three 25.7, four 30, one 26: a CTA's start
 // and its joins take about 3 us), as long as each has 16 turns of rows, or as many as there are SMs with four turns.
 GroupNormSplit group_norm_split(const GroupNormArgs &a, int dtype)
 {
