@@ -12,8 +12,8 @@
 // The terms of a gate's sum cancel but for what a few tokens have of one another, so that it starts again at the end of every
 // 64 tokens, from a state that the rows' pass forward keeps for the one backward.  Heads of 64 x 64 in fp32 are off by at most
 // 1.6e-6 of dg whatever the length, where sums to the sequence's end, in 64 bits but with all later tokens' roundings in their
-// terms, left 1.4e-5 at 16384 tokens (2.5e-5 in the first 256), for K V / 64 floats of workspace a token and head and the same
-// time (4 x 2048 tokens, 8 heads of 128 x 128: 3.71 ms of fp32, 3.75 before).
+// terms, left 1.4e-5 at 16384 tokens (2.5e-5 in the first 256), for K V floats of workspace a chunk and head and the same time
+// (4 x 2048 tokens, 8 heads of 128 x 128: 3.71 ms of fp32, 3.75 before).
 //
 // The columns of S and dS do not meet in n and x (delta_cols), nor their rows in dq, e and f (delta_rows), so each CTA
 // walks all tokens for 8 columns (rows) of one head with its part of the state in registers: 16 lanes hold a column,

@@ -533,7 +533,8 @@ int gla_delta_step(const void *q, const void *k, const void *v, const float *g, 
  *   w, b        [C] fp32 or NULL (ones; zeros);   mean, rstd [N, G] fp32, written (the backward needs them)
  *   C a multiple of G;  N >= 0, S >= 1;  eps finite and >= 0;  act GLA_ACT_NONE or GLA_ACT_SILU
  *   workspace   gla_group_norm_workspace_size() bytes (may be NULL where that is 0)
- * A NaN or an infinity makes its group NaN.  y must not overlap x.
+ * A NaN or an infinity makes its group NaN, and so does eps = 0 a group of equal values.  Squares are fp32: values further than
+ * 2^63 from their group's mean leave it (rstd 0).  y must not overlap x.
  */
 int gla_group_norm_fwd(const void *x, const float *w, const float *b, void *y, float *mean, float *rstd, int64_t N,
                        int64_t S, int C, int G, float eps, int act, int dtype, void *workspace, size_t workspace_bytes,
